@@ -178,7 +178,7 @@ def prepare(case, seed):
         st["dB"] = [torch.empty((L, n, R), device="cuda", dtype=torch.float32) for n in N]
     if own:
         import adapter_apply_amd as aa
-        st["ws"] = aa.alloc_linear_workspace(T, K, sum(N), S, R, L)
+        st["ws"] = aa.alloc_linear_workspace(T, K, N, R, L)
     return st
 
 
