@@ -48,6 +48,7 @@ LORA_FLAG_SEGMENTS_READY = 1
 LORA_FLAG_ACTIVE_ONLY = 2
 LORA_FLAG_PARTIAL = 4
 LORA_FLAG_RELAY_GIVE_UP = 8   # test hook: the RELAY path's waits give up at once
+LORA_FLAG_ACCUMULATE = 16     # lora_linear_backward: dA, dB +=
 
 # Every symbol the header declares, with its ctypes signature.
 _vp = C.c_void_p
@@ -89,6 +90,15 @@ SIGNATURES = {
     "moe_lora_apply": (_i32, [_i32, _vp, _i64, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _vp,
                               _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32,
                               _u32, _vp, _sz, _vp]),
+    "lora_linear_workspace_size": (_i32, [_i32, _i32, _vp, _i32, _i32, _i32, C.POINTER(_sz)]),
+    "lora_linear": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
+                           _i32, _i32, _vp, _vp, _vp, _vp, _i32, _u32, _vp, _sz, _vp]),
+    "lora_linear_backward": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp,
+                                    _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                    _i32, _u32, _vp, _sz, _vp]),
+    "lora_grad_workspace_size": (_i32, [_vp, _i32, _i32, C.POINTER(_sz)]),
+    "lora_grad_norm": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "lora_grad_clip": (_i32, [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp]),
 }
 
 _lib = None
@@ -533,3 +543,166 @@ def moe_lora_apply(kind: int, y, x, A: Sequence, B: Sequence, topk_ids, topk_w, 
                                 E, L, R, _ptr(topk_ids), _ptr(topk_w), _ptr(idx), _ptr(slot_rank),
                                 _ptr(scale), _dtype_code(x), flags, _ptr(ws),
                                 ws.numel() * ws.element_size(), _stream(stream)), "moe_lora_apply")
+
+
+# ---------------------------------------------------------------------------
+# the adapter layer beside a frozen projection
+# ---------------------------------------------------------------------------
+
+def lora_linear_workspace_size(T: int, K: int, N: Sequence[int], R: int, L: int) -> int:
+    n = _sz(0)
+    _check(lib().lora_linear_workspace_size(T, K, (_i64 * len(N))(*N), len(N), R, L, C.byref(n)),
+           "lora_linear_workspace_size")
+    return int(n.value)
+
+
+def alloc_linear_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, device="cuda"):
+    """A zero-filled workspace of lora_linear and lora_linear_backward for at
+    most T tokens; N lists the slices' widths."""
+    return _aligned_ws(lora_linear_workspace_size(T, K, N, R, L), device)
+
+
+def _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, S_cols):
+    """Checks shared by the layer and its gradient; S_cols: the [T, sum N]
+    tensor (y or dy)."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _rowmajor(x, "x")
+    _need_dtype(x, (bf16,), "x")
+    T, K = x.shape
+    _same_list(A, "A", 3, bf16)
+    L, R, _ = A[0].shape
+    _same_list(A, "A", 3, bf16, lambda i: (L, R, K))
+    if len(B) != len(A):
+        raise ValueError(f"A holds {len(A)} tensors but B holds {len(B)}")
+    _same_list(B, "B", 3, bf16, lambda i: (L, None, R))
+    n = sum(b.shape[1] for b in B)
+    t, name = S_cols
+    _rowmajor(t, name)
+    _need_dtype(t, (bf16,), name)
+    _need_shape(t, (T, None), name)
+    if t.shape[1] < n:
+        raise ValueError(f"{name} has {t.shape[1]} columns; the slices need {n}")
+    if W is not None:
+        _rowmajor(W, "W")
+        _need_dtype(W, (bf16,), "W")
+        _need_shape(W, (n, K), "W")
+    if buf is not None:
+        _need_dtype(buf, (torch.float32,), "buf")
+        _need_shape(buf, (len(A), T, R), "buf")
+        if not buf.is_contiguous():
+            raise ValueError("buf must be contiguous")
+    _check_meta(idx, slot_rank, scale, T, L)
+    _check_ws(ws)
+    return T, K, L, R, n
+
+
+def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bias=None, buf=None,
+                flags: int = 0, stream=None):
+    """y[:, :sum N] = x W^T + bias + scale (x A^T) B^T per slice, rounded once.
+    x [T, K]; W [sum N, K]; A[s] [L, R, K]; B[s] [L, N_s, R]; bias [sum N] or
+    None; all bf16.  buf [S, T, R] fp32 (optional) receives x A^T."""
+    torch = _torch()
+    T, K, L, R, n = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
+    if bias is not None:
+        _need_vec(bias, n, torch.bfloat16, "bias")
+    _need_device([y, x, W, *A, *B, idx, slot_rank, scale, buf, bias, ws])
+    N = (_i64 * len(B))(*[b.shape[1] for b in B])
+    with torch.cuda.device(x.device):
+        _check(lib().lora_linear(_ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
+                                 W.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B), N, len(A),
+                                 L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf),
+                                 LORA_DT_BF16, flags, _ptr(ws), ws.numel() * ws.element_size(),
+                                 _stream(stream)), "lora_linear")
+
+
+def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
+                         B: Sequence, idx, slot_rank, scale, ws, buf=None, flags: int = 0,
+                         stream=None):
+    """Gradient of lora_linear (W frozen).  dx [T, K] bf16 or None; dA[s]
+    [L, R, K] and dB[s] [L, N_s, R] fp32, or None; dy [T, >= sum N].  W None:
+    dx += the adapters' part.  buf: x A^T as lora_linear left it, or None."""
+    torch = _torch()
+    T, K, L, R, n = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
+    if dx is not None:
+        _rowmajor(dx, "dx")
+        _need_dtype(dx, (torch.bfloat16,), "dx")
+        _need_shape(dx, (T, K), "dx")
+    for g, name, shape in ((dA, "dA", lambda i: (L, R, K)),
+                           (dB, "dB", lambda i: (L, B[i].shape[1], R))):
+        if g is None:
+            continue
+        if len(g) != len(A):
+            raise ValueError(f"A holds {len(A)} tensors but {name} holds {len(g)}")
+        _same_list(g, name, 3, torch.float32, shape)
+    outs = [t for t in (dx, *(dA or ()), *(dB or ())) if t is not None and t.numel()]
+    if len({t.data_ptr() for t in outs}) != len(outs):
+        raise ValueError("dx, dA and dB must be different tensors")
+    _need_device([dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws])
+    N = (_i64 * len(B))(*[b.shape[1] for b in B])
+    with torch.cuda.device(x.device):
+        _check(lib().lora_linear_backward(
+            _ptr(dx), 0 if dx is None else dx.stride(0), None if dA is None else _ptr_array(dA),
+            None if dB is None else _ptr_array(dB), _ptr(dy), dy.stride(0), _ptr(x), x.stride(0),
+            T, K, _ptr(W), 0 if W is None else W.stride(0), _ptr_array(A), _ptr_array(B), N,
+            len(A), L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags,
+            _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "lora_linear_backward")
+
+
+# ---------------------------------------------------------------------------
+# gradient norm and clip per adapter slot
+# ---------------------------------------------------------------------------
+
+def _check_grads(grads, name):
+    torch = _torch()
+    if len(grads) < 1:
+        raise ValueError(f"{name} must hold at least one tensor")
+    dt, L = grads[0].dtype, grads[0].shape[0] if grads[0].dim() else 0
+    _need_dtype(grads[0], (torch.float32, torch.bfloat16), f"{name}[0]")
+    for i, t in enumerate(grads):
+        if t.dtype != dt or t.dim() < 1 or t.shape[0] != L or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous {dt} tensor stacked over {L} slots")
+    return L, [t.numel() // L if L else 0 for t in grads]
+
+
+def lora_grad_workspace_size(m: Sequence[int], L: int) -> int:
+    n = _sz(0)
+    _check(lib().lora_grad_workspace_size((_i64 * len(m))(*m), len(m), L, C.byref(n)),
+           "lora_grad_workspace_size")
+    return int(n.value)
+
+
+def alloc_grad_workspace(grads: Sequence, device=None):
+    """Workspace of lora_grad_norm over these tensors."""
+    L, m = _check_grads(grads, "grads")
+    return _aligned_ws(lora_grad_workspace_size(m, L), device or grads[0].device)
+
+
+def lora_grad_norm(norm, grads: Sequence, ws, stream=None):
+    """norm [L] fp32: each slot's norm over all tensors ([L, ...], fp32 or bf16)."""
+    torch = _torch()
+    L, m = _check_grads(grads, "grads")
+    _need_vec(norm, L, torch.float32, "norm")
+    _check_ws(ws)
+    _need_device([norm, *grads, ws])
+    with torch.cuda.device(norm.device):
+        _check(lib().lora_grad_norm(_ptr(norm), _ptr_array(grads), (_i64 * len(m))(*m), len(m), L,
+                                    _dtype_code(grads[0]), _ptr(ws), ws.numel() * ws.element_size(),
+                                    _stream(stream)), "lora_grad_norm")
+
+
+def lora_grad_clip(out: Sequence, grads: Sequence, norm, max_norm, stream=None):
+    """out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)) per slot; out[i]
+    may be grads[i].  norm, max_norm [L] fp32."""
+    torch = _torch()
+    L, m = _check_grads(grads, "grads")
+    Lo, mo = _check_grads(out, "out")
+    if Lo != L or mo != m or out[0].dtype != grads[0].dtype:
+        raise ValueError("out must match grads in number, sizes and dtype")
+    _need_vec(norm, L, torch.float32, "norm")
+    _need_vec(max_norm, L, torch.float32, "max_norm")
+    _need_device([norm, max_norm, *grads, *out])
+    with torch.cuda.device(norm.device):
+        _check(lib().lora_grad_clip(_ptr_array(out), _ptr_array(grads), (_i64 * len(m))(*m), len(m),
+                                    L, _ptr(norm), _ptr(max_norm), _dtype_code(grads[0]),
+                                    _stream(stream)), "lora_grad_clip")

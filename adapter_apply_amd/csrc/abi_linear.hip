@@ -1,0 +1,317 @@
+// C-ABI entry points of the adapter layer beside a frozen projection and its
+// gradient, and of the per-adapter gradient norm and clip: argument checks (all
+// before any launch), workspace carving and launches.  Declarations and
+// contracts: include/adapter_apply.h.
+#include "checks.hpp"
+#include "linear.hpp"
+
+using namespace aa;
+
+namespace {
+
+inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// Workspace of lora_linear and lora_linear_backward.  Every region grows with
+// each size argument.  The last line and the region below it belong to the
+// one-launch segment build, which needs them zero and leaves them zero.
+struct LinWs {
+    SegLayout seg;
+    size_t order;       // int32 [T]: row order of the tile GEMM
+    size_t hl_u;        // bf16 [S][T][2R]: scale * u, high and low parts
+    size_t hl_v;        // the same of v
+    size_t part;        // fp32 partial sums
+    size_t pad;         // dy with slices of whole 8-element units, when some N_s % 8
+    size_t end;
+    bool padded;
+    int64_t pad_cols;
+};
+
+LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    LinWs w{};
+    w.seg = seg_layout(T, L);
+    size_t o = w.seg.end;
+    const size_t tsr = (size_t)T * S * R;
+    w.order = o; o = align256(o + sizeof(int32_t) * (size_t)T);
+    w.hl_u = o;  o = align256(o + 4 * tsr);
+    w.hl_v = o;  o = align256(o + 4 * tsr);
+    w.part = o;
+    // the shrink's K splits: either one, or within an eighth of its input
+    // bytes (pre_kspl: 8 k T S R <= in_bytes / 8)
+    size_t part = 4 * tsr;
+    const size_t split = (size_t)K * ((size_t)T + (size_t)(T < L ? T : L) * S * R) / 8;
+    if (split > part) part = split;
+    // the gradient's column splits: k tiles S <= 1024 with at least T / 64
+    // tiles, and at most 16, so k T <= min(16 T, T + 65536)
+    size_t kt = (size_t)T + 65536;
+    if (kt > 16 * (size_t)T) kt = 16 * (size_t)T;
+    if (4 * (size_t)S * R * kt > part) part = 4 * (size_t)S * R * kt;
+    // the weight gradients' token splits (none up to 511 tokens)
+    if (T > 256) {
+        size_t wg = (size_t)131072 * R;
+        if (wg > (size_t)kLinWgPartMax) wg = (size_t)kLinWgPartMax;
+        if (4 * wg > part) part = 4 * wg;
+    }
+    o = align256(o + part);
+    w.pad = o;
+    for (int s = 0; s < S; ++s) {
+        w.padded = w.padded || N[s] % 8;
+        w.pad_cols += round8(N[s]);
+    }
+    if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
+    w.end = o + seg_x_bytes(T, L) + 256;
+    return w;
+}
+
+lora_status_t check_layer(int32_t T, int32_t K, int64_t ldx, const int64_t *N, int32_t S, int32_t L,
+                          int32_t R, int64_t ldy, int32_t dtype) {
+    CHECK(check_sizes(T, S, L, R, dtype));
+    if (dtype != LORA_DT_BF16) return LORA_E_DTYPE;
+    CHECK(check_k(K, ldx));
+    int64_t total = 0;
+    CHECK(check_n(N, S, ldy, 0, &total));
+    if (!lin_grid_fits(T, K, N, S)) return LORA_E_SHAPE;
+    return LORA_OK;
+}
+
+SegPtrs lin_seg(void *ws, size_t ws_bytes, const LinWs &w, int32_t T, int32_t L) {
+    SegPtrs seg = seg_ptrs(ws, w.seg);
+    attach_seg_x(seg, ws, ws_bytes, T, L, 0, w.end - seg_x_bytes(T, L) - 256);
+    return seg;
+}
+
+// x A^T by slot-sorted position in the workspace's partial sums; returns the
+// number of K splits.
+lora_status_t sorted_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl, int32_t S,
+                            int32_t L, int32_t R, const int32_t *slot_rank, const SegPtrs &seg, float *part,
+                            int32_t *nsp, hipStream_t st) {
+    *nsp = pre_kspl(T, K, S, R, L, seg.max_tiles_pre, kMaxKcGrp);
+    return launched(launch_pre_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, nullptr, st, GroupMap(), part, nsp));
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status_t lora_linear_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
+                                         int32_t L, size_t *bytes) {
+    if (!bytes || !N) return LORA_E_NULL;
+    int64_t total = 0;
+    CHECK(check_sizes(T, S, L, R, LORA_DT_BF16));
+    if (K < 1) return LORA_E_SHAPE;
+    CHECK(check_n(N, S, INT64_MAX / 8 * 4, 0, &total));
+    if (!lin_grid_fits(T, K, N, S)) return LORA_E_SHAPE;
+    *bytes = lin_ws(T, K, N, S, R, L).end;
+    return LORA_OK;
+}
+
+lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K,
+                          const void *W, int64_t ldw, const void *bias, const void *const *A,
+                          const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
+                          const int32_t *idx, const int32_t *slot_rank, const float *scale, float *buf,
+                          int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
+    CHECK(check_layer(T, K, ldx, N, S, L, R, ldy, dtype));
+    CHECK(check_k(K, ldw));
+    if (T == 0) return LORA_OK;
+    if (!y || !x || !W || !idx || !scale) return LORA_E_NULL;
+    CHECK(check_ptrs(A, S));
+    CHECK(check_ptrs(B, S));
+    if (!al(y, 16) || !al(x, 16) || !al(W, 16) || !al(buf, 16) || !al(bias, 2)) return LORA_E_ALIGN;
+    const LinWs wl = lin_ws(T, K, N, S, R, L);
+    CHECK(check_ws(ws, ws_bytes, wl.end));
+
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char *wp = static_cast<char *>(ws);
+    const Slices sl = make_slices(A, B, N, S, 0);
+    uint16_t *hl = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
+    int32_t *order = nullptr;
+    if (T <= kLinShrinkTokens) {
+        CHECK(launched(launch_lin_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, scale, hl, buf, st)));
+    } else {
+        const SegPtrs seg = lin_seg(ws, ws_bytes, wl, T, L);
+        float *part = reinterpret_cast<float *>(wp + wl.part);
+        order = reinterpret_cast<int32_t *>(wp + wl.order);
+        int32_t nsp = 1;
+        if (!(flags & LORA_FLAG_SEGMENTS_READY))
+            CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
+        CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
+        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl, buf, order, st)));
+    }
+    LinArgs a{};
+    a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
+    a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
+    a.bias = static_cast<const uint16_t *>(bias);
+    a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
+    a.hl = hl; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
+    a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
+    for (int s = 0; s < S; ++s) {
+        a.lora[s] = static_cast<const uint16_t *>(B[s]);
+        a.n[s] = N[s];
+        a.off[s] = sl.off[s];
+    }
+    return launched(launch_lin_gemm(a, false, st));
+}
+
+lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, float *const *dB,
+                                   const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T,
+                                   int32_t K, const void *W, int64_t ldw, const void *const *A,
+                                   const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
+                                   const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                                   const float *buf, int32_t dtype, uint32_t flags, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    CHECK(check_layer(T, K, ldx, N, S, L, R, lddy, dtype));
+    if (dx) CHECK(check_k(K, lddx));
+    if (dx && W) CHECK(check_k(K, ldw));
+    if (!dx && !dA && !dB) return LORA_E_NULL;
+    for (int s = 0; s < S; ++s) {
+        if ((dA && !dA[s]) || (dB && !dB[s])) return LORA_E_NULL;
+        if ((dA && !al(dA[s], 16)) || (dB && !al(dB[s], 16))) return LORA_E_ALIGN;
+    }
+    const LinWs wl = lin_ws(T, K, N, S, R, L);
+    if (!wl.padded && lddy % 8) return LORA_E_ALIGN;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        if (flags & LORA_FLAG_ACCUMULATE) return LORA_OK;
+        for (int s = 0; s < S; ++s) {
+            if (dA) CHECK(launched(launch_fill_zero(dA[s], sizeof(float) * (size_t)L * R * K, st)));
+            if (dB) CHECK(launched(launch_fill_zero(dB[s], sizeof(float) * (size_t)L * R * N[s], st)));
+        }
+        return LORA_OK;
+    }
+    if (!dy || !x || !idx || !scale) return LORA_E_NULL;
+    CHECK(check_ptrs(A, S));
+    CHECK(check_ptrs(B, S));
+    if (!al(dx, 16) || !al(dy, 16) || !al(x, 16) || !al(W, 16) || !al(buf, 16)) return LORA_E_ALIGN;
+    CHECK(check_ws(ws, ws_bytes, wl.end));
+
+    char *wp = static_cast<char *>(ws);
+    const Slices sl = make_slices(A, B, N, S, 0);
+    const SegPtrs seg = lin_seg(ws, ws_bytes, wl, T, L);
+    uint16_t *hl_u = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
+    uint16_t *hl_v = reinterpret_cast<uint16_t *>(wp + wl.hl_v);
+    float *part = reinterpret_cast<float *>(wp + wl.part);
+    int32_t *order = reinterpret_cast<int32_t *>(wp + wl.order);
+    if (!(flags & LORA_FLAG_SEGMENTS_READY))
+        CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
+
+    // dy with whole 8-element units per slice
+    const uint16_t *p = static_cast<const uint16_t *>(dy);
+    int64_t ldp = lddy, poff[kMaxSlices];
+    for (int s = 0; s < S; ++s) poff[s] = sl.off[s];
+    if (wl.padded) {
+        PadMap m{};
+        int64_t c = 0;
+        for (int s = 0; s < S; ++s) {
+            m.src[s] = sl.off[s];
+            m.dst[s] = poff[s] = c;
+            m.n[s] = N[s];
+            c += round8(N[s]);
+        }
+        uint16_t *pad = reinterpret_cast<uint16_t *>(wp + wl.pad);
+        ldp = wl.pad_cols;
+        CHECK(launched(launch_lin_pad(dy, lddy, T, S, m, pad, ldp, st)));
+        p = pad;
+    }
+    if (dB) {
+        if (buf) {
+            CHECK(launched(launch_lin_split(buf, T, S, L, R, idx, slot_rank, scale, seg, hl_u, nullptr, st)));
+        } else {
+            int32_t nsp = 1;
+            CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
+            CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_u, nullptr,
+                                             nullptr, st)));
+        }
+        LinWgArgs a{};
+        a.p = p; a.ldp = ldp; a.hl = hl_u;
+        for (int s = 0; s < S; ++s) {
+            a.out[s] = dB[s];
+            a.m[s] = N[s];
+            a.poff[s] = poff[s];
+        }
+        a.T = T; a.S = S; a.L = L; a.R = R;
+        a.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
+        a.seg = seg; a.part = part;
+        a.nsp = lin_wg_splits(T, L, N, S, R);
+        CHECK(launched(launch_lin_wg(a, false, st)));
+    }
+    if (dx || dA) {
+        const int32_t nsp = lin_du_splits(T, L, N, S, R);
+        CHECK(launched(launch_lin_du(p, ldp, poff, T, sl, S, L, R, slot_rank, seg, part, nsp, st)));
+        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_v, nullptr,
+                                         dx ? order : nullptr, st)));
+    }
+    if (dA) {
+        LinWgArgs a{};
+        a.p = static_cast<const uint16_t *>(x); a.ldp = ldx; a.hl = hl_v;
+        for (int s = 0; s < S; ++s) {
+            a.out[s] = dA[s];
+            a.m[s] = K;
+        }
+        a.T = T; a.S = S; a.L = L; a.R = R;
+        a.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
+        a.seg = seg; a.part = part;
+        a.nsp = lin_wg_splits(T, L, a.m, S, R);
+        CHECK(launched(launch_lin_wg(a, true, st)));
+    }
+    if (dx) {
+        LinArgs a{};
+        a.p = p; a.ldp = ldp;
+        a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
+        a.out = static_cast<uint16_t *>(dx); a.ldo = lddx;
+        a.hl = hl_v; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
+        a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
+        a.accumulate = W == nullptr;
+        for (int s = 0; s < S; ++s) {
+            a.lora[s] = static_cast<const uint16_t *>(A[s]);
+            a.n[s] = N[s];
+            a.off[s] = sl.off[s];
+            a.poff[s] = poff[s];
+        }
+        CHECK(launched(launch_lin_gemm(a, true, st)));
+    }
+    return LORA_OK;
+}
+
+static lora_status_t check_grads(const void *const *g, const int64_t *m, int32_t n, int32_t L, int32_t dtype) {
+    if (dtype != LORA_DT_F32 && dtype != LORA_DT_BF16) return LORA_E_DTYPE;
+    if (n < 0 || L < 1 || L > LORA_MAX_SLOTS) return LORA_E_SHAPE;
+    if (n > 0 && (!g || !m)) return LORA_E_NULL;
+    if (grad_items(m, n, L) < 0) return LORA_E_SHAPE;
+    for (int32_t i = 0; i < n; ++i) {
+        if (m[i] == 0) continue;
+        if (!g[i]) return LORA_E_NULL;
+        if (!al(g[i], dtype == LORA_DT_BF16 ? 2 : 4)) return LORA_E_ALIGN;
+    }
+    return LORA_OK;
+}
+
+lora_status_t lora_grad_workspace_size(const int64_t *m, int32_t n, int32_t L, size_t *bytes) {
+    if (!bytes || (n > 0 && !m)) return LORA_E_NULL;
+    if (n < 0 || L < 1 || L > LORA_MAX_SLOTS) return LORA_E_SHAPE;
+    const int64_t items = grad_items(m, n, L);
+    if (items < 0) return LORA_E_SHAPE;
+    *bytes = align256(sizeof(double) * (size_t)(items > 0 ? items : 1));
+    return LORA_OK;
+}
+
+lora_status_t lora_grad_norm(float *norm, const void *const *g, const int64_t *m, int32_t n, int32_t L,
+                             int32_t dtype, void *ws, size_t ws_bytes, void *stream) {
+    CHECK(check_grads(g, m, n, L, dtype));
+    if (!norm) return LORA_E_NULL;
+    if (!al(norm, 4)) return LORA_E_ALIGN;
+    size_t need = 0;
+    CHECK(lora_grad_workspace_size(m, n, L, &need));
+    CHECK(check_ws(ws, ws_bytes, need));
+    return launched(launch_grad_norm(g, m, n, L, dtype, static_cast<double *>(ws), norm,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+lora_status_t lora_grad_clip(void *const *out, const void *const *g, const int64_t *m, int32_t n, int32_t L,
+                             const float *norm, const float *max_norm, int32_t dtype, void *stream) {
+    CHECK(check_grads(g, m, n, L, dtype));
+    CHECK(check_grads(const_cast<const void *const *>(out), m, n, L, dtype));
+    if (!norm || !max_norm) return LORA_E_NULL;
+    if (!al(norm, 4) || !al(max_norm, 4)) return LORA_E_ALIGN;
+    return launched(launch_grad_clip(out, g, m, n, L, norm, max_norm, dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,600 @@
+// The adapter layer beside a frozen projection:
+//   forward   y[t][n]  = sum_k x[t][k] W[n][k] + bias[n] + sum_j (scale u[t][j]) B[i][n][j]
+//   gradient  dx[t][k] = sum_n dy[t][n] W[n][k] + sum_s sum_j v_s[t][j] A_s[i][j][k]
+// with i = idx[t].  Both are one tile GEMM (k_lin_tile) whose contraction runs
+// over the projection's K (or N) and then over the rank vectors of every slot
+// that the tile's tokens name, as further K tiles of the same pipeline: the
+// delta costs no pass over y and is rounded together with the base product.
+//
+// A rank vector (fp32) enters the MFMA as two bf16 parts side by side,
+// [high | low] against lora rows repeated, so that the product keeps the
+// fp32 buffer's precision (split_bf16).
+#include "linear.hpp"
+
+namespace aa {
+
+namespace {
+
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_cast(bf16x8_t, u); }
+
+// Tile GEMM.  Work-group = BM tokens x BN output columns, WM x WN waves.  A
+// K tile is 64 contraction steps: P (token rows, 128 bytes each) and Q (weight
+// rows), DMA'd into one of NST LDS stages, NST - 1 tiles ahead.
+//
+// LDS layout: 16-byte units of a 128-byte row are XOR-ed with (row / 2) % 8,
+// so the 16 rows a quarter wave reads together hit 16 different bank groups;
+// the DMA's LDS side is linear, so the XOR is applied to the global address.
+// Gradient (NN): Q rows are contraction steps, BN columns wide, and reach the
+// MFMA through transposed reads; the XOR moves 32-byte pairs by the row's low
+// bits, so the 4 rows of one transposed read hit different banks.
+//
+// D = Q . P^T (output columns as MFMA rows), so a lane holds 4 consecutive
+// output columns of one token.
+//
+// Rows of another slot take part in a slot's K tile with a zero rank vector.
+// A 16-token block that holds only the slot's tokens adds straight into its
+// accumulators; a mixed block goes through a temporary and a select, because
+// zero times an infinity or NaN of this slot's lora rows must not reach the
+// other tokens.
+template <int BM, int BN, int WM, int WN, int NST, bool NN>
+__global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
+    constexpr int NW = WM * WN, TH = NW * 64;
+    constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
+    constexpr int PB = BM * 128, QB = BN * 128;
+    constexpr int PI = PB / 1024 / NW, QI = QB / 1024 / NW;
+    constexpr int CPR = NN ? BN / 8 : 8;          // 16-byte units per Q row
+    static_assert(PI >= 1 && QI >= 1 && NW % 2 == 0, "whole DMA instructions per wave");
+    __shared__ __attribute__((aligned(16))) char s_stage[NST][PB + QB];
+    __shared__ int s_tok[BM], s_slot[BM], s_list[BM], s_n;
+    __shared__ unsigned s_bits[32];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = w / WN, wn = w % WN;
+
+    // Work-group i runs on XCD i % 8: each XCD takes a contiguous run of
+    // tiles, ordered so that 8 token tiles share a column tile before the next.
+    int mt, nt;
+    {
+        const int total = a.m_tiles * a.n_tiles;
+        const int xcd = blockIdx.x % kXcds, q = total / kXcds, rem = total % kXcds;
+        int id = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
+        const int gm = 8, band = gm * a.n_tiles;
+        const int g = id / band, r = id - g * band;
+        const int rows = min(gm, a.m_tiles - g * gm);
+        nt = r / rows;
+        mt = g * gm + r - nt * rows;
+    }
+    int sc = 0;                                   // forward: the tile's slice
+    if (!NN)
+        while (sc + 1 < a.S && nt >= a.tile_start[sc + 1]) ++sc;
+    const int m0 = mt * BM;
+    const int64_t c0 = (int64_t)(NN ? nt : nt - a.tile_start[sc]) * BN;   // column inside the slice
+    const int64_t cend = NN ? a.K : a.n[sc];
+
+    if (tid < 32) s_bits[tid] = 0;
+    __syncthreads();
+    if (tid < BM) {
+        const int m = m0 + tid;
+        const int pos = min(m, a.T - 1);
+        const int t = a.order ? a.order[pos] : pos;
+        const int sl = m < a.T ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -2;
+        s_tok[tid] = t;
+        s_slot[tid] = sl;
+        if (sl >= 0) atomicOr(&s_bits[sl >> 5], 1u << (sl & 31));
+    }
+    __syncthreads();
+    if (tid < 64) {
+        // the tile's slots, ascending
+        const unsigned b = tid < 32 ? s_bits[tid] : 0u;
+        int c = __popc(b), inc = c;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (tid == 31) s_n = inc;
+        if (tid < 32) {
+            unsigned bb = b;
+            for (int k = inc - c; bb; ++k) {
+                const int bit = __ffs(bb) - 1;
+                s_list[k] = tid * 32 + bit;
+                bb &= bb - 1;
+            }
+        }
+    }
+    __syncthreads();
+    const int n_slots = __builtin_amdgcn_readfirstlane(s_n);
+    if (a.accumulate && n_slots == 0) return;
+
+    // K tiles: the projection's (per slice in the gradient), then per slot
+    // (and slice) the [high | low] rank vectors.
+    int nk = 0;
+    if (a.w) {
+        if (NN)
+            for (int s = 0; s < a.S; ++s) nk += (int)((a.n[s] + 63) / 64);
+        else
+            nk = (a.K + 63) / 64;
+    }
+    const int lc_per = (2 * a.R + 63) / 64;       // K tiles per rank vector
+    const int per_slot = lc_per * (NN ? a.S : 1);
+    const int nv = nk + n_slots * per_slot;
+
+    // DMA lanes: fixed rows, global units XOR-ed.
+    const int prow0 = w * 8 + (lane >> 3);        // + i * NW * 8
+    const int plc = (lane & 7) ^ ((prow0 >> 1) & 7);
+    const uint16_t *pptr[PI];
+#pragma unroll
+    for (int i = 0; i < PI; ++i)
+        pptr[i] = a.p + (int64_t)s_tok[prow0 + i * NW * 8] * a.ldp + plc * 8;
+    constexpr int RPI = 64 / CPR;                 // Q rows per DMA instruction
+    auto qrow = [&](int i) { return (i * NW + w) * RPI + lane / CPR; };
+    auto qlc = [&](int i) {
+        const int row = qrow(i), pc = lane % CPR;
+        if (!NN) return pc ^ ((row >> 1) & 7);
+        const int f = (row & 3) | (CPR >= 16 ? ((row >> 3) & 1) << 2 : 0);
+        return pc ^ (f << 1);
+    };
+    const uint16_t *qptr[QI];
+    if (a.w) {
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+            if (NN) {
+                const int64_t col = c0 + qlc(i) * 8;
+                qptr[i] = a.w + (int64_t)qrow(i) * a.ldw + (col < cend ? col : 0);
+            } else {
+                const int64_t n = min(c0 + qrow(i), cend - 1);
+                qptr[i] = a.w + (a.off[sc] + n) * a.ldw + qlc(i) * 8;
+            }
+        }
+    }
+    const void *zero = g_zero16;
+
+    int cs = 0;                 // gradient: slice and tile inside it of the next base K tile
+    int64_t ci = 0;
+    auto issue = [&](int v, int stage) {
+        const uint32_t pl = lds_addr(&s_stage[stage][0]) + w * 1024;
+        const uint32_t ql = pl + PB;
+        if (v < nk) {
+            if (NN) {
+                while (ci * 64 >= a.n[cs]) { ++cs; ci = 0; }
+                const int64_t rem = a.n[cs] - ci * 64;
+                const int64_t pc = a.poff[cs] + ci * 64, qr = (a.off[cs] + ci * 64) * a.ldw;
+                // p holds whole 8-element units per slice, zero past N_s
+#pragma unroll
+                for (int i = 0; i < PI; ++i)
+                    dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + pc) : zero);
+#pragma unroll
+                for (int i = 0; i < QI; ++i)
+                    dma16(ql + i * NW * 1024,
+                          qrow(i) < rem ? (const void *)(qptr[i] + qr) : zero);
+                ++ci;
+            } else {
+                const int kb = v * 64, rem = a.K - kb;
+                if (rem >= 64) {
+#pragma unroll
+                    for (int i = 0; i < PI; ++i) dma16(pl + i * NW * 1024, pptr[i] + kb);
+#pragma unroll
+                    for (int i = 0; i < QI; ++i) dma16(ql + i * NW * 1024, qptr[i] + kb);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PI; ++i)
+                        dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + kb) : zero);
+#pragma unroll
+                    for (int i = 0; i < QI; ++i)
+                        dma16(ql + i * NW * 1024, qlc(i) * 8 < rem ? (const void *)(qptr[i] + kb) : zero);
+                }
+            }
+            return;
+        }
+        const int u = v - nk, d = u / per_slot, x = u - d * per_slot;
+        const int s = NN ? x / lc_per : sc, c = x % lc_per;
+        const int slot = __builtin_amdgcn_readfirstlane(s_list[d]);
+        const int R = a.R;
+        const int pj = c * 64 + plc * 8;
+        const uint16_t *hl = a.hl + (int64_t)s * a.T * 2 * R;
+#pragma unroll
+        for (int i = 0; i < PI; ++i) {
+            const int row = prow0 + i * NW * 8;
+            const bool in = s_slot[row] == slot && pj < 2 * R;
+            dma16(pl + i * NW * 1024,
+                  in ? (const void *)(hl + (int64_t)s_tok[row] * 2 * R + pj) : zero);
+        }
+        const uint16_t *lo = a.lora[s];
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+            const void *src = zero;
+            if (NN) {
+                const int j2 = c * 64 + qrow(i);
+                const int64_t col = c0 + qlc(i) * 8;
+                if (j2 < 2 * R)
+                    src = lo + ((int64_t)slot * R + (j2 < R ? j2 : j2 - R)) * a.K + (col < cend ? col : 0);
+            } else {
+                const int j2 = c * 64 + qlc(i) * 8;
+                const int64_t n = min(c0 + qrow(i), cend - 1);
+                if (j2 < 2 * R) src = lo + ((int64_t)slot * cend + n) * R + (j2 < R ? j2 : j2 - R);
+            }
+            dma16(ql + i * NW * 1024, src);
+        }
+    };
+
+    floatx4_t acc[NB][MB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    const int g = lane >> 4, l16 = lane & 15;
+    auto pfrag = [&](const char *st, int mb, int kk) {
+        const int row = (wm * MB + mb) * 16 + l16;
+        return frag(*reinterpret_cast<const uint4 *>(st + row * 128 + (((kk * 4 + g) ^ ((row >> 1) & 7)) << 4)));
+    };
+    auto qfrag = [&](const char *st, int nb, int kk) {
+        if (NN) {
+            const int row = kk * 32 + g * 8 + (l16 >> 2);
+            const int col = (wn * NB + nb) * 16 + (l16 & 3) * 4;
+            const int f = (row & 3) | (CPR >= 16 ? ((row >> 3) & 1) << 2 : 0);
+            const char *p = st + PB + row * (BN * 2) + ((((col >> 3) ^ (f << 1)) << 4) | ((col & 4) << 1));
+            const uint2 x0 = tr_read(p), x1 = tr_read(p + 4 * BN * 2);
+            return frag(make_uint4(x0.x, x0.y, x1.x, x1.y));
+        }
+        const int row = (wn * NB + nb) * 16 + l16;
+        return frag(*reinterpret_cast<const uint4 *>(st + PB + row * 128 + (((kk * 4 + g) ^ ((row >> 1) & 7)) << 4)));
+    };
+
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i)
+        if (i < nv) issue(i, i);
+    int stage = 0;
+    for (int v = 0; v < nv; ++v) {
+        // tile v has landed once at most the NST - 2 tiles after it are in flight
+        if (v + NST - 2 < nv) wait_barrier<(NST - 2) * (PI + QI)>();
+        else wait_barrier<0>();
+        if (v + NST - 1 < nv) {
+            const int ns = stage + NST - 1;
+            issue(v + NST - 1, ns >= NST ? ns - NST : ns);
+        }
+        const char *st = s_stage[stage];
+        if (v < nk) {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                bf16x8_t q[NB], p[MB];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) q[i] = qfrag(st, i, kk);
+#pragma unroll
+                for (int j = 0; j < MB; ++j) p[j] = pfrag(st, j, kk);
+#pragma unroll
+                for (int j = 0; j < MB; ++j)
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p[j], acc[i][j], 0, 0, 0);
+            }
+        } else {
+            const int slot = __builtin_amdgcn_readfirstlane(s_list[(v - nk) / per_slot]);
+            bf16x8_t q[2][NB];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) q[kk][i] = qfrag(st, i, kk);
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+                const int rs = s_slot[(wm * MB + j) * 16 + l16];
+                const bool mine = rs == slot;
+                if (__ballot(mine) == 0) continue;
+                const bf16x8_t p0 = pfrag(st, j, 0), p1 = pfrag(st, j, 1);
+                if (__ballot(!mine && rs != -2) == 0) {
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[0][i], p0, acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[1][i], p1, acc[i][j], 0, 0, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        floatx4_t t = {0.f, 0.f, 0.f, 0.f};
+                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[0][i], p0, t, 0, 0, 0);
+                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[1][i], p1, t, 0, 0, 0);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
+                    }
+                }
+            }
+        }
+        if (++stage == NST) stage = 0;
+    }
+
+    // One rounding per output element; 4 consecutive columns per lane.
+    const int64_t obase = NN ? 0 : a.off[sc];
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+        const int row = (wm * MB + j) * 16 + l16;
+        if (m0 + row >= a.T) continue;
+        if (a.accumulate && s_slot[row] < 0) continue;
+        uint16_t *o = a.out + (int64_t)s_tok[row] * a.ldo + obase;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int64_t c = c0 + (wn * NB + i) * 16 + 4 * g;
+            if (c >= cend) continue;
+            floatx4_t r = acc[i][j];
+            uint2 *dst = reinterpret_cast<uint2 *>(o + c);
+            if (!NN && a.bias) {
+                const uint16_t *b = a.bias + obase + c;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[e] += bf16_to_f32(b[e]);
+            }
+            if (NN && a.accumulate) {
+                const uint2 old = *dst;
+                r[0] += bf16_lo(old.x); r[1] += bf16_hi(old.x);
+                r[2] += bf16_lo(old.y); r[3] += bf16_hi(old.y);
+            }
+            *dst = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+        }
+    }
+}
+
+// Rank vectors of a small batch: u[t][j] = sum_k x[t][k] A[i][j][k] with no
+// segment build.  Work-group = (16 tokens, the y-th different slot among them,
+// 16 ranks of a slice), 8 waves each taking every eighth 64-column step of K
+// straight from global memory into 16x16x32 MFMA fragments; the waves' sums
+// are added in order.  Work-groups of y past the block's slots end at once;
+// y = 0 clears buf for the tokens without a slot.
+constexpr int kShWaves = 8;
+struct LinShrinkArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    int32_t T, K, S, L, R;
+    const uint16_t *a[kMaxSlices];
+    const int32_t *idx, *slot_rank;
+    const float *scale;
+    uint16_t *hl;
+    float *buf;
+};
+
+__global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
+    __shared__ floatx4_t s_sum[kShWaves][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int l16 = lane & 15, g = lane >> 4;
+    const int t0 = blockIdx.x * 16, nrb = (a.R + 15) / 16;
+    const int s = blockIdx.z / nrb, j0 = (blockIdx.z - s * nrb) * 16;
+    const int t = t0 + l16;
+    const int mine = t < a.T ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -2;
+    // lanes 0..15 that name a slot first; the y-th of them is this group's slot
+    bool lead = mine >= 0 && lane < 16;
+    for (int o = 0; o < 15; ++o) {
+        const int other = __shfl(mine, o);
+        if (o < lane && other == mine) lead = false;
+    }
+    unsigned long long leads = __ballot(lead);
+    if (blockIdx.y == 0 && a.buf && tid < 256) {
+        const int tt = tid >> 4, jj = j0 + (tid & 15);
+        const int sl = __shfl(mine, tt);
+        if (sl == -1 && jj < a.R) a.buf[((int64_t)s * a.T + t0 + tt) * a.R + jj] = 0.f;
+    }
+    if ((int)blockIdx.y >= __popcll(leads)) return;
+    for (unsigned y = 0; y < blockIdx.y; ++y) leads &= leads - 1;
+    const int slot = __builtin_amdgcn_readfirstlane(__shfl(mine, __ffsll(leads) - 1));
+    const int r = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+
+    const uint16_t *xr = a.x + (int64_t)min(t, a.T - 1) * a.ldx;
+    const uint16_t *ar = a.a[s] + ((int64_t)slot * a.R + min(j0 + l16, a.R - 1)) * a.K;
+    floatx4_t acc = {0.f, 0.f, 0.f, 0.f};
+    const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int kb = w * 64; kb < a.K; kb += kShWaves * 64) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = kb + h * 32 + g * 8;
+            const bool in = k < a.K;
+            const int kc = in ? k : 0;
+            uint4 xa = ldg<uint4>(xr + kc), aa = ldg<uint4>(ar + kc);
+            if (!in) { xa = z; aa = z; }
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(aa), frag(xa), acc, 0, 0, 0);
+        }
+    }
+    s_sum[w][lane] = acc;
+    __syncthreads();
+    if (w) return;
+    floatx4_t sum = s_sum[0][lane];
+    for (int i = 1; i < kShWaves; ++i) {
+        const floatx4_t o = s_sum[i][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += o[e];
+    }
+    const int j = j0 + 4 * g;
+    if (mine != slot || j >= a.R) return;
+    const float sc = a.scale[slot];
+    const int64_t row = (int64_t)s * a.T + t;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (j + e >= r) sum[e] = 0.f;
+        split_bf16(j + e < r ? sc * sum[e] : 0.f, hi[e], lo[e]);
+    }
+    uint16_t *h = a.hl + row * 2 * a.R + j;
+    *reinterpret_cast<uint2 *>(h) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2 *>(h + a.R) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
+}
+
+// Rank vectors from partial sums (by slot-sorted position) or from a caller's
+// buffer (by token): sums the splits in order, zeroes ranks past the slot's
+// own, scales, splits into [high | low], and clears buf for tokens without a
+// slot.  The first block row also writes the row order of the tile GEMM: the
+// slot-sorted tokens, then the tokens without a slot in token order (their
+// rank among themselves is counted from idx; one pass over the idx before the
+// block).
+constexpr int kRedThreads = 256;
+struct LinReduceArgs {
+    const float *part;
+    const float *in;        // the caller's rank vectors, by token (part null)
+    int32_t nsp, T, S, L, R;
+    const int32_t *idx, *slot_rank;
+    const float *scale;
+    SegPtrs seg;
+    uint16_t *hl;
+    float *buf;
+    int32_t *order;
+};
+
+__global__ __launch_bounds__(kRedThreads) void k_lin_order(LinReduceArgs a) {
+    __shared__ int s_cnt[kRedThreads / 64 + 1];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int base = blockIdx.x * kRedThreads;
+    if (tid <= kRedThreads / 64) s_cnt[tid] = 0;
+    __syncthreads();
+    // tokens without a slot before this block
+    int before = 0;
+    for (int i = tid; i < base; i += kRedThreads)
+        before += slot_of_token(a.idx, a.slot_rank, a.L, i) < 0;
+    for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+    if (lane == 0) atomicAdd(&s_cnt[kRedThreads / 64], before);
+    const int t = base + tid;
+    const bool none = t < a.T && slot_of_token(a.idx, a.slot_rank, a.L, t) < 0;
+    const unsigned long long b = __ballot(none);
+    if (lane == 0) s_cnt[w] = __popcll(b);
+    __syncthreads();
+    int pos = a.seg.header[0] + s_cnt[kRedThreads / 64];
+    for (int i = 0; i < w; ++i) pos += s_cnt[i];
+    pos += __popcll(b & ((1ull << lane) - 1));
+    if (none) a.order[pos] = t;
+    if (t < a.seg.header[0]) a.order[t] = a.seg.perm[t];
+}
+
+__global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
+    const int rq = a.R / 4;                                   // 4 ranks per thread
+    const int64_t q = (int64_t)blockIdx.x * kRedThreads + threadIdx.x;
+    const int s = blockIdx.y;
+    const int64_t i = q / rq;
+    const int j = (int)(q - i * rq) * 4;
+    if (i >= a.T) return;
+    // as a token: buf of tokens without a slot
+    if (a.buf && slot_of_token(a.idx, a.slot_rank, a.L, (int)i) < 0)
+        *reinterpret_cast<floatx4_t *>(a.buf + ((int64_t)s * a.T + i) * a.R + j) = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    // as a slot-sorted position
+    if (i >= a.seg.header[0]) return;
+    const int t = a.seg.perm[i];
+    const int slot = a.idx[t];
+    const int r = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
+    if (a.part) {
+        for (int k = 0; k < a.nsp; ++k) {
+            const floatx4_t o = *reinterpret_cast<const floatx4_t *>(
+                a.part + (((int64_t)s * a.nsp + k) * a.T + i) * a.R + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += o[e];
+        }
+    } else {
+        sum = *reinterpret_cast<const floatx4_t *>(a.in + ((int64_t)s * a.T + t) * a.R + j);
+    }
+    const float sc = a.scale[slot];
+    const int64_t row = (int64_t)s * a.T + t;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (j + e >= r) sum[e] = 0.f;
+        split_bf16(j + e < r ? sc * sum[e] : 0.f, hi[e], lo[e]);
+    }
+    uint16_t *h = a.hl + row * 2 * a.R + j;
+    *reinterpret_cast<uint2 *>(h) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2 *>(h + a.R) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
+}
+
+template <int BM, int BN, int WM, int WN, int NST>
+hipError_t run_tile(LinArgs a, bool gradient, hipStream_t st) {
+    a.m_tiles = (a.T + BM - 1) / BM;
+    if (gradient) {
+        a.n_tiles = (a.K + BN - 1) / BN;
+    } else {
+        int c = 0;
+        for (int s = 0; s < a.S; ++s) {
+            a.tile_start[s] = c;
+            c += (int)((a.n[s] + BN - 1) / BN);
+        }
+        for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
+        a.n_tiles = c;
+    }
+    const dim3 grid((unsigned)(a.m_tiles * a.n_tiles)), block(WM * WN * 64);
+    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false>), grid, block, 0, st, a);
+    return hipGetLastError();
+}
+
+int64_t tiles(int32_t T, int32_t K, const int64_t *N, int32_t S, bool gradient, int b) {
+    int64_t c = 0;
+    if (gradient) c = (K + b - 1) / b;
+    else
+        for (int s = 0; s < S; ++s) c += (N[s] + b - 1) / b;
+    return c * ((T + b - 1) / b);
+}
+
+}  // namespace
+
+// A launch's threads stay under 2^32: tile work-groups of 512 threads, and
+// column tiles times rank blocks of the weight gradients.
+bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
+    for (int s = 0; s < S; ++s)
+        if (N[s] > (1 << 24)) return false;
+    return K <= (1 << 24) && tiles(T, K, N, S, false, 256) <= (1 << 22) &&
+           tiles(T, K, N, S, true, 256) <= (1 << 22);
+}
+
+hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
+    if (tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192) return run_tile<256, 256, 2, 4, 2>(a, gradient, st);
+    if (tiles(a.T, a.K, a.n, a.S, gradient, 128) >= 192) return run_tile<128, 128, 2, 2, 2>(a, gradient, st);
+    return run_tile<64, 64, 2, 2, 4>(a, gradient, st);
+}
+
+hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
+                             int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                             const int32_t *slot_rank, const float *scale, uint16_t *hl, float *buf,
+                             hipStream_t st) {
+    LinShrinkArgs a{};
+    a.x = static_cast<const uint16_t *>(x); a.ldx = ldx; a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
+    for (int s = 0; s < S; ++s) a.a[s] = static_cast<const uint16_t *>(sl.a[s]);
+    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.hl = hl; a.buf = buf;
+    int y = L < 16 ? L : 16;
+    if (y > T) y = T;
+    const dim3 grid((unsigned)((T + 15) / 16), (unsigned)y, (unsigned)(S * ((R + 15) / 16)));
+    hipLaunchKernelGGL(k_lin_shrink, grid, dim3(kShWaves * 64), 0, st, a);
+    return hipGetLastError();
+}
+
+static hipError_t run_reduce(LinReduceArgs a, hipStream_t st) {
+    if (a.order) {
+        hipLaunchKernelGGL(k_lin_order, dim3((unsigned)((a.T + kRedThreads - 1) / kRedThreads)),
+                           dim3(kRedThreads), 0, st, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const int64_t items = (int64_t)a.T * (a.R / 4);
+    const dim3 grid((unsigned)((items + kRedThreads - 1) / kRedThreads), (unsigned)a.S);
+    hipLaunchKernelGGL(k_lin_reduce, grid, dim3(kRedThreads), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
+                             const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                             const SegPtrs &seg, uint16_t *hl, float *buf, int32_t *order,
+                             hipStream_t st) {
+    LinReduceArgs a{};
+    a.part = part; a.nsp = nsp; a.T = T; a.S = S; a.L = L; a.R = R;
+    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg;
+    a.hl = hl; a.buf = buf; a.order = order;
+    return run_reduce(a, st);
+}
+
+hipError_t launch_lin_split(const float *buf, int32_t T, int32_t S, int32_t L, int32_t R,
+                            const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                            const SegPtrs &seg, uint16_t *hl, int32_t *order, hipStream_t st) {
+    LinReduceArgs a{};
+    a.in = buf; a.T = T; a.S = S; a.L = L; a.R = R;
+    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg;
+    a.hl = hl; a.order = order;
+    return run_reduce(a, st);
+}
+
+}  // namespace aa

@@ -1,0 +1,147 @@
+// Argument blocks and launchers of the adapter layer beside a frozen
+// projection: lora_linear and its gradient (linear.hip, linear_bwd.hip), and
+// of the per-adapter gradient norm and clip (grad.hip).
+#pragma once
+
+#include "common.hpp"
+
+namespace aa {
+
+// The tile GEMM (k_lin_tile).  Forward: out[t][n] = sum_k p[t][k] w[n][k] +
+// delta; gradient: out[t][k] = sum_n p[t][n] w[n][k] + delta.
+struct LinArgs {
+    const uint16_t *p;        // x [T][ldp], or dy (whole 8-element units per slice)
+    int64_t ldp;
+    const uint16_t *w;        // the projection [sum N][ldw]; null: no base product
+    int64_t ldw;
+    const uint16_t *bias;     // [sum N] or null (forward)
+    uint16_t *out;
+    int64_t ldo;
+    const uint16_t *hl;       // bf16 [S][T][2R]: scaled rank vectors, high and low parts
+    const int32_t *order;     // row position -> token, or null (identity)
+    const int32_t *idx;
+    const int32_t *slot_rank;
+    int32_t T, K, S, L, R;
+    int32_t accumulate;       // out += delta (no base product); rows without a slot untouched
+    int32_t m_tiles, n_tiles;
+    const uint16_t *lora[kMaxSlices];   // forward: lora_b [L][N_s][R]; gradient: lora_a [L][R][K]
+    int64_t n[kMaxSlices];              // N_s
+    int64_t off[kMaxSlices];            // first row of slice s in w (first column in out)
+    int64_t poff[kMaxSlices];           // gradient: first column of slice s in p
+    int32_t tile_start[kMaxSlices + 1]; // forward: column tiles by slice
+};
+
+hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
+// Whether the sizes stay within what one launch's grid takes.
+bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
+
+// Rank vectors of up to kLinShrinkTokens tokens in one launch, no segments.
+constexpr int kLinShrinkTokens = 256;
+hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
+                             int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                             const int32_t *slot_rank, const float *scale, uint16_t *hl, float *buf,
+                             hipStream_t st);
+// hl (and buf, if given) from partial sums [S][nsp][T][R] by slot-sorted
+// position; `scaled`: hl holds scale * sum.  order (nullable): receives the
+// slot-sorted tokens followed by the tokens without a slot.
+hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
+                             const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                             const SegPtrs &seg, uint16_t *hl, float *buf, int32_t *order,
+                             hipStream_t st);
+// hl from a caller's fp32 rank vectors [S][T][R]; order as above.
+hipError_t launch_lin_split(const float *buf, int32_t T, int32_t S, int32_t L, int32_t R,
+                            const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                            const SegPtrs &seg, uint16_t *hl, int32_t *order, hipStream_t st);
+
+// Gradient side (linear_bwd.hip).
+struct PadMap {
+    int64_t src[kMaxSlices];   // first column of slice s in dy
+    int64_t dst[kMaxSlices];   // first column in the padded copy
+    int64_t n[kMaxSlices];     // N_s
+};
+hipError_t launch_lin_pad(const void *dy, int64_t lddy, int32_t T, int32_t S, const PadMap &m,
+                          uint16_t *out, int64_t ldo, hipStream_t st);
+// Partial sums [S][nsp][T][R] of dy . lora_b by slot-sorted position.
+int32_t lin_du_splits(int32_t T, int32_t L, const int64_t *N, int32_t S, int32_t R);
+hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, int32_t T,
+                         const Slices &sl, int32_t S, int32_t L, int32_t R, const int32_t *slot_rank,
+                         const SegPtrs &seg, float *part, int32_t nsp, hipStream_t st);
+// One weight gradient family: out_s[slot][..] = sum over the slot's tokens of
+// rows p (M_s columns at poff[s]) times rank vectors hl.  transposed: out is
+// [L][R][M] (lora_a), else [L][M_s][R] (lora_b).
+struct LinWgArgs {
+    const uint16_t *p;
+    int64_t ldp;
+    const uint16_t *hl;
+    float *out[kMaxSlices];
+    int64_t m[kMaxSlices];
+    int64_t poff[kMaxSlices];
+    int32_t T, S, L, R;
+    int32_t accumulate;
+    SegPtrs seg;
+    float *part;               // fp32 partial sums of the token splits
+    int32_t nsp;
+    int32_t tile_start[kMaxSlices + 1];
+    int64_t part_off[kMaxSlices];   // element offset of slice s inside one split
+    int64_t part_stride;            // elements of one split
+};
+// Partial sums of the token splits stay within this many elements.
+constexpr int64_t kLinWgPartMax = 16 << 20;
+int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *M, int32_t S, int32_t R);
+hipError_t launch_lin_wg(LinWgArgs a, bool transposed, hipStream_t st);
+
+// Gradient norm and clip (grad.hip).
+hipError_t launch_grad_norm(const void *const *g, const int64_t *m, int32_t n, int32_t L, int32_t dtype,
+                            double *part, float *norm, hipStream_t st);
+hipError_t launch_grad_clip(void *const *out, const void *const *g, const int64_t *m, int32_t n,
+                            int32_t L, const float *norm, const float *max_norm, int32_t dtype,
+                            hipStream_t st);
+int64_t grad_items(const int64_t *m, int32_t n, int32_t L);   // partial sums of the norm, or -1
+
+#ifdef __HIPCC__
+// 16 zero bytes that masked LDS-DMA lanes read instead of their row.
+static __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
+
+// 64 lanes x 16 bytes straight from global memory into LDS at `lds` (uniform)
+// + lane * 16.  The load is counted in vmcnt; every reader waits for it with
+// wait_barrier.
+__device__ __forceinline__ void dma16(uint32_t lds, const void *src) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(lds), "v"(src) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+}
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+// Address of an LDS byte as the 32-bit LDS offset DMA and transposed reads use.
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+// Transposed read of a 4-row x 16-column block of 16-bit values per 16 lanes:
+// lane i of the group supplies row i / 4, columns 4 (i % 4)..+3 and receives
+// column i, rows 0..3.
+__device__ __forceinline__ uint2 tr_read(const char *p) {
+    typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+    const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    return __builtin_bit_cast(uint2, v);
+}
+// A token's slot: idx outside [0, L) and slots of rank <= 0 carry no delta.
+__device__ __forceinline__ int slot_of_token(const int32_t *idx, const int32_t *slot_rank, int L, int t) {
+    const int s = idx[t];
+    if (s < 0 || s >= L) return -1;
+    return slot_rank && slot_rank[s] <= 0 ? -1 : s;
+}
+// fp32 as a sum of two bf16 values: the high part rounded to nearest, the low
+// part the rounded remainder, so the pair is within 2^-16 of the value (2^-8
+// of the remainder, itself at most 2^-8 of the value, and the MFMA products
+// of both parts are exact in fp32).  Values past bf16's largest (infinities,
+// NaN, and the few fp32 values that round up to infinity) have no low part.
+__device__ __forceinline__ void split_bf16(float v, uint32_t &hi, uint32_t &lo) {
+    hi = f32_to_bf16_rne(v);
+    const float h = __uint_as_float(hi << 16);
+    lo = (hi & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_rne(v - h);
+}
+#endif
+
+}  // namespace aa

@@ -181,6 +181,7 @@ typedef int32_t lora_status_t;
 #define LORA_FLAG_ACTIVE_ONLY    2u
 #define LORA_FLAG_PARTIAL        4u
 #define LORA_FLAG_RELAY_GIVE_UP  8u   /* test hook, see lora_workspace_check */
+#define LORA_FLAG_ACCUMULATE    16u   /* lora_linear_backward: dA, dB += */
 
 #define LORA_MAX_SLICES 8
 #define LORA_MAX_RANK   512
@@ -403,6 +404,100 @@ lora_status_t moe_lora_apply(int32_t kind, void *y, int64_t ldy, int32_t reduce_
                              const int32_t *topk_ids, const float *topk_w, const int32_t *idx,
                              const int32_t *slot_rank, const float *scale, int32_t dtype,
                              uint32_t flags, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The adapter layer beside a frozen projection: the base product and the
+ * delta in one pass over y, and the gradient of the adapters ([vLLM]
+ * RowParallelLinearWithShardedLoRA.apply calls the base layer first and then
+ * add_shrink / add_expand; here the expand rides in the base product's
+ * pipeline).  bf16 only; idx, slot_rank, scale, A, B, N as above, and rows
+ * without an adapter get the projection alone.
+ * Alignment: as above for x, A, B, K and ldx; W 16-byte aligned and ldw % 8;
+ * every N[s] and ldy % 4 (lddy % 8 in the gradient when every N[s] % 8 == 0);
+ * lddx % 8; dA[s], dB[s], buf 16-byte aligned.  Sizes: K and every N[s] at most 2^24,
+ * and at most 2^22 tiles of 256 tokens x 256 columns of y or dx.
+ * Outputs and ws must not overlap each other or any input.  An infinity or NaN
+ * in one slot's A or B reaches only that slot's tokens and gradients.
+ * ------------------------------------------------------------------------ */
+
+/* Workspace bytes of lora_linear and lora_linear_backward for these sizes.
+ * Rules of `ws` as above (256-byte aligned, zero-filled once by
+ * lora_workspace_init, calls ordered on one stream, sized at the largest value
+ * of each argument when shared by several layers; a layer with some
+ * N[s] % 8 needs at least its own size), but it is not shared with the
+ * calls above, lora_build_segments excepted. */
+lora_status_t lora_linear_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
+                                         int32_t L, size_t *bytes);
+
+/*
+ * Forward:
+ *   u_s[t][j] = sum_k x[t][k] * A[s][i][j][k]        i = idx[t], j < slot_rank[i]
+ *   y[t][off_s + n] = round(sum_k x[t][k] * W[off_s + n][k] + bias[off_s + n]
+ *                           + scale[i] * sum_j u_s[t][j] * B[s][i][n][j])
+ *   off_s = N[0] + ... + N[s-1]
+ * W: device bf16 [sum N][ldw], the slices' projections one after the other;
+ * bias: device bf16 [sum N] or NULL; y: device bf16 [T][ldy], overwritten (its
+ * columns past sum N untouched).  All sums in fp32, one rounding; u enters the
+ * second product as a sum of two bf16 values (within 2^-16 of the fp32 value).
+ * buf: NULL, or device fp32 [S][T][R] that receives u (zero for tokens without
+ * an adapter and for j >= slot_rank[i]) for lora_linear_backward.
+ * flags: LORA_FLAG_SEGMENTS_READY.
+ */
+lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K,
+                          const void *W, int64_t ldw, const void *bias, const void *const *A,
+                          const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
+                          const int32_t *idx, const int32_t *slot_rank, const float *scale, float *buf,
+                          int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of lora_linear (and of lora_apply_packed) with W and bias frozen:
+ *   v_s[t][j] = scale[i] * sum_n dy[t][off_s + n] * B[s][i][n][j]
+ *   dx[t][k]  = round(sum_n dy[t][n] * W[n][k] + sum_s sum_j v_s[t][j] * A[s][i][j][k])
+ *   dA[s][i][j][k] = sum_{t: idx[t] = i} v_s[t][j] * x[t][k]
+ *   dB[s][i][n][j] = scale[i] * sum_{t: idx[t] = i} dy[t][off_s + n] * u_s[t][j]
+ * dy: device bf16 [T][lddy].  dx: device bf16 [T][lddx] or NULL (not wanted).
+ * W NULL: dx holds the base layer's own gradient and receives the adapters'
+ * part in place (rows without an adapter untouched).
+ * dA, dB: host arrays of S device pointers, fp32 [L][R][K] and [L][N[s]][R],
+ * or NULL (not wanted; at least one of dx, dA, dB is).  They are overwritten
+ * entirely, zeros for slots without tokens and ranks j >= slot_rank[i], or
+ * added to with LORA_FLAG_ACCUMULATE.  T == 0 clears them too.  No two output
+ * pointers may be equal.
+ * buf: u as lora_linear left it, or NULL (computed again from x and A; read
+ * for dB only).  Deterministic: no atomics on sums.
+ * flags: LORA_FLAG_SEGMENTS_READY, LORA_FLAG_ACCUMULATE.
+ */
+lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, float *const *dB,
+                                   const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T,
+                                   int32_t K, const void *W, int64_t ldw, const void *const *A,
+                                   const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
+                                   const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                                   const float *buf, int32_t dtype, uint32_t flags, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gradient norm and clip, per adapter slot over all of a model's stacked
+ * tensors (each adapter is a model of its own; L == 1 is the ordinary global
+ * norm).
+ *   g[n]  host array of n device pointers, g[i] = [L][m[i]] contiguous, of
+ *         dtype LORA_DT_F32 or LORA_DT_BF16; element aligned, m[i] >= 0 of any size
+ *         (faster when rows start at 16-byte addresses).
+ * ------------------------------------------------------------------------ */
+
+/* Workspace bytes of lora_grad_norm; its contents need no preparation. */
+lora_status_t lora_grad_workspace_size(const int64_t *m, int32_t n, int32_t L, size_t *bytes);
+
+/* norm[l] = sqrt(sum over i, e < m[i] of g[i][l][e]^2), summed in 64 bits in a
+ * fixed order, one rounding to fp32.  norm: device float [L] (0 when n == 0). */
+lora_status_t lora_grad_norm(float *norm, const void *const *g, const int64_t *m, int32_t n, int32_t L,
+                             int32_t dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* out[i][l][e] = round(g[i][l][e] * min(1, max_norm[l] / (norm[l] + 1e-6))).
+ * norm, max_norm: device float [L]; norm as lora_grad_norm left it, or joined
+ * over several groups of tensors.  out[i] may be g[i] (in place), else it must
+ * not overlap any g.  A NaN norm gives NaN, an infinite one zero times g. */
+lora_status_t lora_grad_clip(void *const *out, const void *const *g, const int64_t *m, int32_t n, int32_t L,
+                             const float *norm, const float *max_norm, int32_t dtype, void *stream);
 
 #ifdef __cplusplus
 }
