@@ -17,7 +17,7 @@ inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 struct LinWs {
     SegLayout seg;
     size_t order;       // int32 [T]: row order of the tile GEMM
-    size_t hl_u;        // bf16 [S][T][2R]: scale * u, high and low parts
+    size_t hl_u;        // bf16 [S][T][kLinPartsBwd R]: scale * u in parts
     size_t hl_v;        // the same of v
     size_t part;        // fp32 partial sums
     size_t pad;         // dy with slices of whole 8-element units, when some N_s % 8
@@ -32,8 +32,8 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     size_t o = w.seg.end;
     const size_t tsr = (size_t)T * S * R;
     w.order = o; o = align256(o + sizeof(int32_t) * (size_t)T);
-    w.hl_u = o;  o = align256(o + 4 * tsr);
-    w.hl_v = o;  o = align256(o + 4 * tsr);
+    w.hl_u = o;  o = align256(o + 2 * kLinPartsBwd * tsr);
+    w.hl_v = o;  o = align256(o + 2 * kLinPartsBwd * tsr);
     w.part = o;
     // the shrink's K splits: either one, or within an eighth of its input
     // bytes (pre_kspl: 8 k T S R <= in_bytes / 8)
@@ -134,14 +134,14 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
         if (!(flags & LORA_FLAG_SEGMENTS_READY))
             CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
         CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
-        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl, buf, order, st)));
+        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl, kLinPartsFwd, buf, order, st)));
     }
     LinArgs a{};
     a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
     a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
-    a.hl = hl; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
+    a.hl = hl; a.hl_row = kLinPartsFwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
     a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) {
         a.lora[s] = static_cast<const uint16_t *>(B[s]);
@@ -213,12 +213,12 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
     }
     if (dB) {
         if (buf) {
-            CHECK(launched(launch_lin_split(buf, T, S, L, R, idx, slot_rank, scale, seg, hl_u, nullptr, st)));
+            CHECK(launched(launch_lin_split(buf, T, S, L, R, idx, slot_rank, scale, seg, hl_u, kLinPartsBwd, nullptr, st)));
         } else {
             int32_t nsp = 1;
             CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
-            CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_u, nullptr,
-                                             nullptr, st)));
+            CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_u,
+                                             kLinPartsBwd, nullptr, nullptr, st)));
         }
         LinWgArgs a{};
         a.p = p; a.ldp = ldp; a.hl = hl_u;
@@ -236,7 +236,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
     if (dx || dA) {
         const int32_t nsp = lin_du_splits(T, L, N, S, R);
         CHECK(launched(launch_lin_du(p, ldp, poff, T, sl, S, L, R, slot_rank, seg, part, nsp, st)));
-        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_v, nullptr,
+        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_v, kLinPartsBwd, nullptr,
                                          dx ? order : nullptr, st)));
     }
     if (dA) {
@@ -257,7 +257,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         a.p = p; a.ldp = ldp;
         a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
         a.out = static_cast<uint16_t *>(dx); a.ldo = lddx;
-        a.hl = hl_v; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
+        a.hl = hl_v; a.hl_row = kLinPartsBwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
         a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
         a.accumulate = W == nullptr;
         for (int s = 0; s < S; ++s) {

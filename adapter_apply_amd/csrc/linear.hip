@@ -7,8 +7,8 @@
 // delta costs no pass over y and is rounded together with the base product.
 //
 // A rank vector (fp32) enters the MFMA as two bf16 parts side by side,
-// [high | low] against lora rows repeated, so that the product keeps the
-// fp32 buffer's precision (split_bf16).
+// [high | low] against lora rows repeated, so that the product is within 2^-16
+// of the fp32 buffer's, well below the bf16 rounding of the output.
 #include "linear.hpp"
 
 namespace aa {
@@ -22,33 +22,43 @@ constexpr int kXcds = 8;
 __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_cast(bf16x8_t, u); }
 
 // Tile GEMM.  Work-group = BM tokens x BN output columns, WM x WN waves.  A
-// K tile is 64 contraction steps: P (token rows, 128 bytes each) and Q (weight
-// rows), DMA'd into one of NST LDS stages, NST - 1 tiles ahead.
+// K tile is BK contraction steps: P (token rows) and Q (weight rows), DMA'd
+// into one of NST LDS stages, NST - 1 tiles ahead.
 //
-// LDS layout: 16-byte units of a 128-byte row are XOR-ed with (row / 2) % 8,
-// so the 16 rows a quarter wave reads together hit 16 different bank groups;
-// the DMA's LDS side is linear, so the XOR is applied to the global address.
-// Gradient (NN): Q rows are contraction steps, BN columns wide, and reach the
-// MFMA through transposed reads; the XOR moves 32-byte pairs by the row's low
-// bits, so the 4 rows of one transposed read hit different banks.
+// LDS layout: the 16-byte units of a P row (BK * 2 bytes) are XOR-ed with the
+// row's place in the 256-byte bank window, so the 16 rows a quarter wave reads
+// together hit 16 different bank groups; the DMA's LDS side is linear, so the
+// XOR is applied to the global address.  Gradient (NN): Q rows are contraction
+// steps, BN columns wide, and reach the MFMA through transposed reads; the
+// XOR moves 32-byte pairs by the row's low bits, so the 4 rows of one
+// transposed read hit different banks.
 //
 // D = Q . P^T (output columns as MFMA rows), so a lane holds 4 consecutive
 // output columns of one token.
+//
+// The fragments of the next 32 contraction steps are read, and the next tile's
+// DMA issued, between the MFMAs of the current 32, so the one barrier per tile
+// finds the MFMA pipe busy.
 //
 // Rows of another slot take part in a slot's K tile with a zero rank vector.
 // A 16-token block that holds only the slot's tokens adds straight into its
 // accumulators; a mixed block goes through a temporary and a select, because
 // zero times an infinity or NaN of this slot's lora rows must not reach the
 // other tokens.
-template <int BM, int BN, int WM, int WN, int NST, bool NN>
+template <int V>
+struct Const { static constexpr int v = V; };
+
+template <int BM, int BN, int WM, int WN, int BK, int NST, bool NN>
 __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
-    constexpr int NW = WM * WN, TH = NW * 64;
-    constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
-    constexpr int PB = BM * 128, QB = BN * 128;
+    constexpr int NW = WM * WN;
+    constexpr int MB = BM / WM / 16, NB = BN / WN / 16, KK = BK / 32;
+    constexpr int PB = BM * BK * 2, QB = BN * BK * 2;
     constexpr int PI = PB / 1024 / NW, QI = QB / 1024 / NW;
-    constexpr int CPR = NN ? BN / 8 : 8;          // 16-byte units per Q row
+    constexpr int UP = BK / 8;                    // 16-byte units per P row (and Q row, forward)
+    constexpr int CPR = NN ? BN / 8 : UP;         // 16-byte units per Q row
     static_assert(PI >= 1 && QI >= 1 && NW % 2 == 0, "whole DMA instructions per wave");
-    __shared__ __attribute__((aligned(16))) char s_stage[NST][PB + QB];
+    static_assert(BM * BN * 2 <= NST * (PB + QB), "the output tile fits the stages");
+    __shared__ __attribute__((aligned(16))) char s_stage[NST * (PB + QB)];
     __shared__ int s_tok[BM], s_slot[BM], s_list[BM], s_n;
     __shared__ unsigned s_bits[32];
 
@@ -78,13 +88,13 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
 
     if (tid < 32) s_bits[tid] = 0;
     __syncthreads();
-    if (tid < BM) {
-        const int m = m0 + tid;
+    for (int i = tid; i < BM; i += NW * 64) {
+        const int m = m0 + i;
         const int pos = min(m, a.T - 1);
         const int t = a.order ? a.order[pos] : pos;
         const int sl = m < a.T ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -2;
-        s_tok[tid] = t;
-        s_slot[tid] = sl;
+        s_tok[i] = t;
+        s_slot[i] = sl;
         if (sl >= 0) atomicOr(&s_bits[sl >> 5], 1u << (sl & 31));
     }
     __syncthreads();
@@ -115,105 +125,103 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     int nk = 0;
     if (a.w) {
         if (NN)
-            for (int s = 0; s < a.S; ++s) nk += (int)((a.n[s] + 63) / 64);
+            for (int s = 0; s < a.S; ++s) nk += (int)((a.n[s] + BK - 1) / BK);
         else
-            nk = (a.K + 63) / 64;
+            nk = (a.K + BK - 1) / BK;
     }
-    const int lc_per = (2 * a.R + 63) / 64;       // K tiles per rank vector
+    const int lc_per = (2 * a.R + BK - 1) / BK;   // K tiles per rank vector
     const int per_slot = lc_per * (NN ? a.S : 1);
     const int nv = nk + n_slots * per_slot;
 
     // DMA lanes: fixed rows, global units XOR-ed.
-    const int prow0 = w * 8 + (lane >> 3);        // + i * NW * 8
-    const int plc = (lane & 7) ^ ((prow0 >> 1) & 7);
+    auto pswz = [](int row) { return BK == 32 ? (row >> 2) & 3 : (row >> 1) & 7; };
+    auto qswz = [&](int row) {
+        if (!NN) return pswz(row);
+        return ((row & 3) | (CPR >= 16 ? ((row >> 3) & 1) << 2 : 0)) << 1;
+    };
+    const int prow0 = w * (64 / UP) + lane / UP;  // + i * NW * 64 / UP
+    const int plc = (lane % UP) ^ pswz(prow0);
     const uint16_t *pptr[PI];
 #pragma unroll
     for (int i = 0; i < PI; ++i)
-        pptr[i] = a.p + (int64_t)s_tok[prow0 + i * NW * 8] * a.ldp + plc * 8;
-    constexpr int RPI = 64 / CPR;                 // Q rows per DMA instruction
-    auto qrow = [&](int i) { return (i * NW + w) * RPI + lane / CPR; };
-    auto qlc = [&](int i) {
-        const int row = qrow(i), pc = lane % CPR;
-        if (!NN) return pc ^ ((row >> 1) & 7);
-        const int f = (row & 3) | (CPR >= 16 ? ((row >> 3) & 1) << 2 : 0);
-        return pc ^ (f << 1);
-    };
+        pptr[i] = a.p + (int64_t)s_tok[prow0 + i * (NW * 64 / UP)] * a.ldp + plc * 8;
+    auto qrow = [&](int i) { return (i * NW + w) * (64 / CPR) + lane / CPR; };
+    auto qlc = [&](int i) { return (lane % CPR) ^ qswz(qrow(i)); };
     const uint16_t *qptr[QI];
-    if (a.w) {
 #pragma unroll
-        for (int i = 0; i < QI; ++i) {
+    for (int i = 0; i < QI; ++i) {
+        qptr[i] = a.w;
+        if (a.w) {
             if (NN) {
                 const int64_t col = c0 + qlc(i) * 8;
-                qptr[i] = a.w + (int64_t)qrow(i) * a.ldw + (col < cend ? col : 0);
+                qptr[i] += (int64_t)qrow(i) * a.ldw + (col < cend ? col : 0);
             } else {
                 const int64_t n = min(c0 + qrow(i), cend - 1);
-                qptr[i] = a.w + (a.off[sc] + n) * a.ldw + qlc(i) * 8;
+                qptr[i] += (a.off[sc] + n) * a.ldw + qlc(i) * 8;
             }
         }
     }
     const void *zero = g_zero16;
+    const uint32_t lds0 = lds_addr(s_stage) + w * 1024;
 
-    int cs = 0;                 // gradient: slice and tile inside it of the next base K tile
-    int64_t ci = 0;
+    // The next base K tile: steps left in its row (forward) or slice, and the
+    // offsets into the P and Q rows.
+    int cs = 0;
+    int64_t rem = NN ? a.n[0] : a.K, po = NN ? a.poff[0] : 0, qo = NN ? a.off[0] * a.ldw : 0;
+    const int64_t qstep = NN ? BK * a.ldw : BK;
+    auto next_slice = [&]() {
+        if (NN && rem <= 0 && ++cs < a.S) {
+            rem = a.n[cs];
+            po = a.poff[cs];
+            qo = a.off[cs] * a.ldw;
+        }
+    };
+    auto advance = [&]() { rem -= BK; po += BK; qo += qstep; };
     auto issue = [&](int v, int stage) {
-        const uint32_t pl = lds_addr(&s_stage[stage][0]) + w * 1024;
-        const uint32_t ql = pl + PB;
+        // recomputed here each time: hoisted lane values would crowd the
+        // registers of the fast loop
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));
+        const int prow0 = w * (64 / UP) + lane / UP, plc = (lane % UP) ^ pswz(prow0);
+        auto qrow = [&](int i) { return (i * NW + w) * (64 / CPR) + lane / CPR; };
+        auto qlc = [&](int i) { return (lane % CPR) ^ qswz(qrow(i)); };
+        const uint32_t pl = lds0 + stage * (PB + QB), ql = pl + PB;
         if (v < nk) {
-            if (NN) {
-                while (ci * 64 >= a.n[cs]) { ++cs; ci = 0; }
-                const int64_t rem = a.n[cs] - ci * 64;
-                const int64_t pc = a.poff[cs] + ci * 64, qr = (a.off[cs] + ci * 64) * a.ldw;
-                // p holds whole 8-element units per slice, zero past N_s
+            next_slice();
 #pragma unroll
-                for (int i = 0; i < PI; ++i)
-                    dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + pc) : zero);
+            for (int i = 0; i < PI; ++i)
+                dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + po) : zero);
 #pragma unroll
-                for (int i = 0; i < QI; ++i)
-                    dma16(ql + i * NW * 1024,
-                          qrow(i) < rem ? (const void *)(qptr[i] + qr) : zero);
-                ++ci;
-            } else {
-                const int kb = v * 64, rem = a.K - kb;
-                if (rem >= 64) {
-#pragma unroll
-                    for (int i = 0; i < PI; ++i) dma16(pl + i * NW * 1024, pptr[i] + kb);
-#pragma unroll
-                    for (int i = 0; i < QI; ++i) dma16(ql + i * NW * 1024, qptr[i] + kb);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < PI; ++i)
-                        dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + kb) : zero);
-#pragma unroll
-                    for (int i = 0; i < QI; ++i)
-                        dma16(ql + i * NW * 1024, qlc(i) * 8 < rem ? (const void *)(qptr[i] + kb) : zero);
-                }
-            }
+            for (int i = 0; i < QI; ++i)
+                dma16(ql + i * NW * 1024,
+                      (NN ? qrow(i) : qlc(i) * 8) < rem ? (const void *)(qptr[i] + qo) : zero);
+            advance();
             return;
         }
         const int u = v - nk, d = u / per_slot, x = u - d * per_slot;
         const int s = NN ? x / lc_per : sc, c = x % lc_per;
         const int slot = __builtin_amdgcn_readfirstlane(s_list[d]);
         const int R = a.R;
-        const int pj = c * 64 + plc * 8;
-        const uint16_t *hl = a.hl + (int64_t)s * a.T * 2 * R;
+        const int pj = c * BK + plc * 8;
+        const uint16_t *hl = a.hl + (int64_t)s * a.T * a.hl_row;
 #pragma unroll
         for (int i = 0; i < PI; ++i) {
-            const int row = prow0 + i * NW * 8;
+            const int row = prow0 + i * (NW * 64 / UP);
             const bool in = s_slot[row] == slot && pj < 2 * R;
             dma16(pl + i * NW * 1024,
-                  in ? (const void *)(hl + (int64_t)s_tok[row] * 2 * R + pj) : zero);
+                  in ? (const void *)(hl + (int64_t)s_tok[row] * a.hl_row + pj) : zero);
         }
         const uint16_t *lo = a.lora[s];
 #pragma unroll
         for (int i = 0; i < QI; ++i) {
             const void *src = zero;
             if (NN) {
-                const int j2 = c * 64 + qrow(i);
+                const int j2 = c * BK + qrow(i);
                 const int64_t col = c0 + qlc(i) * 8;
                 if (j2 < 2 * R)
                     src = lo + ((int64_t)slot * R + (j2 < R ? j2 : j2 - R)) * a.K + (col < cend ? col : 0);
             } else {
-                const int j2 = c * 64 + qlc(i) * 8;
+                const int j2 = c * BK + qlc(i) * 8;
                 const int64_t n = min(c0 + qrow(i), cend - 1);
                 if (j2 < 2 * R) src = lo + ((int64_t)slot * cend + n) * R + (j2 < R ? j2 : j2 - R);
             }
@@ -230,108 +238,182 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     const int g = lane >> 4, l16 = lane & 15;
     auto pfrag = [&](const char *st, int mb, int kk) {
         const int row = (wm * MB + mb) * 16 + l16;
-        return frag(*reinterpret_cast<const uint4 *>(st + row * 128 + (((kk * 4 + g) ^ ((row >> 1) & 7)) << 4)));
+        return frag(*reinterpret_cast<const uint4 *>(st + row * (BK * 2) + (((kk * 4 + g) ^ pswz(row)) << 4)));
     };
     auto qfrag = [&](const char *st, int nb, int kk) {
         if (NN) {
             const int row = kk * 32 + g * 8 + (l16 >> 2);
             const int col = (wn * NB + nb) * 16 + (l16 & 3) * 4;
-            const int f = (row & 3) | (CPR >= 16 ? ((row >> 3) & 1) << 2 : 0);
-            const char *p = st + PB + row * (BN * 2) + ((((col >> 3) ^ (f << 1)) << 4) | ((col & 4) << 1));
+            const char *p = st + PB + row * (BN * 2) + ((((col >> 3) ^ qswz(row)) << 4) | ((col & 4) << 1));
             const uint2 x0 = tr_read(p), x1 = tr_read(p + 4 * BN * 2);
             return frag(make_uint4(x0.x, x0.y, x1.x, x1.y));
         }
         const int row = (wn * NB + nb) * 16 + l16;
-        return frag(*reinterpret_cast<const uint4 *>(st + PB + row * 128 + (((kk * 4 + g) ^ ((row >> 1) & 7)) << 4)));
+        return frag(*reinterpret_cast<const uint4 *>(st + PB + row * (BK * 2) + (((kk * 4 + g) ^ pswz(row)) << 4)));
+    };
+    auto stage_ptr = [&](int v) { return s_stage + (v % NST) * (PB + QB); };
+    // Tile v's reads are done: wait for tile v + 1 (the tiles after it may
+    // stay in flight) and meet.
+    auto meet = [&](int v) {
+        if (v + NST - 1 < nv) wait_barrier<(NST - 2) * (PI + QI)>();
+        else wait_barrier<0>();
     };
 
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i)
+    for (int i = 0; i < NST; ++i)
         if (i < nv) issue(i, i);
-    int stage = 0;
+    if (nv >= NST) wait_barrier<(NST - 1) * (PI + QI)>();
+    else wait_barrier<0>();
     for (int v = 0; v < nv; ++v) {
-        // tile v has landed once at most the NST - 2 tiles after it are in flight
-        if (v + NST - 2 < nv) wait_barrier<(NST - 2) * (PI + QI)>();
-        else wait_barrier<0>();
-        if (v + NST - 1 < nv) {
-            const int ns = stage + NST - 1;
-            issue(v + NST - 1, ns >= NST ? ns - NST : ns);
-        }
-        const char *st = s_stage[stage];
-        if (v < nk) {
+        // Fast tiles: tile v's DMA slot takes a whole base tile, v + NST.
+        next_slice();
+        if (v + NST < nk && rem >= BK) {
+            bf16x8_t fq[2][NB], fp[2][MB];
+            // The MFMAs of fragment set CUR; between them the other set is read
+            // from (st, kk) and, with DMA, tile v + NST's loads are issued.
+            auto step = [&](auto CUR, auto DMA, const char *st, int kk, uint32_t pl, int64_t po, int64_t qo) {
+                constexpr int cur = decltype(CUR)::v, nxt = cur ^ 1;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8_t q[NB], p[MB];
+                for (int j = 0; j < MB; ++j) {
+                    fp[nxt][j] = pfrag(st, j, kk);
 #pragma unroll
-                for (int i = 0; i < NB; ++i) q[i] = qfrag(st, i, kk);
+                    for (int i = j * NB / MB; i < (j + 1) * NB / MB; ++i) fq[nxt][i] = qfrag(st, i, kk);
+                    if (decltype(DMA)::v) {
 #pragma unroll
-                for (int j = 0; j < MB; ++j) p[j] = pfrag(st, j, kk);
+                        for (int i = j * PI / MB; i < (j + 1) * PI / MB; ++i)
+                            dma16(pl + i * NW * 1024, pptr[i] + po);
 #pragma unroll
-                for (int j = 0; j < MB; ++j)
+                        for (int i = j * QI / MB; i < (j + 1) * QI / MB; ++i)
+                            dma16(pl + PB + i * NW * 1024, qptr[i] + qo);
+                    }
 #pragma unroll
                     for (int i = 0; i < NB; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p[j], acc[i][j], 0, 0, 0);
+                        acc[i][j] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[cur][i], fp[cur][j], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            auto tile = [&](auto PAR) {
+                constexpr int par = decltype(PAR)::v;
+                if (KK == 2) step(Const<0>{}, Const<0>{}, stage_ptr(v), 1, 0u, 0, 0);
+                meet(v);
+                step(Const<KK == 2 ? 1 : par>{}, Const<1>{}, stage_ptr(v + 1), 0, lds0 + (v % NST) * (PB + QB),
+                     po, qo);
+                advance();
+                ++v;
+            };
+            {
+                const char *st = stage_ptr(v);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) fq[0][i] = qfrag(st, i, 0);
+#pragma unroll
+                for (int j = 0; j < MB; ++j) fp[0][j] = pfrag(st, j, 0);
             }
-        } else {
-            const int slot = __builtin_amdgcn_readfirstlane(s_list[(v - nk) / per_slot]);
-            bf16x8_t q[2][NB];
+            if (KK == 1) {
+                // two tiles a round (the fragment sets swap)
+                if (v + 1 + NST < nk && rem >= 2 * BK) {
+                    do {
+                        tile(Const<0>{});
+                        tile(Const<1>{});
+                    } while (v + 1 + NST < nk && rem >= 2 * BK);
+                }
+            } else {
+                do {
+                    tile(Const<0>{});
+                } while (v + NST < nk && rem >= BK);
+            }
+        }
+        // Any other tile, without the pipelined fragments.
+        const char *st = stage_ptr(v);
+        const bool base = v < nk;
+        const int slot = base ? 0 : __builtin_amdgcn_readfirstlane(s_list[(v - nk) / per_slot]);
+        bf16x8_t q[KK][NB];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int i = 0; i < NB; ++i) q[kk][i] = qfrag(st, i, kk);
+            for (int i = 0; i < NB; ++i) q[kk][i] = qfrag(st, i, kk);
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-                const int rs = s_slot[(wm * MB + j) * 16 + l16];
-                const bool mine = rs == slot;
-                if (__ballot(mine) == 0) continue;
-                const bf16x8_t p0 = pfrag(st, j, 0), p1 = pfrag(st, j, 1);
-                if (__ballot(!mine && rs != -2) == 0) {
+        for (int j = 0; j < MB; ++j) {
+            const int rs = s_slot[(wm * MB + j) * 16 + l16];
+            const bool mine = base || rs == slot;
+            if (__ballot(mine) == 0) continue;
+            bf16x8_t p[KK];
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[0][i], p0, acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[1][i], p1, acc[i][j], 0, 0, 0);
-                    }
-                } else {
+            for (int kk = 0; kk < KK; ++kk) p[kk] = pfrag(st, j, kk);
+            if (__ballot(!mine && rs != -2) == 0) {
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        floatx4_t t = {0.f, 0.f, 0.f, 0.f};
-                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[0][i], p0, t, 0, 0, 0);
-                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[1][i], p1, t, 0, 0, 0);
+                for (int i = 0; i < NB; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
-                    }
+                    for (int kk = 0; kk < KK; ++kk)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[kk][i], p[kk], acc[i][j], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    floatx4_t t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk)
+                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[kk][i], p[kk], t, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
                 }
             }
         }
-        if (++stage == NST) stage = 0;
+        if (v + 1 < nv) {
+            meet(v);
+            if (v + NST < nv) issue(v + NST, v % NST);
+        }
     }
 
-    // One rounding per output element; 4 consecutive columns per lane.
+    // One rounding per output element.
     const int64_t obase = NN ? 0 : a.off[sc];
+    if (NN && a.accumulate) {
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-        const int row = (wm * MB + j) * 16 + l16;
-        if (m0 + row >= a.T) continue;
-        if (a.accumulate && s_slot[row] < 0) continue;
-        uint16_t *o = a.out + (int64_t)s_tok[row] * a.ldo + obase;
+        for (int j = 0; j < MB; ++j) {
+            const int row = (wm * MB + j) * 16 + l16;
+            if (s_slot[row] < 0) continue;
+            uint16_t *o = a.out + (int64_t)s_tok[row] * a.ldo;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int64_t c = c0 + (wn * NB + i) * 16 + 4 * g;
-            if (c >= cend) continue;
-            floatx4_t r = acc[i][j];
-            uint2 *dst = reinterpret_cast<uint2 *>(o + c);
-            if (!NN && a.bias) {
-                const uint16_t *b = a.bias + obase + c;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] += bf16_to_f32(b[e]);
-            }
-            if (NN && a.accumulate) {
+            for (int i = 0; i < NB; ++i) {
+                const int64_t c = c0 + (wn * NB + i) * 16 + 4 * g;
+                if (c >= cend) continue;
+                const floatx4_t r = acc[i][j];
+                uint2 *dst = reinterpret_cast<uint2 *>(o + c);
                 const uint2 old = *dst;
-                r[0] += bf16_lo(old.x); r[1] += bf16_hi(old.x);
-                r[2] += bf16_lo(old.y); r[3] += bf16_hi(old.y);
+                *dst = make_uint2(pack_bf16x2(r[0] + bf16_lo(old.x), r[1] + bf16_hi(old.x)),
+                                  pack_bf16x2(r[2] + bf16_lo(old.y), r[3] + bf16_hi(old.y)));
             }
-            *dst = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
         }
+        return;
+    }
+    // Through LDS (the stages are free), so that a wave writes whole rows: 8
+    // bytes per lane, the 16-byte units of a row XOR-ed with the row.
+    constexpr int UO = BN / 8;
+    wait_barrier<0>();
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int cl = (wn * NB + i) * 16 + 4 * g;
+        floatx4_t bias = {0.f, 0.f, 0.f, 0.f};
+        if (!NN && a.bias && c0 + cl < cend) {
+            const uint16_t *b = a.bias + obase + c0 + cl;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bias[e] = bf16_to_f32(b[e]);
+        }
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+            const int row = (wm * MB + j) * 16 + l16;
+            const floatx4_t r = acc[i][j];
+            *reinterpret_cast<uint2 *>(s_stage + row * (BN * 2) + (((cl >> 3) ^ (row & (UO - 1))) << 4) +
+                                       ((cl & 4) << 1)) =
+                make_uint2(pack_bf16x2(r[0] + bias[0], r[1] + bias[1]), pack_bf16x2(r[2] + bias[2], r[3] + bias[3]));
+        }
+    }
+    __syncthreads();
+    constexpr int LPR = BN / 4, RPW = 64 / LPR > 0 ? 64 / LPR : 1;   // lanes per row, rows per wave store
+    for (int r0 = w * RPW; r0 < BM; r0 += NW * RPW) {
+        const int row = r0 + lane / LPR, cl = (lane % LPR) * 4;
+        const uint2 v = *reinterpret_cast<const uint2 *>(
+            s_stage + row * (BN * 2) + (((cl >> 3) ^ (row & (UO - 1))) << 4) + ((cl & 4) << 1));
+        if (m0 + row < a.T && c0 + cl < cend)
+            *reinterpret_cast<uint2 *>(a.out + (int64_t)s_tok[row] * a.ldo + obase + c0 + cl) = v;
     }
 }
 
@@ -407,21 +489,19 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     if (mine != slot || j >= a.R) return;
     const float sc = a.scale[slot];
     const int64_t row = (int64_t)s * a.T + t;
-    uint32_t hi[4], lo[4];
+    float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (j + e >= r) sum[e] = 0.f;
-        split_bf16(j + e < r ? sc * sum[e] : 0.f, hi[e], lo[e]);
+        v[e] = j + e < r ? sc * sum[e] : 0.f;
     }
-    uint16_t *h = a.hl + row * 2 * a.R + j;
-    *reinterpret_cast<uint2 *>(h) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *reinterpret_cast<uint2 *>(h + a.R) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    store_parts(a.hl + row * kLinPartsFwd * a.R, kLinPartsFwd, a.R, j, v);
     if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
 }
 
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
-// own, scales, splits into [high | low], and clears buf for tokens without a
+// own, scales, splits into bf16 parts, and clears buf for tokens without a
 // slot.  The first block row also writes the row order of the tile GEMM: the
 // slot-sorted tokens, then the tokens without a slot in token order (their
 // rank among themselves is counted from idx; one pass over the idx before the
@@ -430,7 +510,7 @@ constexpr int kRedThreads = 256;
 struct LinReduceArgs {
     const float *part;
     const float *in;        // the caller's rank vectors, by token (part null)
-    int32_t nsp, T, S, L, R;
+    int32_t nsp, T, S, L, R, parts;
     const int32_t *idx, *slot_rank;
     const float *scale;
     SegPtrs seg;
@@ -491,19 +571,17 @@ __global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
     }
     const float sc = a.scale[slot];
     const int64_t row = (int64_t)s * a.T + t;
-    uint32_t hi[4], lo[4];
+    float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (j + e >= r) sum[e] = 0.f;
-        split_bf16(j + e < r ? sc * sum[e] : 0.f, hi[e], lo[e]);
+        v[e] = j + e < r ? sc * sum[e] : 0.f;
     }
-    uint16_t *h = a.hl + row * 2 * a.R + j;
-    *reinterpret_cast<uint2 *>(h) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *reinterpret_cast<uint2 *>(h + a.R) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    store_parts(a.hl + row * a.parts * a.R, a.parts, a.R, j, v);
     if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
 }
 
-template <int BM, int BN, int WM, int WN, int NST>
+template <int BM, int BN, int WM, int WN, int BK, int NST>
 hipError_t run_tile(LinArgs a, bool gradient, hipStream_t st) {
     a.m_tiles = (a.T + BM - 1) / BM;
     if (gradient) {
@@ -518,8 +596,8 @@ hipError_t run_tile(LinArgs a, bool gradient, hipStream_t st) {
         a.n_tiles = c;
     }
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles)), block(WM * WN * 64);
-    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false>), grid, block, 0, st, a);
+    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, BK, NST, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, BK, NST, false>), grid, block, 0, st, a);
     return hipGetLastError();
 }
 
@@ -543,9 +621,9 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192) return run_tile<256, 256, 2, 4, 2>(a, gradient, st);
-    if (tiles(a.T, a.K, a.n, a.S, gradient, 128) >= 192) return run_tile<128, 128, 2, 2, 2>(a, gradient, st);
-    return run_tile<64, 64, 2, 2, 4>(a, gradient, st);
+    if (tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192) return run_tile<256, 256, 2, 2, 32, 4>(a, gradient, st);
+    if (tiles(a.T, a.K, a.n, a.S, gradient, 128) >= 192) return run_tile<128, 128, 2, 2, 32, 4>(a, gradient, st);
+    return run_tile<64, 64, 2, 2, 64, 4>(a, gradient, st);
 }
 
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
@@ -578,22 +656,22 @@ static hipError_t run_reduce(LinReduceArgs a, hipStream_t st) {
 
 hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
                              const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                             const SegPtrs &seg, uint16_t *hl, float *buf, int32_t *order,
+                             const SegPtrs &seg, uint16_t *hl, int32_t parts, float *buf, int32_t *order,
                              hipStream_t st) {
     LinReduceArgs a{};
     a.part = part; a.nsp = nsp; a.T = T; a.S = S; a.L = L; a.R = R;
     a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg;
-    a.hl = hl; a.buf = buf; a.order = order;
+    a.hl = hl; a.parts = parts; a.buf = buf; a.order = order;
     return run_reduce(a, st);
 }
 
 hipError_t launch_lin_split(const float *buf, int32_t T, int32_t S, int32_t L, int32_t R,
                             const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                            const SegPtrs &seg, uint16_t *hl, int32_t *order, hipStream_t st) {
+                            const SegPtrs &seg, uint16_t *hl, int32_t parts, int32_t *order, hipStream_t st) {
     LinReduceArgs a{};
     a.in = buf; a.T = T; a.S = S; a.L = L; a.R = R;
     a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg;
-    a.hl = hl; a.order = order;
+    a.hl = hl; a.parts = parts; a.order = order;
     return run_reduce(a, st);
 }
 

@@ -17,7 +17,8 @@ struct LinArgs {
     const uint16_t *bias;     // [sum N] or null (forward)
     uint16_t *out;
     int64_t ldo;
-    const uint16_t *hl;       // bf16 [S][T][2R]: scaled rank vectors, high and low parts
+    const uint16_t *hl;       // bf16 [S][T][hl_row]: scaled rank vectors' parts (the first two are used)
+    int32_t hl_row;           // kLinParts* R
     const int32_t *order;     // row position -> token, or null (identity)
     const int32_t *idx;
     const int32_t *slot_rank;
@@ -32,6 +33,10 @@ struct LinArgs {
 };
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
+// bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
+// dx), three where it is an fp32 gradient (split_bf16).
+constexpr int kLinPartsFwd = 2;
+constexpr int kLinPartsBwd = 3;
 // Whether the sizes stay within what one launch's grid takes.
 bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
 
@@ -41,17 +46,17 @@ hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, c
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,
                              const int32_t *slot_rank, const float *scale, uint16_t *hl, float *buf,
                              hipStream_t st);
-// hl (and buf, if given) from partial sums [S][nsp][T][R] by slot-sorted
-// position; `scaled`: hl holds scale * sum.  order (nullable): receives the
+// hl (`parts` parts of scale * sum; and buf, if given) from partial sums
+// [S][nsp][T][R] by slot-sorted position.  order (nullable): receives the
 // slot-sorted tokens followed by the tokens without a slot.
 hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
                              const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                             const SegPtrs &seg, uint16_t *hl, float *buf, int32_t *order,
+                             const SegPtrs &seg, uint16_t *hl, int32_t parts, float *buf, int32_t *order,
                              hipStream_t st);
 // hl from a caller's fp32 rank vectors [S][T][R]; order as above.
 hipError_t launch_lin_split(const float *buf, int32_t T, int32_t S, int32_t L, int32_t R,
                             const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                            const SegPtrs &seg, uint16_t *hl, int32_t *order, hipStream_t st);
+                            const SegPtrs &seg, uint16_t *hl, int32_t parts, int32_t *order, hipStream_t st);
 
 // Gradient side (linear_bwd.hip).
 struct PadMap {
@@ -72,7 +77,7 @@ hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, 
 struct LinWgArgs {
     const uint16_t *p;
     int64_t ldp;
-    const uint16_t *hl;
+    const uint16_t *hl;        // bf16 [S][T][3R]
     float *out[kMaxSlices];
     int64_t m[kMaxSlices];
     int64_t poff[kMaxSlices];
@@ -132,15 +137,27 @@ __device__ __forceinline__ int slot_of_token(const int32_t *idx, const int32_t *
     if (s < 0 || s >= L) return -1;
     return slot_rank && slot_rank[s] <= 0 ? -1 : s;
 }
-// fp32 as a sum of two bf16 values: the high part rounded to nearest, the low
-// part the rounded remainder, so the pair is within 2^-16 of the value (2^-8
-// of the remainder, itself at most 2^-8 of the value, and the MFMA products
-// of both parts are exact in fp32).  Values past bf16's largest (infinities,
-// NaN, and the few fp32 values that round up to infinity) have no low part.
-__device__ __forceinline__ void split_bf16(float v, uint32_t &hi, uint32_t &lo) {
-    hi = f32_to_bf16_rne(v);
-    const float h = __uint_as_float(hi << 16);
-    lo = (hi & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_rne(v - h);
+// fp32 as a sum of bf16 parts, each the rounded remainder of those before it:
+// a remainder is at most 2^-8 of the part's value, so two parts are within
+// 2^-16 of the value and three hold all its 24 bits (2^-24); the MFMA products
+// of a part are exact in fp32.  Values past bf16's largest (infinities, NaN,
+// and the few fp32 values that round up to infinity) are all in the first part.
+__device__ __forceinline__ void split_bf16(float v, uint32_t (&part)[3]) {
+    part[0] = f32_to_bf16_rne(v);
+    const bool whole = (part[0] & 0x7f80u) == 0x7f80u;
+    const float r = whole ? 0.f : v - __uint_as_float(part[0] << 16);
+    part[1] = f32_to_bf16_rne(r);
+    part[2] = f32_to_bf16_rne(r - __uint_as_float(part[1] << 16));
+}
+// The parts of 4 ranks j..j+3 of one rank vector row (`parts` of R each).
+__device__ __forceinline__ void store_parts(uint16_t *row, int parts, int R, int j, const float (&v)[4]) {
+    uint32_t p[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_bf16(v[e], p[e]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (k < parts)
+            *reinterpret_cast<uint2 *>(row + k * R + j) = make_uint2(p[0][k] | p[1][k] << 16, p[2][k] | p[3][k] << 16);
 }
 #endif
 

@@ -23,7 +23,7 @@ __device__ __forceinline__ bf16x8_t frag2(const uint2 &a, const uint2 &b) {
 // groups, where the row has 8 pairs) lie in different banks.
 template <int CPR>
 __device__ __forceinline__ int tr_swz(int row) {
-    return CPR <= 4 ? 0 : CPR == 8 ? (row & 3) << 1 : ((row & 3) | ((row >> 3) & 1) << 2) << 1;
+    return CPR == 2 ? 0 : CPR == 4 ? 0 : CPR == 8 ? (row & 3) << 1 : ((row & 3) | ((row >> 3) & 1) << 2) << 1;
 }
 // Transposed fragment: 8 rows 32 kk + 8 g.. of columns col0..+15.
 template <int CPR>
@@ -154,18 +154,19 @@ __global__ __launch_bounds__(256) void k_lin_du(DuArgs a) {
 
 // Weight gradients: work-group = (128 columns of a slice, RB ranks, slot,
 // token split), 4 waves of 32 columns, 64 tokens per stage (both operands
-// through transposed reads; the rank vectors' high and low parts add into the
-// same accumulators).  Slots without tokens write zeros.
+// through transposed reads; the rank vectors' three bf16 parts, which hold the
+// whole fp32 value, add into the same accumulators).  Slots without tokens
+// write zeros.
 constexpr int kWgCols = 128;
 constexpr int kWgTokens = 1024;       // token indexes staged at a time
 
 template <int RB, bool TRANSPOSED>
 __global__ __launch_bounds__(256) void k_lin_wg(LinWgArgs a, int nrb) {
-    constexpr int PB = 64 * kWgCols * 2, QB = 64 * RB * 4;
-    constexpr int CPP = kWgCols / 8, CPQ = RB / 4, RPP = 64 / CPP, RPQ = 64 / CPQ;
-    constexpr int PI = PB / 4096, QI = QB / 4096, NB = RB / 16;
-    static_assert(QI >= 1, "whole DMA instructions per wave");
-    __shared__ __attribute__((aligned(16))) char s_stage[2][PB + QB];
+    constexpr int NP = kLinPartsBwd;
+    constexpr int PB = 64 * kWgCols * 2, QB = 64 * RB * 2;      // bytes of a stage's p rows and of one part
+    constexpr int CPP = kWgCols / 8, CPQ = RB / 8, RPP = 64 / CPP, RPQ = 64 / CPQ;
+    constexpr int PI = PB / 4096, QN = NP * QB / 1024, NB = RB / 16;
+    __shared__ __attribute__((aligned(16))) char s_stage[2][PB + NP * QB];
     __shared__ int s_tok[kWgTokens];
     int s = 0;
     const int mt_all = blockIdx.x / nrb, r0 = (blockIdx.x - mt_all * nrb) * RB;
@@ -182,7 +183,8 @@ __global__ __launch_bounds__(256) void k_lin_wg(LinWgArgs a, int nrb) {
         e = min(b + per, e);
     }
     const void *zero = g_zero16;
-    const uint16_t *hl = a.hl + (int64_t)s * a.T * 2 * a.R;
+    const int hlr = NP * a.R;
+    const uint16_t *hl = a.hl + (int64_t)s * a.T * hlr;
 
     floatx4_t acc[2][NB];
 #pragma unroll
@@ -206,14 +208,14 @@ __global__ __launch_bounds__(256) void k_lin_wg(LinWgArgs a, int nrb) {
                       in ? (const void *)(a.p + (int64_t)s_tok[in ? tk : 0] * a.ldp + a.poff[s] + c) : zero);
             }
 #pragma unroll
-            for (int i = 0; i < QI; ++i) {
-                const int row = (i * 4 + w) * RPQ + lane / CPQ, tk = v * 64 + row;
-                const int u = (lane % CPQ) ^ tr_swz<CPQ>(row);         // unit: high parts, then low
-                const int j = r0 + (u % (RB / 8)) * 8;
+            for (int i = 0; i < (QN + 3) / 4; ++i) {
+                const int q = i * 4 + w;                       // DMA instruction: part, rows
+                if (QN % 4 && q >= QN) break;
+                const int part = q / (QB / 1024), row = (q % (QB / 1024)) * RPQ + lane / CPQ, tk = v * 64 + row;
+                const int j = r0 + ((lane % CPQ) ^ tr_swz<CPQ>(row)) * 8;
                 const bool in = tk < cnt && j < a.R;
                 dma16(ql + i * 4096,
-                      in ? (const void *)(hl + (int64_t)s_tok[in ? tk : 0] * 2 * a.R + (u >= RB / 8 ? a.R : 0) + j)
-                         : zero);
+                      in ? (const void *)(hl + (int64_t)s_tok[in ? tk : 0] * hlr + part * a.R + j) : zero);
             }
         };
         issue(0, 0);
@@ -227,10 +229,10 @@ __global__ __launch_bounds__(256) void k_lin_wg(LinWgArgs a, int nrb) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) p[i] = tr_frag<CPP>(st, w * 32 + i * 16, kk, lane);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < NP; ++h)
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        const bf16x8_t q = tr_frag<CPQ>(st + PB, h * RB + j * 16, kk, lane);
+                        const bf16x8_t q = tr_frag<CPQ>(st + PB + h * QB, j * 16, kk, lane);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             acc[i][j] = TRANSPOSED
