@@ -36,22 +36,20 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // D = Q . P^T (output columns as MFMA rows), so a lane holds 4 consecutive
 // output columns of one token.
 //
-// The fragments of the next 32 contraction steps are read, and the next tile's
-// DMA issued, between the MFMAs of the current 32, so the one barrier per tile
-// finds the MFMA pipe busy.
+// A tile's 64 steps are two fragment sets of 32.  While the MFMAs of the first
+// run, the second is read (the stage is then free, and the DMA of the tile NST
+// ahead starts); while those of the second run, the next tile's first set is
+// read.  Both barriers of a tile find the MFMA pipe busy.
 //
-// Rows of another slot take part in a slot's K tile with a zero rank vector.
-// A 16-token block that holds only the slot's tokens adds straight into its
-// accumulators; a mixed block goes through a temporary and a select, because
-// zero times an infinity or NaN of this slot's lora rows must not reach the
-// other tokens.
-template <int V>
-struct Const { static constexpr int v = V; };
-
-template <int BM, int BN, int WM, int WN, int BK, int NST, bool NN>
-__global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
-    constexpr int NW = WM * WN;
-    constexpr int MB = BM / WM / 16, NB = BN / WN / 16, KK = BK / 32;
+// An infinity or NaN in one slot's lora rows must not reach other slots'
+// tokens, and zero times either is NaN, so zeroed rank vectors do not isolate
+// them: a 16-token block of one slot takes part in that slot's K tiles only,
+// and a block of several goes through a temporary and a select, in the K
+// tiles (MIXED) or after them.
+template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED>
+__global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
+    constexpr int NW = WM * WN, BK = 64, KK = 2;
+    constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
     constexpr int PB = BM * BK * 2, QB = BN * BK * 2;
     constexpr int PI = PB / 1024 / NW, QI = QB / 1024 / NW;
     constexpr int UP = BK / 8;                    // 16-byte units per P row (and Q row, forward)
@@ -59,7 +57,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     static_assert(PI >= 1 && QI >= 1 && NW % 2 == 0, "whole DMA instructions per wave");
     static_assert(BM * BN * 2 <= NST * (PB + QB), "the output tile fits the stages");
     __shared__ __attribute__((aligned(16))) char s_stage[NST * (PB + QB)];
-    __shared__ int s_tok[BM], s_slot[BM], s_list[BM], s_n;
+    __shared__ int s_tok[BM], s_slot[BM], s_list[BM], s_whole[BM / 16], s_n, s_any;
     __shared__ unsigned s_bits[32];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -87,6 +85,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     const int64_t cend = NN ? a.K : a.n[sc];
 
     if (tid < 32) s_bits[tid] = 0;
+    if (tid == 0) s_any = 0;
     __syncthreads();
     for (int i = tid; i < BM; i += NW * 64) {
         const int m = m0 + i;
@@ -95,7 +94,12 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
         const int sl = m < a.T ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -2;
         s_tok[i] = t;
         s_slot[i] = sl;
-        if (sl >= 0) atomicOr(&s_bits[sl >> 5], 1u << (sl & 31));
+        // MIXED: every slot; else the slots that have a 16-token block of their own
+        const int first = __shfl(sl, lane & 48);
+        const bool whole = !(__ballot(sl != first && sl != -2) >> (lane & 48) & 0xffff);
+        if (!MIXED && (lane & 15) == 0) s_whole[i >> 4] = whole;
+        if (sl >= 0 && (MIXED || whole)) atomicOr(&s_bits[sl >> 5], 1u << (sl & 31));
+        if (sl >= 0) s_any = 1;
     }
     __syncthreads();
     if (tid < 64) {
@@ -118,7 +122,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     }
     __syncthreads();
     const int n_slots = __builtin_amdgcn_readfirstlane(s_n);
-    if (a.accumulate && n_slots == 0) return;
+    if (a.accumulate && !s_any) return;
 
     // K tiles: the projection's (per slice in the gradient), then per slot
     // (and slice) the [high | low] rank vectors.
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     const int nv = nk + n_slots * per_slot;
 
     // DMA lanes: fixed rows, global units XOR-ed.
-    auto pswz = [](int row) { return BK == 32 ? (row >> 2) & 3 : (row >> 1) & 7; };
+    auto pswz = [](int row) { return (row >> 1) & 7; };
     auto qswz = [&](int row) {
         if (!NN) return pswz(row);
         return ((row & 3) | (CPR >= 16 ? ((row >> 3) & 1) << 2 : 0)) << 1;
@@ -254,6 +258,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
     auto stage_ptr = [&](int v) { return s_stage + (v % NST) * (PB + QB); };
     // Tile v's reads are done: wait for tile v + 1 (the tiles after it may
     // stay in flight) and meet.
+    auto meet_reads = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     auto meet = [&](int v) {
         if (v + NST - 1 < nv) wait_barrier<(NST - 2) * (PI + QI)>();
         else wait_barrier<0>();
@@ -268,98 +273,137 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
         next_slice();
         if (v + NST < nk && rem >= BK) {
             bf16x8_t fq[2][NB], fp[2][MB];
-            // The MFMAs of fragment set CUR; between them the other set is read
-            // from (st, kk) and, with DMA, tile v + NST's loads are issued.
-            auto step = [&](auto CUR, auto DMA, const char *st, int kk, uint32_t pl, int64_t po, int64_t qo) {
-                constexpr int cur = decltype(CUR)::v, nxt = cur ^ 1;
+            auto mfmas = [&](int set, int j) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[set][i], fp[set][j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            // share j of n of a fragment set's reads, or of a tile's DMA
+            auto reads = [&](int set, const char *st, int kk, int j, int n) {
+#pragma unroll
+                for (int i = j * MB / n; i < (j + 1) * MB / n; ++i) fp[set][i] = pfrag(st, i, kk);
+#pragma unroll
+                for (int i = j * NB / n; i < (j + 1) * NB / n; ++i) fq[set][i] = qfrag(st, i, kk);
+            };
+            auto loads = [&](uint32_t pl, int j, int n) {
+#pragma unroll
+                for (int i = j * PI / n; i < (j + 1) * PI / n; ++i) dma16(pl + i * NW * 1024, pptr[i] + po);
+#pragma unroll
+                for (int i = j * QI / n; i < (j + 1) * QI / n; ++i) dma16(pl + PB + i * NW * 1024, qptr[i] + qo);
+            };
+            constexpr int RG = MB / 4 > 0 ? MB / 4 : 1;   // MFMA groups that carry the second set's reads
+            constexpr int LG = MB - RG - (MB > 4);        // and a tile's DMA
+            reads(0, stage_ptr(v), 0, 0, 1);
+            do {
+                const char *st = stage_ptr(v);
+                const uint32_t pl = lds0 + (v % NST) * (PB + QB);
+                // first half: the stage's second fragment set, after which the
+                // stage is free for the tile NST ahead
 #pragma unroll
                 for (int j = 0; j < MB; ++j) {
-                    fp[nxt][j] = pfrag(st, j, kk);
-#pragma unroll
-                    for (int i = j * NB / MB; i < (j + 1) * NB / MB; ++i) fq[nxt][i] = qfrag(st, i, kk);
-                    if (decltype(DMA)::v) {
-#pragma unroll
-                        for (int i = j * PI / MB; i < (j + 1) * PI / MB; ++i)
-                            dma16(pl + i * NW * 1024, pptr[i] + po);
-#pragma unroll
-                        for (int i = j * QI / MB; i < (j + 1) * QI / MB; ++i)
-                            dma16(pl + PB + i * NW * 1024, qptr[i] + qo);
-                    }
-#pragma unroll
-                    for (int i = 0; i < NB; ++i)
-                        acc[i][j] =
-                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[cur][i], fp[cur][j], acc[i][j], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
+                    if (j < RG) reads(1, st, 1, j, RG);
+                    if (j == RG) meet_reads();
+                    if (j >= RG && j < RG + LG) loads(pl, j - RG, LG);
+                    mfmas(0, j);
                 }
-            };
-            auto tile = [&](auto PAR) {
-                constexpr int par = decltype(PAR)::v;
-                if (KK == 2) step(Const<0>{}, Const<0>{}, stage_ptr(v), 1, 0u, 0, 0);
-                meet(v);
-                step(Const<KK == 2 ? 1 : par>{}, Const<1>{}, stage_ptr(v + 1), 0, lds0 + (v % NST) * (PB + QB),
-                     po, qo);
                 advance();
                 ++v;
-            };
-            {
-                const char *st = stage_ptr(v);
+                wait_barrier<(NST - 1) * (PI + QI)>();     // tile v has landed
+                // second half: the next tile's first set
+                const char *nx = stage_ptr(v);
 #pragma unroll
-                for (int i = 0; i < NB; ++i) fq[0][i] = qfrag(st, i, 0);
-#pragma unroll
-                for (int j = 0; j < MB; ++j) fp[0][j] = pfrag(st, j, 0);
-            }
-            if (KK == 1) {
-                // two tiles a round (the fragment sets swap)
-                if (v + 1 + NST < nk && rem >= 2 * BK) {
-                    do {
-                        tile(Const<0>{});
-                        tile(Const<1>{});
-                    } while (v + 1 + NST < nk && rem >= 2 * BK);
+                for (int j = 0; j < MB; ++j) {
+                    reads(0, nx, 0, j, MB);
+                    mfmas(1, j);
                 }
-            } else {
-                do {
-                    tile(Const<0>{});
-                } while (v + NST < nk && rem >= BK);
-            }
+            } while (v + NST < nk && rem >= BK);
         }
         // Any other tile, without the pipelined fragments.
         const char *st = stage_ptr(v);
         const bool base = v < nk;
         const int slot = base ? 0 : __builtin_amdgcn_readfirstlane(s_list[(v - nk) / per_slot]);
-        bf16x8_t q[KK][NB];
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+        for (int kk = 0; kk < KK; ++kk) {
+            bf16x8_t q[NB];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) q[kk][i] = qfrag(st, i, kk);
+            for (int i = 0; i < NB; ++i) q[i] = qfrag(st, i, kk);
 #pragma unroll
-        for (int j = 0; j < MB; ++j) {
-            const int rs = s_slot[(wm * MB + j) * 16 + l16];
-            const bool mine = base || rs == slot;
-            if (__ballot(mine) == 0) continue;
-            bf16x8_t p[KK];
+            for (int j = 0; j < MB; ++j) {
+                const int rs = s_slot[(wm * MB + j) * 16 + (MIXED ? l16 : 0)];
+                const bool mine = base || (rs == slot && (MIXED || s_whole[wm * MB + j]));
+                if (__ballot(mine) == 0) continue;
+                const bf16x8_t p = pfrag(st, j, kk);
+                if (!MIXED || __ballot(!mine && rs != -2) == 0) {
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) p[kk] = pfrag(st, j, kk);
-            if (__ballot(!mine && rs != -2) == 0) {
+                    for (int i = 0; i < NB; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p, acc[i][j], 0, 0, 0);
+                } else {
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
+                    for (int i = 0; i < NB; ++i) {
+                        const floatx4_t z = {0.f, 0.f, 0.f, 0.f};
+                        const floatx4_t t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p, z, 0, 0, 0);
 #pragma unroll
-                    for (int kk = 0; kk < KK; ++kk)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[kk][i], p[kk], acc[i][j], 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    floatx4_t t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk)
-                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[kk][i], p[kk], t, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
+                    }
                 }
             }
         }
         if (v + 1 < nv) {
             meet(v);
             if (v + NST < nv) issue(v + NST, v % NST);
+        }
+    }
+
+    // 16-token blocks that hold several slots: each slot's part from global
+    // memory into a temporary, kept for the slot's own tokens.  (At most one
+    // block per slot boundary; kept out of the K tiles, where a select on the
+    // accumulators made the compiler spill them: 2.45 against 1.75 ms for the
+    // forward tiles of 8192 tokens, 4096 x 28672, rank 64.)
+    if (!MIXED) {
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+            if (s_whole[wm * MB + j]) continue;
+            const int row = (wm * MB + j) * 16 + l16, rs = s_slot[row];
+            unsigned long long todo = __ballot(rs >= 0) & 0xffff;
+            while (todo) {
+                const int slot = __builtin_amdgcn_readlane(rs, __ffsll(todo) - 1);
+                const bool mine = rs == slot;
+                todo &= ~__ballot(mine);
+                floatx4_t t[NB];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) t[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+                for (int s = NN ? 0 : sc; s < (NN ? a.S : sc + 1); ++s) {
+                    const uint16_t *hl = a.hl + ((int64_t)s * a.T + s_tok[row]) * a.hl_row;
+                    for (int k0 = 0; k0 < 2 * a.R; k0 += 32) {
+                        const int k = k0 + g * 8, kr = k < a.R ? k : k - a.R;
+                        uint4 p = make_uint4(0, 0, 0, 0);
+                        if (mine && k < 2 * a.R) p = ldg<uint4>(hl + k);
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const int64_t n = min(c0 + (wn * NB + i) * 16 + l16, cend - 1);
+                            uint4 q = make_uint4(0, 0, 0, 0);
+                            if (k < 2 * a.R) {
+                                if (NN) {
+                                    const uint16_t *c = a.lora[s] + ((int64_t)slot * a.R + kr) * a.K + n;
+                                    uint32_t v[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) v[e] = c[(int64_t)e * a.K];
+                                    q = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                                                   v[6] | v[7] << 16);
+                                } else {
+                                    q = ldg<uint4>(a.lora[s] + ((int64_t)slot * cend + n) * a.R + kr);
+                                }
+                            }
+                            t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(q), frag(p), t[i], 0, 0, 0);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] += mine ? t[i][e] : 0.f;
+            }
         }
     }
 
@@ -412,7 +456,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_lin_tile(LinArgs a) {
         const int row = r0 + lane / LPR, cl = (lane % LPR) * 4;
         const uint2 v = *reinterpret_cast<const uint2 *>(
             s_stage + row * (BN * 2) + (((cl >> 3) ^ (row & (UO - 1))) << 4) + ((cl & 4) << 1));
-        if (m0 + row < a.T && c0 + cl < cend)
+        if (s_slot[row] != -2 && c0 + cl < cend)
             *reinterpret_cast<uint2 *>(a.out + (int64_t)s_tok[row] * a.ldo + obase + c0 + cl) = v;
     }
 }
@@ -502,10 +546,7 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
 // own, scales, splits into bf16 parts, and clears buf for tokens without a
-// slot.  The first block row also writes the row order of the tile GEMM: the
-// slot-sorted tokens, then the tokens without a slot in token order (their
-// rank among themselves is counted from idx; one pass over the idx before the
-// block).
+// slot.
 constexpr int kRedThreads = 256;
 struct LinReduceArgs {
     const float *part;
@@ -519,28 +560,44 @@ struct LinReduceArgs {
     int32_t *order;
 };
 
+// The row order of the tile GEMM: each slot's tokens, slots ascending, then
+// the tokens without a slot in token order.  A work-group writes 256 positions
+// of the slots' runs and places its 256 tokens without a slot, whose number
+// before it is counted from idx (a bitmap of the slots in use in LDS).
 __global__ __launch_bounds__(kRedThreads) void k_lin_order(LinReduceArgs a) {
-    __shared__ int s_cnt[kRedThreads / 64 + 1];
+    constexpr int NW = kRedThreads / 64;
+    __shared__ unsigned s_act[kMaxSlots / 32];
+    __shared__ int s_cnt[NW], s_before[NW];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int base = blockIdx.x * kRedThreads;
-    if (tid <= kRedThreads / 64) s_cnt[tid] = 0;
+    const int base = blockIdx.x * kRedThreads, t = base + tid;
+    for (int i = tid; i < kMaxSlots; i += kRedThreads) {
+        const unsigned long long b = __ballot(i < a.L && (!a.slot_rank || a.slot_rank[i] > 0));
+        if (lane == 0) {
+            s_act[i >> 5] = (unsigned)b;
+            s_act[(i >> 5) + 1] = (unsigned)(b >> 32);
+        }
+    }
     __syncthreads();
-    // tokens without a slot before this block
+    auto none = [&](int s) { return s < 0 || s >= a.L || !(s_act[s >> 5] >> (s & 31) & 1); };
     int before = 0;
-    for (int i = tid; i < base; i += kRedThreads)
-        before += slot_of_token(a.idx, a.slot_rank, a.L, i) < 0;
+#pragma unroll 4
+    for (int i = tid; i < base; i += kRedThreads) before += none(a.idx[i]);
     for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
-    if (lane == 0) atomicAdd(&s_cnt[kRedThreads / 64], before);
-    const int t = base + tid;
-    const bool none = t < a.T && slot_of_token(a.idx, a.slot_rank, a.L, t) < 0;
-    const unsigned long long b = __ballot(none);
-    if (lane == 0) s_cnt[w] = __popcll(b);
+    const bool mine = t < a.T && none(a.idx[t]);
+    const unsigned long long b = __ballot(mine);
+    if (lane == 0) {
+        s_before[w] = before;
+        s_cnt[w] = __popcll(b);
+    }
     __syncthreads();
-    int pos = a.seg.header[0] + s_cnt[kRedThreads / 64];
-    for (int i = 0; i < w; ++i) pos += s_cnt[i];
-    pos += __popcll(b & ((1ull << lane) - 1));
-    if (none) a.order[pos] = t;
-    if (t < a.seg.header[0]) a.order[t] = a.seg.perm[t];
+    const int run_end = a.seg.header[0];
+    if (mine) {
+        int pos = run_end + __popcll(b & ((1ull << lane) - 1));
+        for (int i = 0; i < NW; ++i) pos += s_before[i];
+        for (int i = 0; i < w; ++i) pos += s_cnt[i];
+        a.order[pos] = t;
+    }
+    if (t < run_end) a.order[t] = a.seg.perm[t];
 }
 
 __global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
@@ -581,7 +638,7 @@ __global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
     if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
 }
 
-template <int BM, int BN, int WM, int WN, int BK, int NST>
+template <int BM, int BN, int WM, int WN, int NST, bool MIXED>
 hipError_t run_tile(LinArgs a, bool gradient, hipStream_t st) {
     a.m_tiles = (a.T + BM - 1) / BM;
     if (gradient) {
@@ -596,8 +653,8 @@ hipError_t run_tile(LinArgs a, bool gradient, hipStream_t st) {
         a.n_tiles = c;
     }
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles)), block(WM * WN * 64);
-    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, BK, NST, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, BK, NST, false>), grid, block, 0, st, a);
+    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
     return hipGetLastError();
 }
 
@@ -621,9 +678,10 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192) return run_tile<256, 256, 2, 2, 32, 4>(a, gradient, st);
-    if (tiles(a.T, a.K, a.n, a.S, gradient, 128) >= 192) return run_tile<128, 128, 2, 2, 32, 4>(a, gradient, st);
-    return run_tile<64, 64, 2, 2, 64, 4>(a, gradient, st);
+    if (a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
+        return run_tile<256, 256, 2, 2, 2, false>(a, gradient, st);
+    if (tiles(a.T, a.K, a.n, a.S, gradient, 128) >= 192) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, st);
+    return run_tile<64, 64, 2, 2, 4, true>(a, gradient, st);
 }
 
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,

@@ -19,7 +19,7 @@ struct LinArgs {
     int64_t ldo;
     const uint16_t *hl;       // bf16 [S][T][hl_row]: scaled rank vectors' parts (the first two are used)
     int32_t hl_row;           // kLinParts* R
-    const int32_t *order;     // row position -> token, or null (identity)
+    const int32_t *order;     // row -> token, slot-sorted, or null (identity)
     const int32_t *idx;
     const int32_t *slot_rank;
     int32_t T, K, S, L, R;
@@ -47,8 +47,8 @@ hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, c
                              const int32_t *slot_rank, const float *scale, uint16_t *hl, float *buf,
                              hipStream_t st);
 // hl (`parts` parts of scale * sum; and buf, if given) from partial sums
-// [S][nsp][T][R] by slot-sorted position.  order (nullable): receives the
-// slot-sorted tokens followed by the tokens without a slot.
+// [S][nsp][T][R] by slot-sorted position.  order (nullable): receives the row
+// order of the tile GEMM.
 hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
                              const int32_t *idx, const int32_t *slot_rank, const float *scale,
                              const SegPtrs &seg, uint16_t *hl, int32_t parts, float *buf, int32_t *order,
