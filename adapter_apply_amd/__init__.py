@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from itertools import repeat
+from operator import attrgetter
 from typing import Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -562,39 +564,85 @@ def alloc_linear_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, dev
     return _aligned_ws(lora_linear_workspace_size(T, K, N, R, L), device)
 
 
+# The layer and gradient wrappers run once per layer of a step, next to kernels
+# of a few microseconds, so their checks touch each tensor attribute once.
+
+class _OnDevice:
+    """Makes `dev` (an index) the current device for a call, if it is not."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        torch = _torch()
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            _torch().cuda.set_device(self.prev)
+
+
+def _raw_stream(stream, dev):
+    """The stream handle of a call on device `dev` (its current stream)."""
+    if stream is None:
+        return _torch().cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _one_device(tensors):
+    """The index of the one GPU all tensors are on."""
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) != 1 or min(devs) < 0:
+        _need_device(tensors)
+    return devs.pop()
+
+
+def _bad_stack(ts, name, shapes, dtype):
+    raise ValueError(f"{name} must hold {len(shapes)} contiguous {dtype} tensors of shapes "
+                     f"{[list(s) for s in shapes]}; got {[(list(t.shape), t.dtype) for t in ts]}")
+
+
+def _need_stack(ts, name, shapes, dtype):
+    if len(ts) != len(shapes):
+        raise ValueError(f"{name} holds {len(ts)} tensors; expected {len(shapes)}")
+    for t, shape in zip(ts, shapes):
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _bad_stack(ts, name, shapes, dtype)
+
+
 def _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, S_cols):
     """Checks shared by the layer and its gradient; S_cols: the [T, sum N]
-    tensor (y or dy)."""
+    tensor (y or dy) and its name.  Returns T, K, L, R and the widths."""
     torch = _torch()
     bf16 = torch.bfloat16
     _rowmajor(x, "x")
     _need_dtype(x, (bf16,), "x")
     T, K = x.shape
-    _same_list(A, "A", 3, bf16)
+    if len(A) < 1 or A[0].dim() != 3 or len(A) != len(B) or any(b.dim() != 3 for b in B):
+        raise ValueError("A and B must hold one [L, R, K] and one [L, N_s, R] tensor per slice "
+                         f"(got {len(A)} and {len(B)} tensors)")
     L, R, _ = A[0].shape
-    _same_list(A, "A", 3, bf16, lambda i: (L, R, K))
-    if len(B) != len(A):
-        raise ValueError(f"A holds {len(A)} tensors but B holds {len(B)}")
-    _same_list(B, "B", 3, bf16, lambda i: (L, None, R))
-    n = sum(b.shape[1] for b in B)
+    N = [b.shape[1] for b in B]
+    _need_stack(A, "A", [(L, R, K)] * len(A), bf16)
+    _need_stack(B, "B", [(L, n, R) for n in N], bf16)
+    n = sum(N)
     t, name = S_cols
     _rowmajor(t, name)
     _need_dtype(t, (bf16,), name)
-    _need_shape(t, (T, None), name)
-    if t.shape[1] < n:
-        raise ValueError(f"{name} has {t.shape[1]} columns; the slices need {n}")
+    if t.shape[0] != T or t.shape[1] < n:
+        raise ValueError(f"{name} has shape {list(t.shape)}; expected [{T}, >= {n}]")
     if W is not None:
         _rowmajor(W, "W")
         _need_dtype(W, (bf16,), "W")
         _need_shape(W, (n, K), "W")
-    if buf is not None:
-        _need_dtype(buf, (torch.float32,), "buf")
-        _need_shape(buf, (len(A), T, R), "buf")
-        if not buf.is_contiguous():
-            raise ValueError("buf must be contiguous")
+    if buf is not None and (buf.dtype is not torch.float32 or buf.shape != (len(A), T, R) or
+                            not buf.is_contiguous()):
+        raise ValueError(f"buf must be a contiguous fp32 [{len(A)}, {T}, {R}] tensor")
     _check_meta(idx, slot_rank, scale, T, L)
     _check_ws(ws)
-    return T, K, L, R, n
+    return T, K, L, R, N
 
 
 def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bias=None, buf=None,
@@ -602,18 +650,17 @@ def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bi
     """y[:, :sum N] = x W^T + bias + scale (x A^T) B^T per slice, rounded once.
     x [T, K]; W [sum N, K]; A[s] [L, R, K]; B[s] [L, N_s, R]; bias [sum N] or
     None; all bf16.  buf [S, T, R] fp32 (optional) receives x A^T."""
-    torch = _torch()
-    T, K, L, R, n = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
+    T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
     if bias is not None:
-        _need_vec(bias, n, torch.bfloat16, "bias")
-    _need_device([y, x, W, *A, *B, idx, slot_rank, scale, buf, bias, ws])
-    N = (_i64 * len(B))(*[b.shape[1] for b in B])
-    with torch.cuda.device(x.device):
+        _need_vec(bias, sum(N), _torch().bfloat16, "bias")
+    dev = _one_device((y, x, W, *A, *B, idx, slot_rank, scale, buf, bias, ws))
+    S = len(N)
+    with _OnDevice(dev):
         _check(lib().lora_linear(_ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
-                                 W.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B), N, len(A),
-                                 L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf),
-                                 LORA_DT_BF16, flags, _ptr(ws), ws.numel() * ws.element_size(),
-                                 _stream(stream)), "lora_linear")
+                                 W.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B),
+                                 (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale),
+                                 _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes,
+                                 _raw_stream(stream, dev)), "lora_linear")
 
 
 def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
@@ -623,30 +670,28 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
     [L, R, K] and dB[s] [L, N_s, R] fp32, or None; dy [T, >= sum N].  W None:
     dx += the adapters' part.  buf: x A^T as lora_linear left it, or None."""
     torch = _torch()
-    T, K, L, R, n = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
+    T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
+    S = len(N)
     if dx is not None:
         _rowmajor(dx, "dx")
         _need_dtype(dx, (torch.bfloat16,), "dx")
         _need_shape(dx, (T, K), "dx")
-    for g, name, shape in ((dA, "dA", lambda i: (L, R, K)),
-                           (dB, "dB", lambda i: (L, B[i].shape[1], R))):
-        if g is None:
-            continue
-        if len(g) != len(A):
-            raise ValueError(f"A holds {len(A)} tensors but {name} holds {len(g)}")
-        _same_list(g, name, 3, torch.float32, shape)
-    outs = [t for t in (dx, *(dA or ()), *(dB or ())) if t is not None and t.numel()]
-    if len({t.data_ptr() for t in outs}) != len(outs):
+    if dA is not None:
+        _need_stack(dA, "dA", [(L, R, K)] * S, torch.float32)
+    if dB is not None:
+        _need_stack(dB, "dB", [(L, n, R) for n in N], torch.float32)
+    outs = [t.data_ptr() for t in (dx, *(dA or ()), *(dB or ())) if t is not None and t.numel()]
+    if len(set(outs)) != len(outs):
         raise ValueError("dx, dA and dB must be different tensors")
-    _need_device([dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws])
-    N = (_i64 * len(B))(*[b.shape[1] for b in B])
-    with torch.cuda.device(x.device):
+    dev = _one_device((dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws))
+    with _OnDevice(dev):
         _check(lib().lora_linear_backward(
             _ptr(dx), 0 if dx is None else dx.stride(0), None if dA is None else _ptr_array(dA),
             None if dB is None else _ptr_array(dB), _ptr(dy), dy.stride(0), _ptr(x), x.stride(0),
-            T, K, _ptr(W), 0 if W is None else W.stride(0), _ptr_array(A), _ptr_array(B), N,
-            len(A), L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags,
-            _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "lora_linear_backward")
+            T, K, _ptr(W), 0 if W is None else W.stride(0), _ptr_array(A), _ptr_array(B),
+            (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf),
+            LORA_DT_BF16, flags, _ptr(ws), ws.nbytes, _raw_stream(stream, dev)),
+            "lora_linear_backward")
 
 
 # ---------------------------------------------------------------------------
@@ -654,15 +699,26 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
 # ---------------------------------------------------------------------------
 
 def _check_grads(grads, name):
+    """(device index or -1, slots, elements per slot, pointers) of a list of
+    stacked tensors.  A model has hundreds of them, so every check runs over the
+    whole list at once."""
     torch = _torch()
     if len(grads) < 1:
         raise ValueError(f"{name} must hold at least one tensor")
-    dt, L = grads[0].dtype, grads[0].shape[0] if grads[0].dim() else 0
+    Tensor = torch.Tensor
+    dt = grads[0].dtype
     _need_dtype(grads[0], (torch.float32, torch.bfloat16), f"{name}[0]")
-    for i, t in enumerate(grads):
-        if t.dtype != dt or t.dim() < 1 or t.shape[0] != L or not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be a contiguous {dt} tensor stacked over {L} slots")
-    return L, [t.numel() // L if L else 0 for t in grads]
+    if 0 in map(Tensor.dim, grads):
+        raise ValueError(f"{name} must hold tensors stacked over slots")
+    L = grads[0].size(0)
+    if (set(map(attrgetter("dtype"), grads)) != {dt} or not all(map(Tensor.is_contiguous, grads)) or
+            set(map(Tensor.size, grads, repeat(0))) != {L}):
+        raise ValueError(f"{name} must hold contiguous {dt} tensors stacked over {L} slots")
+    m = (_i64 * len(grads))(*[e // L if L else 0 for e in map(Tensor.numel, grads)])
+    devs = set(map(Tensor.get_device, grads))
+    if len(devs) != 1:
+        _need_device(grads)
+    return devs.pop(), L, m, (_vp * len(grads))(*map(Tensor.data_ptr, grads))
 
 
 def lora_grad_workspace_size(m: Sequence[int], L: int) -> int:
@@ -674,35 +730,35 @@ def lora_grad_workspace_size(m: Sequence[int], L: int) -> int:
 
 def alloc_grad_workspace(grads: Sequence, device=None):
     """Workspace of lora_grad_norm over these tensors."""
-    L, m = _check_grads(grads, "grads")
+    _, L, m, _ = _check_grads(grads, "grads")
     return _aligned_ws(lora_grad_workspace_size(m, L), device or grads[0].device)
 
 
 def lora_grad_norm(norm, grads: Sequence, ws, stream=None):
     """norm [L] fp32: each slot's norm over all tensors ([L, ...], fp32 or bf16)."""
-    torch = _torch()
-    L, m = _check_grads(grads, "grads")
-    _need_vec(norm, L, torch.float32, "norm")
+    dev, L, m, ptrs = _check_grads(grads, "grads")
+    _need_vec(norm, L, _torch().float32, "norm")
     _check_ws(ws)
-    _need_device([norm, *grads, ws])
-    with torch.cuda.device(norm.device):
-        _check(lib().lora_grad_norm(_ptr(norm), _ptr_array(grads), (_i64 * len(m))(*m), len(m), L,
-                                    _dtype_code(grads[0]), _ptr(ws), ws.numel() * ws.element_size(),
-                                    _stream(stream)), "lora_grad_norm")
+    if _one_device((norm, ws)) != dev:
+        _need_device((norm, grads[0], ws))
+    with _OnDevice(dev):
+        _check(lib().lora_grad_norm(_ptr(norm), ptrs, m, len(m), L, _dtype_code(grads[0]), _ptr(ws),
+                                    ws.nbytes, _raw_stream(stream, dev)), "lora_grad_norm")
 
 
 def lora_grad_clip(out: Sequence, grads: Sequence, norm, max_norm, stream=None):
     """out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)) per slot; out[i]
     may be grads[i].  norm, max_norm [L] fp32."""
     torch = _torch()
-    L, m = _check_grads(grads, "grads")
-    Lo, mo = _check_grads(out, "out")
-    if Lo != L or mo != m or out[0].dtype != grads[0].dtype:
+    dev, L, m, ptrs = _check_grads(grads, "grads")
+    odev, Lo, mo, optrs = (dev, L, m, ptrs) if out is grads else _check_grads(out, "out")
+    if Lo != L or len(mo) != len(m) or bytes(mo) != bytes(m) or out[0].dtype != grads[0].dtype:
         raise ValueError("out must match grads in number, sizes and dtype")
     _need_vec(norm, L, torch.float32, "norm")
     _need_vec(max_norm, L, torch.float32, "max_norm")
-    _need_device([norm, max_norm, *grads, *out])
-    with torch.cuda.device(norm.device):
-        _check(lib().lora_grad_clip(_ptr_array(out), _ptr_array(grads), (_i64 * len(m))(*m), len(m),
-                                    L, _ptr(norm), _ptr(max_norm), _dtype_code(grads[0]),
-                                    _stream(stream)), "lora_grad_clip")
+    if _one_device((norm, max_norm)) != dev or odev != dev:
+        _need_device((norm, max_norm, grads[0], out[0]))
+    with _OnDevice(dev):
+        _check(lib().lora_grad_clip(optrs, ptrs, m, len(m), L, _ptr(norm), _ptr(max_norm),
+                                    _dtype_code(grads[0]), _raw_stream(stream, dev)),
+               "lora_grad_clip")

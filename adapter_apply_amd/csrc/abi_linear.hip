@@ -51,6 +51,14 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         if (wg > (size_t)kLinWgPartMax) wg = (size_t)kLinWgPartMax;
         if (4 * wg > part) part = 4 * wg;
     }
+    // the tile GEMM's K splits: at most 8, and at most kLinSplitTiles tiles of
+    // 128 x 128 sums
+    size_t cols = 0;
+    for (int s = 0; s < S; ++s) cols += (size_t)N[s];
+    if (cols < (size_t)K) cols = (size_t)K;
+    size_t sums = 8 * (size_t)T * cols;
+    if (sums > (size_t)kLinSplitTiles * 16384) sums = (size_t)kLinSplitTiles * 16384;
+    if (4 * sums > part) part = 4 * sums;
     o = align256(o + part);
     w.pad = o;
     for (int s = 0; s < S; ++s) {
@@ -141,6 +149,7 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
+    a.part = reinterpret_cast<float *>(wp + wl.part);
     a.hl = hl; a.hl_row = kLinPartsFwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
     a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) {
@@ -257,6 +266,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         a.p = p; a.ldp = ldp;
         a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
         a.out = static_cast<uint16_t *>(dx); a.ldo = lddx;
+        a.part = part;
         a.hl = hl_v; a.hl_row = kLinPartsBwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
         a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
         a.accumulate = W == nullptr;

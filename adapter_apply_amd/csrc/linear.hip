@@ -121,17 +121,23 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         }
     }
     __syncthreads();
-    const int n_slots = __builtin_amdgcn_readfirstlane(s_n);
+    const int n_slots = MIXED && blockIdx.y + 1 < gridDim.y ? 0 : __builtin_amdgcn_readfirstlane(s_n);
     if (a.accumulate && !s_any) return;
 
     // K tiles: the projection's (per slice in the gradient), then per slot
     // (and slice) the [high | low] rank vectors.
-    int nk = 0;
+    int nk = 0, k0 = 0;
     if (a.w) {
         if (NN)
             for (int s = 0; s < a.S; ++s) nk += (int)((a.n[s] + BK - 1) / BK);
         else
             nk = (a.K + BK - 1) / BK;
+        // MIXED: this split's share of them (the last takes the rank vectors')
+        if (MIXED) {
+            const int per = (nk + a.ksp - 1) / a.ksp;
+            k0 = min((int)blockIdx.y * per, nk);
+            nk = min(per, nk - k0);
+        }
     }
     const int lc_per = (2 * a.R + BK - 1) / BK;   // K tiles per rank vector
     const int per_slot = lc_per * (NN ? a.S : 1);
@@ -181,6 +187,13 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         }
     };
     auto advance = [&]() { rem -= BK; po += BK; qo += qstep; };
+    if (MIXED && k0) {
+        if (NN)
+            for (; (int64_t)k0 * BK >= a.n[cs]; ++cs) k0 -= (int)((a.n[cs] + BK - 1) / BK);
+        rem = (NN ? a.n[cs] : a.K) - (int64_t)k0 * BK;
+        po = (NN ? a.poff[cs] : 0) + (int64_t)k0 * BK;
+        qo = NN ? (a.off[cs] + (int64_t)k0 * BK) * a.ldw : (int64_t)k0 * BK;
+    }
     auto issue = [&](int v, int stage) {
         // recomputed here each time: hoisted lane values would crowd the
         // registers of the fast loop
@@ -407,8 +420,22 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         }
     }
 
-    // One rounding per output element.
+    // One rounding per output element; a split leaves its fp32 sums by row.
     const int64_t obase = NN ? 0 : a.off[sc];
+    if (MIXED && a.ksp > 1) {
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+            const int row = (wm * MB + j) * 16 + l16;
+            if (m0 + row >= a.T) continue;
+            float *o = a.part + ((int64_t)blockIdx.y * a.T + m0 + row) * a.part_ld + obase;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int64_t c = c0 + (wn * NB + i) * 16 + 4 * g;
+                if (c < cend) *reinterpret_cast<floatx4_t *>(o + c) = acc[i][j];
+            }
+        }
+        return;
+    }
     if (NN && a.accumulate) {
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
@@ -480,6 +507,7 @@ struct LinShrinkArgs {
 };
 
 __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
+    constexpr int U = 8;                      // steps in flight: K <= 4096 is one round of loads
     __shared__ floatx4_t s_sum[kShWaves][64];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
@@ -489,8 +517,9 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     const int mine = t < a.T ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -2;
     // lanes 0..15 that name a slot first; the y-th of them is this group's slot
     bool lead = mine >= 0 && lane < 16;
+#pragma unroll
     for (int o = 0; o < 15; ++o) {
-        const int other = __shfl(mine, o);
+        const int other = __builtin_amdgcn_readlane(mine, o);
         if (o < lane && other == mine) lead = false;
     }
     unsigned long long leads = __ballot(lead);
@@ -501,24 +530,33 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     }
     if ((int)blockIdx.y >= __popcll(leads)) return;
     for (unsigned y = 0; y < blockIdx.y; ++y) leads &= leads - 1;
-    const int slot = __builtin_amdgcn_readfirstlane(__shfl(mine, __ffsll(leads) - 1));
-    const int r = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    const int slot = __builtin_amdgcn_readlane(mine, __ffsll(leads) - 1);
 
     const uint16_t *xr = a.x + (int64_t)min(t, a.T - 1) * a.ldx;
     const uint16_t *ar = a.a[s] + ((int64_t)slot * a.R + min(j0 + l16, a.R - 1)) * a.K;
+    const int r = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    const float sc = a.scale[slot];
     floatx4_t acc = {0.f, 0.f, 0.f, 0.f};
     const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int kb = w * 64; kb < a.K; kb += kShWaves * 64) {
+    for (int kb = w * 64; kb < a.K; kb += U * kShWaves * 64) {
+        uint4 xv[U][2], av[U][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = kb + h * 32 + g * 8;
-            const bool in = k < a.K;
-            const int kc = in ? k : 0;
-            uint4 xa = ldg<uint4>(xr + kc), aa = ldg<uint4>(ar + kc);
-            if (!in) { xa = z; aa = z; }
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(aa), frag(xa), acc, 0, 0, 0);
-        }
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kb + u * kShWaves * 64 + h * 32 + g * 8, kc = k < a.K ? k : 0;
+                xv[u][h] = ldg<uint4>(xr + kc);
+                av[u][h] = ldg<uint4>(ar + kc);
+            }
+        __builtin_amdgcn_sched_barrier(0);        // every load of the round in flight
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = kb + u * kShWaves * 64 + h * 32 + g * 8 < a.K;
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? av[u][h] : z), frag(in ? xv[u][h] : z), acc,
+                                                             0, 0, 0);
+            }
     }
     s_sum[w][lane] = acc;
     __syncthreads();
@@ -531,7 +569,6 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     }
     const int j = j0 + 4 * g;
     if (mine != slot || j >= a.R) return;
-    const float sc = a.scale[slot];
     const int64_t row = (int64_t)s * a.T + t;
     float v[4];
 #pragma unroll
@@ -541,6 +578,124 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     }
     store_parts(a.hl + row * kLinPartsFwd * a.R, kLinPartsFwd, a.R, j, v);
     if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
+}
+
+// A few tokens (decode): work-group = 16 * CT output columns, 16 * TB tokens
+// (all of them), 8 waves each taking every eighth 64-column step of K straight
+// from global memory into 16x16x32 MFMA fragments -- W is read once, 64 bytes
+// of 16 rows per load, with U steps in flight.  The waves' sums are added in
+// order through LDS; then each thread adds the delta of one token and 4
+// columns from the rank vector's parts (fp32 FMAs, so slots stay apart).
+constexpr int kFewWaves = 8;
+template <int TB, int CT, int U>
+__global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
+    __shared__ floatx4_t s_sum[kFewWaves][CT * TB][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int l16 = lane & 15, g = lane >> 4;
+    int sc = 0;
+    while (sc + 1 < a.S && (int)blockIdx.x >= a.tile_start[sc + 1]) ++sc;
+    const int64_t c0 = (int64_t)(blockIdx.x - a.tile_start[sc]) * (16 * CT), cend = a.n[sc];
+
+    const uint16_t *xr[TB], *wr[CT];
+#pragma unroll
+    for (int i = 0; i < TB; ++i) xr[i] = a.p + (int64_t)min(i * 16 + l16, a.T - 1) * a.ldp;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) wr[i] = a.w + (a.off[sc] + min(c0 + i * 16 + l16, cend - 1)) * a.ldw;
+    floatx4_t acc[CT][TB];
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    for (int kb = w * 64; kb < a.K; kb += U * kFewWaves * 64) {
+        uint4 wv[U][2][CT], xv[U][2][TB];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kb + u * kFewWaves * 64 + h * 32 + g * 8, kc = k < a.K ? k : 0;
+#pragma unroll
+                for (int i = 0; i < CT; ++i) wv[u][h][i] = ldg<uint4>(wr[i] + kc);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) xv[u][h][j] = ldg<uint4>(xr[j] + kc);
+            }
+        __builtin_amdgcn_sched_barrier(0);        // every load of the round in flight
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = kb + u * kFewWaves * 64 + h * 32 + g * 8 < a.K;
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+#pragma unroll
+                    for (int j = 0; j < TB; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            frag(in ? wv[u][h][i] : z), frag(in ? xv[u][h][j] : z), acc[i][j], 0, 0, 0);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) s_sum[w][i * TB + j][lane] = acc[i][j];
+    __syncthreads();
+    if (w >= CT * TB) return;                     // wave w: column block w / TB, token block w % TB
+    floatx4_t r = s_sum[0][w][lane];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) {
+        const floatx4_t o = s_sum[i][w][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] += o[e];
+    }
+    const int t = (w % TB) * 16 + l16;
+    const int64_t c = c0 + (w / TB) * 16 + 4 * g;
+    if (t >= a.T || c >= cend) return;
+    const int64_t col = a.off[sc] + c;
+    if (a.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] += bf16_to_f32(a.bias[col + e]);
+    }
+    const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
+    if (slot >= 0) {
+        const uint16_t *hl = a.hl + ((int64_t)sc * a.T + t) * a.hl_row;
+        const uint16_t *b = a.lora[sc] + ((int64_t)slot * cend + c) * a.R;
+#pragma unroll 2
+        for (int j = 0; j < a.R; j += 8) {
+            const uint4 h = ldg<uint4>(hl + j), l = ldg<uint4>(hl + a.R + j);
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint4 v = ldg<uint4>(b + (int64_t)e * a.R + j);
+                const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    r[e] += (bf16_lo(hw[q]) + bf16_lo(lw[q])) * bf16_lo(bw[q]);
+                    r[e] += (bf16_hi(hw[q]) + bf16_hi(lw[q])) * bf16_hi(bw[q]);
+                }
+            }
+        }
+    }
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ldo + col) =
+        make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+}
+
+// The K splits of a tile GEMM, summed in order, bias added, rounded once.
+__global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int64_t cols) {
+    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, per = cols / 4;
+    const int64_t m = q / per, c = (q - m * per) * 4;
+    if (m >= a.T) return;
+    floatx4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < a.ksp; ++k) {
+        const floatx4_t o = *reinterpret_cast<const floatx4_t *>(a.part + ((int64_t)k * a.T + m) * a.part_ld + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += o[e];
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(a.bias[c + e]);
+    }
+    const int64_t t = a.order ? a.order[m] : m;
+    *reinterpret_cast<uint2 *>(a.out + t * a.ldo + c) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
@@ -638,23 +793,42 @@ __global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
     if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
 }
 
-template <int BM, int BN, int WM, int WN, int NST, bool MIXED>
-hipError_t run_tile(LinArgs a, bool gradient, hipStream_t st) {
-    a.m_tiles = (a.T + BM - 1) / BM;
-    if (gradient) {
-        a.n_tiles = (a.K + BN - 1) / BN;
-    } else {
-        int c = 0;
-        for (int s = 0; s < a.S; ++s) {
-            a.tile_start[s] = c;
-            c += (int)((a.n[s] + BN - 1) / BN);
-        }
-        for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
-        a.n_tiles = c;
+// Column tiles of width b by slice; returns their number.
+int column_tiles(LinArgs &a, int b) {
+    int c = 0;
+    for (int s = 0; s < a.S; ++s) {
+        a.tile_start[s] = c;
+        c += (int)((a.n[s] + b - 1) / b);
     }
-    const dim3 grid((unsigned)(a.m_tiles * a.n_tiles)), block(WM * WN * 64);
+    for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
+    return c;
+}
+
+template <int BM, int BN, int WM, int WN, int NST, bool MIXED>
+hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
+    a.m_tiles = (a.T + BM - 1) / BM;
+    a.n_tiles = gradient ? (a.K + BN - 1) / BN : column_tiles(a, BN);
+    a.ksp = ksp;
+    int64_t cols = a.K;
+    if (!gradient) {
+        cols = 0;
+        for (int s = 0; s < a.S; ++s) cols += a.n[s];
+    }
+    a.part_ld = cols;
+    const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
     if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || ksp == 1) return e;
+    const int64_t units = (int64_t)a.T * (cols / 4);
+    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, st, a, cols);
+    return hipGetLastError();
+}
+
+template <int TB, int CT, int U>
+hipError_t run_few(LinArgs a, hipStream_t st) {
+    const int n = column_tiles(a, 16 * CT);
+    hipLaunchKernelGGL((k_lin_few<TB, CT, U>), dim3((unsigned)n), dim3(kFewWaves * 64), 0, st, a);
     return hipGetLastError();
 }
 
@@ -668,7 +842,7 @@ int64_t tiles(int32_t T, int32_t K, const int64_t *N, int32_t S, bool gradient, 
 
 }  // namespace
 
-// A launch's threads stay under 2^32: tile work-groups of 512 threads, and
+// A launch's threads stay under 2^32: tile work-groups of 256 threads, and
 // column tiles times rank blocks of the weight gradients.
 bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
     for (int s = 0; s < S; ++s)
@@ -678,10 +852,32 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
+    if (!gradient && a.T <= kLinFewTokens) {
+        if (a.T <= 16) return run_few<1, 1, 8>(a, st);
+        if (a.T <= 32) return run_few<2, 2, 4>(a, st);
+        return run_few<4, 2, 2>(a, st);
+    }
     if (a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
-        return run_tile<256, 256, 2, 2, 2, false>(a, gradient, st);
-    if (tiles(a.T, a.K, a.n, a.S, gradient, 128) >= 192) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, st);
-    return run_tile<64, 64, 2, 2, 4, true>(a, gradient, st);
+        return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
+    // Few tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
+    // each), joined by a second launch.
+    int64_t nk = (a.K + 63) / 64;
+    if (gradient) {
+        nk = 0;
+        for (int s = 0; s < a.S; ++s) nk += (a.n[s] + 63) / 64;
+    }
+    if (!a.w) nk = 0;
+    auto splits = [&](int64_t t) {
+        int64_t k = kLinSplitTiles / t;
+        if (k > nk / 8) k = nk / 8;
+        if (k > 8) k = 8;
+        return (int)(k < 1 ? 1 : k);
+    };
+    const int64_t t128 = tiles(a.T, a.K, a.n, a.S, gradient, 128), t64 = tiles(a.T, a.K, a.n, a.S, gradient, 64);
+    if (t128 >= 192) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, 1, st);
+    if (t128 * splits(t128) >= kLinSplitTiles / 2)
+        return run_tile<128, 128, 2, 2, 2, true>(a, gradient, splits(t128), st);
+    return run_tile<64, 64, 2, 2, 4, true>(a, gradient, splits(t64), st);
 }
 
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,

@@ -25,6 +25,9 @@ struct LinArgs {
     int32_t T, K, S, L, R;
     int32_t accumulate;       // out += delta (no base product); rows without a slot untouched
     int32_t m_tiles, n_tiles;
+    int32_t ksp;              // K splits; more than one: fp32 sums to part [ksp][T][part_ld]
+    float *part;
+    int64_t part_ld;
     const uint16_t *lora[kMaxSlices];   // forward: lora_b [L][N_s][R]; gradient: lora_a [L][R][K]
     int64_t n[kMaxSlices];              // N_s
     int64_t off[kMaxSlices];            // first row of slice s in w (first column in out)
@@ -33,6 +36,8 @@ struct LinArgs {
 };
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
+constexpr int kLinFewTokens = 64;       // forward batches of at most this many tokens: k_lin_few
+constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits (k T cols <= this * 128^2)
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
 constexpr int kLinPartsFwd = 2;
