@@ -40,6 +40,11 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     size_t part = 4 * tsr;
     const size_t split = (size_t)K * ((size_t)T + (size_t)(T < L ? T : L) * S * R) / 8;
     if (split > part) part = split;
+    // the grouped shrink's chunks of 512 columns (direct batches)
+    size_t kc = ((size_t)K + 511) / 512;
+    if (kc > (size_t)kMaxKcGrp) kc = (size_t)kMaxKcGrp;
+    const size_t gt = T < kLinDirectTokens ? T : kLinDirectTokens;
+    if (4 * gt * S * R * kc > part) part = 4 * gt * S * R * kc;
     // the gradient's column splits: k tiles S <= 1024 with at least T / 64
     // tiles, and at most 16, so k T <= min(16 T, T + 65536)
     size_t kt = (size_t)T + 65536;
@@ -51,8 +56,8 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         if (wg > (size_t)kLinWgPartMax) wg = (size_t)kLinWgPartMax;
         if (4 * wg > part) part = 4 * wg;
     }
-    // the tile GEMM's K splits: at most 8, and at most kLinSplitTiles tiles of
-    // 128 x 128 sums
+    // the tile GEMM's sums: K splits (at most 8) of at most kLinSplitTiles tiles
+    // of 128 x 128, or one sum of a direct batch (T N <= kLinDirectBytes / 16)
     size_t cols = 0;
     for (int s = 0; s < S; ++s) cols += (size_t)N[s];
     if (cols < (size_t)K) cols = (size_t)K;
@@ -85,6 +90,13 @@ SegPtrs lin_seg(void *ws, size_t ws_bytes, const LinWs &w, int32_t T, int32_t L)
     SegPtrs seg = seg_ptrs(ws, w.seg);
     attach_seg_x(seg, ws, ws_bytes, T, L, 0, w.end - seg_x_bytes(T, L) - 256);
     return seg;
+}
+
+// Direct batches whose rank vectors the slot-grouped kernels find (more than
+// one launch of k_lin_few takes, whole 64-column steps, in-kernel discovery).
+bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L) {
+    return T > kLinFewTokens && grp_discovers(T, L) && R % 16 == 0 && R <= kGrpMaxPartialRank && K % 64 == 0 &&
+           grp_kchunks(K) <= kMaxKcGrp;
 }
 
 // x A^T by slot-sorted position in the workspace's partial sums; returns the
@@ -132,8 +144,19 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     const Slices sl = make_slices(A, B, N, S, 0);
     uint16_t *hl = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
     int32_t *order = nullptr;
-    if (T <= kLinShrinkTokens) {
-        CHECK(launched(launch_lin_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, scale, hl, buf, st)));
+    const bool direct = lin_direct(T, K, N, S, R, L);
+    float *u = buf, *clear = nullptr;
+    if (direct) {
+        // fp32 rank vectors by token, in buf if it is wanted
+        if (!u) u = reinterpret_cast<float *>(wp + wl.hl_u);
+        if (lin_grouped(T, K, R, L)) {
+            float *part = reinterpret_cast<float *>(wp + wl.part);
+            CHECK(launched(launch_grp_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, part, nullptr, nullptr, st)));
+            CHECK(launched(launch_grp_reduce(T, S, L, R, idx, slot_rank, part, grp_kchunks(K), u, nullptr, st)));
+            clear = buf;
+        } else {
+            CHECK(launched(launch_lin_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, u, st)));
+        }
     } else {
         const SegPtrs seg = lin_seg(ws, ws_bytes, wl, T, L);
         float *part = reinterpret_cast<float *>(wp + wl.part);
@@ -150,6 +173,8 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
     a.part = reinterpret_cast<float *>(wp + wl.part);
+    a.join_delta = direct;
+    a.u = u; a.scale = scale; a.clear = clear;
     a.hl = hl; a.hl_row = kLinPartsFwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
     a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) {

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     static_assert(PI >= 1 && QI >= 1 && NW % 2 == 0, "whole DMA instructions per wave");
     static_assert(BM * BN * 2 <= NST * (PB + QB), "the output tile fits the stages");
     __shared__ __attribute__((aligned(16))) char s_stage[NST * (PB + QB)];
-    __shared__ int s_tok[BM], s_slot[BM], s_list[BM], s_whole[BM / 16], s_n, s_any;
+    __shared__ int s_tok[BM], s_slot[BM], s_list[BM + 1], s_r8[BM + 1], s_whole[BM / 16], s_n, s_nt, s_any;
     __shared__ unsigned s_bits[32];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         const int m = m0 + i;
         const int pos = min(m, a.T - 1);
         const int t = a.order ? a.order[pos] : pos;
-        const int sl = m < a.T ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -2;
+        const int sl = m >= a.T ? -2 : MIXED && a.join_delta ? -1 : slot_of_token(a.idx, a.slot_rank, a.L, t);
         s_tok[i] = t;
         s_slot[i] = sl;
         // MIXED: every slot; else the slots that have a 16-token block of their own
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         if (sl >= 0) s_any = 1;
     }
     __syncthreads();
-    if (tid < 64) {
+    if (tid < 64 && !(MIXED && a.join_delta)) {
         // the tile's slots, ascending
         const unsigned b = tid < 32 ? s_bits[tid] : 0u;
         int c = __popc(b), inc = c;
@@ -112,17 +112,27 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         }
         if (tid == 31) s_n = inc;
         if (tid < 32) {
+            // with each its rank in whole 16-byte units and the K tiles of its
+            // [high | low] rank vector
+            int nt = 0;
             unsigned bb = b;
             for (int k = inc - c; bb; ++k) {
-                const int bit = __ffs(bb) - 1;
-                s_list[k] = tid * 32 + bit;
+                const int s = tid * 32 + __ffs(bb) - 1;
+                const int r8 = ((a.slot_rank ? min(a.slot_rank[s], a.R) : a.R) + 7) & ~7;
+                s_list[k] = s;
+                s_r8[k] = r8;
+                nt += (2 * r8 + BK - 1) / BK;
                 bb &= bb - 1;
             }
+            for (int d = 16; d; d >>= 1) nt += __shfl_xor(nt, d, 32);
+            if (tid == 0) s_nt = nt;
         }
     }
     __syncthreads();
-    const int n_slots = MIXED && blockIdx.y + 1 < gridDim.y ? 0 : __builtin_amdgcn_readfirstlane(s_n);
     if (a.accumulate && !s_any) return;
+    // (delta in the join, or in the last split)
+    const bool no_delta = MIXED && (a.join_delta || blockIdx.y + 1 < gridDim.y);
+    const int n_lt = no_delta ? 0 : __builtin_amdgcn_readfirstlane(s_nt) * (NN ? a.S : 1);
 
     // K tiles: the projection's (per slice in the gradient), then per slot
     // (and slice) the [high | low] rank vectors.
@@ -139,9 +149,18 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
             nk = min(per, nk - k0);
         }
     }
-    const int lc_per = (2 * a.R + BK - 1) / BK;   // K tiles per rank vector
-    const int per_slot = lc_per * (NN ? a.S : 1);
-    const int nv = nk + n_slots * per_slot;
+    const int nv = nk + n_lt;
+    // the rank-vector tile to load or to use next: slot, slice, tile inside it
+    struct Cursor { int d, s, c; };
+    const int s_first = NN ? 0 : sc, s_last = NN ? a.S - 1 : sc;
+    auto step = [&](Cursor &u) {
+        if (++u.c < (2 * __builtin_amdgcn_readfirstlane(s_r8[u.d]) + BK - 1) / BK) return;
+        u.c = 0;
+        if (++u.s <= s_last) return;
+        u.s = s_first;
+        ++u.d;
+    };
+    Cursor ld = {0, s_first, 0}, use = {0, s_first, 0};
 
     // DMA lanes: fixed rows, global units XOR-ed.
     auto pswz = [](int row) { return (row >> 1) & 7; };
@@ -215,18 +234,17 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
             advance();
             return;
         }
-        const int u = v - nk, d = u / per_slot, x = u - d * per_slot;
-        const int s = NN ? x / lc_per : sc, c = x % lc_per;
-        const int slot = __builtin_amdgcn_readfirstlane(s_list[d]);
-        const int R = a.R;
+        const int s = ld.s, c = ld.c, R = a.R;
+        const int slot = __builtin_amdgcn_readfirstlane(s_list[ld.d]), r8 = __builtin_amdgcn_readfirstlane(s_r8[ld.d]);
+        step(ld);
         const int pj = c * BK + plc * 8;
         const uint16_t *hl = a.hl + (int64_t)s * a.T * a.hl_row;
 #pragma unroll
         for (int i = 0; i < PI; ++i) {
             const int row = prow0 + i * (NW * 64 / UP);
-            const bool in = s_slot[row] == slot && pj < 2 * R;
+            const bool in = s_slot[row] == slot && pj < 2 * r8;
             dma16(pl + i * NW * 1024,
-                  in ? (const void *)(hl + (int64_t)s_tok[row] * a.hl_row + pj) : zero);
+                  in ? (const void *)(hl + (int64_t)s_tok[row] * a.hl_row + (pj < r8 ? pj : pj - r8 + R)) : zero);
         }
         const uint16_t *lo = a.lora[s];
 #pragma unroll
@@ -235,12 +253,12 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
             if (NN) {
                 const int j2 = c * BK + qrow(i);
                 const int64_t col = c0 + qlc(i) * 8;
-                if (j2 < 2 * R)
-                    src = lo + ((int64_t)slot * R + (j2 < R ? j2 : j2 - R)) * a.K + (col < cend ? col : 0);
+                if (j2 < 2 * r8)
+                    src = lo + ((int64_t)slot * R + (j2 < r8 ? j2 : j2 - r8)) * a.K + (col < cend ? col : 0);
             } else {
                 const int j2 = c * BK + qlc(i) * 8;
                 const int64_t n = min(c0 + qrow(i), cend - 1);
-                if (j2 < 2 * R) src = lo + ((int64_t)slot * cend + n) * R + (j2 < R ? j2 : j2 - R);
+                if (j2 < 2 * r8) src = lo + ((int64_t)slot * cend + n) * R + (j2 < r8 ? j2 : j2 - r8);
             }
             dma16(ql + i * NW * 1024, src);
         }
@@ -335,7 +353,8 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         // Any other tile, without the pipelined fragments.
         const char *st = stage_ptr(v);
         const bool base = v < nk;
-        const int slot = base ? 0 : __builtin_amdgcn_readfirstlane(s_list[(v - nk) / per_slot]);
+        const int slot = base ? 0 : __builtin_amdgcn_readfirstlane(s_list[use.d]);
+        if (!base) step(use);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             bf16x8_t q[NB];
@@ -422,7 +441,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
 
     // One rounding per output element; a split leaves its fp32 sums by row.
     const int64_t obase = NN ? 0 : a.off[sc];
-    if (MIXED && a.ksp > 1) {
+    if (MIXED && a.part) {
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
             const int row = (wm * MB + j) * 16 + l16;
@@ -501,13 +520,12 @@ struct LinShrinkArgs {
     int32_t T, K, S, L, R;
     const uint16_t *a[kMaxSlices];
     const int32_t *idx, *slot_rank;
-    const float *scale;
-    uint16_t *hl;
     float *buf;
 };
 
+// U: steps in flight (8: K <= 4096 is one round of loads).
+template <int U>
 __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
-    constexpr int U = 8;                      // steps in flight: K <= 4096 is one round of loads
     __shared__ floatx4_t s_sum[kShWaves][64];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
@@ -523,7 +541,7 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
         if (o < lane && other == mine) lead = false;
     }
     unsigned long long leads = __ballot(lead);
-    if (blockIdx.y == 0 && a.buf && tid < 256) {
+    if (blockIdx.y == 0 && tid < 256) {
         const int tt = tid >> 4, jj = j0 + (tid & 15);
         const int sl = __shfl(mine, tt);
         if (sl == -1 && jj < a.R) a.buf[((int64_t)s * a.T + t0 + tt) * a.R + jj] = 0.f;
@@ -535,7 +553,6 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     const uint16_t *xr = a.x + (int64_t)min(t, a.T - 1) * a.ldx;
     const uint16_t *ar = a.a[s] + ((int64_t)slot * a.R + min(j0 + l16, a.R - 1)) * a.K;
     const int r = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
-    const float sc = a.scale[slot];
     floatx4_t acc = {0.f, 0.f, 0.f, 0.f};
     const uint4 z = make_uint4(0, 0, 0, 0);
     for (int kb = w * 64; kb < a.K; kb += U * kShWaves * 64) {
@@ -569,15 +586,36 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
     }
     const int j = j0 + 4 * g;
     if (mine != slot || j >= a.R) return;
-    const int64_t row = (int64_t)s * a.T + t;
-    float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4; ++e)
         if (j + e >= r) sum[e] = 0.f;
-        v[e] = j + e < r ? sc * sum[e] : 0.f;
+    *reinterpret_cast<floatx4_t *>(a.buf + ((int64_t)s * a.T + t) * a.R + j) = sum;
+}
+
+// r += the delta of one token's 4 columns of slice s, whose lora_b rows start at
+// b: fp32 FMAs with the rank vector (a slot's rows meet its own tokens only).
+__device__ __forceinline__ void add_delta(floatx4_t &r, const LinArgs &a, const uint16_t *b, int s, int t, int slot) {
+    const float *u = a.u + ((int64_t)s * a.T + t) * a.R;
+    const int rank = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    const float sc = a.scale[slot];
+    floatx4_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int j = 0; j < rank; j += 8) {
+        const floatx4_t u0 = ldg<floatx4_t>(u + j), u1 = ldg<floatx4_t>(u + j + 4);
+        const float v[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint4 w = ldg<uint4>(b + (int64_t)e * a.R + j);
+            const uint32_t bw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                d[e] += v[2 * q] * bf16_lo(bw[q]);
+                d[e] += v[2 * q + 1] * bf16_hi(bw[q]);
+            }
+        }
     }
-    store_parts(a.hl + row * kLinPartsFwd * a.R, kLinPartsFwd, a.R, j, v);
-    if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] += sc * d[e];
 }
 
 // A few tokens (decode): work-group = 16 * CT output columns, 16 * TB tokens
@@ -585,7 +623,7 @@ __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
 // from global memory into 16x16x32 MFMA fragments -- W is read once, 64 bytes
 // of 16 rows per load, with U steps in flight.  The waves' sums are added in
 // order through LDS; then each thread adds the delta of one token and 4
-// columns from the rank vector's parts (fp32 FMAs, so slots stay apart).
+// columns.
 constexpr int kFewWaves = 8;
 template <int TB, int CT, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
@@ -655,34 +693,24 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
         for (int e = 0; e < 4; ++e) r[e] += bf16_to_f32(a.bias[col + e]);
     }
     const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
-    if (slot >= 0) {
-        const uint16_t *hl = a.hl + ((int64_t)sc * a.T + t) * a.hl_row;
-        const uint16_t *b = a.lora[sc] + ((int64_t)slot * cend + c) * a.R;
-#pragma unroll 2
-        for (int j = 0; j < a.R; j += 8) {
-            const uint4 h = ldg<uint4>(hl + j), l = ldg<uint4>(hl + a.R + j);
-            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4 v = ldg<uint4>(b + (int64_t)e * a.R + j);
-                const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    r[e] += (bf16_lo(hw[q]) + bf16_lo(lw[q])) * bf16_lo(bw[q]);
-                    r[e] += (bf16_hi(hw[q]) + bf16_hi(lw[q])) * bf16_hi(bw[q]);
-                }
-            }
-        }
-    }
+    if (slot >= 0) add_delta(r, a, a.lora[sc] + ((int64_t)slot * cend + c) * a.R, sc, t, slot);
     *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ldo + col) =
         make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
 }
 
-// The K splits of a tile GEMM, summed in order, bias added, rounded once.
-__global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int64_t cols) {
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, per = cols / 4;
-    const int64_t m = q / per, c = (q - m * per) * 4;
-    if (m >= a.T) return;
+// The K splits of a tile GEMM, summed in order, bias (and with join_delta the
+// forward's delta) added, rounded once.
+__global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
+    const int m = blockIdx.y;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int t = a.order ? a.order[m] : m;
+    const int slot = a.join_delta ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -1;
+    if (a.clear && slot < 0 && blockIdx.x == 0) {
+        // the rank vectors of a token without a slot, which the grouped shrink leaves
+        for (int s = 0; s < a.S; ++s)
+            for (int j = threadIdx.x; j < a.R; j += 256) a.clear[((int64_t)s * a.T + t) * a.R + j] = 0.f;
+    }
+    if (c >= a.part_ld) return;
     floatx4_t v = {0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < a.ksp; ++k) {
         const floatx4_t o = *reinterpret_cast<const floatx4_t *>(a.part + ((int64_t)k * a.T + m) * a.part_ld + c);
@@ -693,8 +721,23 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int64_t cols) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(a.bias[c + e]);
     }
-    const int64_t t = a.order ? a.order[m] : m;
-    *reinterpret_cast<uint2 *>(a.out + t * a.ldo + c) =
+    if (slot >= 0) {
+        // the column's slice by selects (an index that differs between lanes
+        // would load the arguments from memory, one after the other)
+        int s = 0;
+        int64_t o = 0, n = a.n[0];
+        const uint16_t *lora = a.lora[0];
+#pragma unroll
+        for (int i = 1; i < kMaxSlices; ++i)
+            if (i < a.S && c >= a.off[i]) {
+                s = i;
+                o = a.off[i];
+                n = a.n[i];
+                lora = a.lora[i];
+            }
+        add_delta(v, a, lora + ((int64_t)slot * n + c - o) * a.R, s, t, slot);
+    }
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ldo + c) =
         make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
@@ -815,13 +858,13 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
         for (int s = 0; s < a.S; ++s) cols += a.n[s];
     }
     a.part_ld = cols;
+    if (ksp == 1 && !a.join_delta) a.part = nullptr;
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
     if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || ksp == 1) return e;
-    const int64_t units = (int64_t)a.T * (cols / 4);
-    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, st, a, cols);
+    if (e != hipSuccess || !a.part) return e;
+    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + 1023) / 1024), (unsigned)a.T), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -857,7 +900,7 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
         return run_few<4, 2, 2>(a, st);
     }
-    if (a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
+    if (a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)   // (not with join_delta)
         return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
     // Few tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
     // each), joined by a second launch.
@@ -880,18 +923,34 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     return run_tile<64, 64, 2, 2, 4, true>(a, gradient, splits(t64), st);
 }
 
+// Whether a forward batch takes the direct path: rank vectors by k_lin_shrink
+// (no segment build) and the delta in k_lin_few or the join.  Both read their
+// lora rows once per token block or token, so their bytes bound it: past
+// kLinDirectBytes either the segment build and the tiles' own rank-vector K
+// tiles are the faster.
+bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    if (T <= kLinFewTokens) return true;
+    if (T > kLinDirectTokens) return false;
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) n += N[s];
+    const int64_t slots = L < 16 ? L : 16, blocks = (T + 15) / 16, ranks = (int64_t)S * ((R + 15) / 16);
+    return blocks * slots * ranks * K * 64 <= kLinDirectBytes && (int64_t)T * n * R * 2 <= kLinDirectBytes;
+}
+
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,
-                             const int32_t *slot_rank, const float *scale, uint16_t *hl, float *buf,
-                             hipStream_t st) {
+                             const int32_t *slot_rank, float *buf, hipStream_t st) {
     LinShrinkArgs a{};
     a.x = static_cast<const uint16_t *>(x); a.ldx = ldx; a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) a.a[s] = static_cast<const uint16_t *>(sl.a[s]);
-    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.hl = hl; a.buf = buf;
+    a.idx = idx; a.slot_rank = slot_rank; a.buf = buf;
     int y = L < 16 ? L : 16;
     if (y > T) y = T;
     const dim3 grid((unsigned)((T + 15) / 16), (unsigned)y, (unsigned)(S * ((R + 15) / 16)));
-    hipLaunchKernelGGL(k_lin_shrink, grid, dim3(kShWaves * 64), 0, st, a);
+    // one token block leaves most of the card idle: all of K in flight; many
+    // blocks share a CU better with half the registers
+    if (T <= 16 && K > 2048) hipLaunchKernelGGL(k_lin_shrink<8>, grid, dim3(kShWaves * 64), 0, st, a);
+    else hipLaunchKernelGGL(k_lin_shrink<4>, grid, dim3(kShWaves * 64), 0, st, a);
     return hipGetLastError();
 }
 

@@ -25,7 +25,11 @@ struct LinArgs {
     int32_t T, K, S, L, R;
     int32_t accumulate;       // out += delta (no base product); rows without a slot untouched
     int32_t m_tiles, n_tiles;
-    int32_t ksp;              // K splits; more than one: fp32 sums to part [ksp][T][part_ld]
+    int32_t ksp;              // K splits; with part, fp32 sums go to part [ksp][T][part_ld]
+    int32_t join_delta;       // the join adds the delta (direct path), not the tiles
+    const float *u;           // direct path: fp32 rank vectors [S][T][R]
+    const float *scale;
+    float *clear;             // join: u rows of tokens without a slot to clear, or null
     float *part;
     int64_t part_ld;
     const uint16_t *lora[kMaxSlices];   // forward: lora_b [L][N_s][R]; gradient: lora_a [L][R][K]
@@ -45,12 +49,13 @@ constexpr int kLinPartsBwd = 3;
 // Whether the sizes stay within what one launch's grid takes.
 bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
 
-// Rank vectors of up to kLinShrinkTokens tokens in one launch, no segments.
-constexpr int kLinShrinkTokens = 256;
+// The direct path: rank vectors in one launch without segments.
+constexpr int kLinDirectTokens = 1024;
+constexpr int64_t kLinDirectBytes = 128 << 20;
+bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,
-                             const int32_t *slot_rank, const float *scale, uint16_t *hl, float *buf,
-                             hipStream_t st);
+                             const int32_t *slot_rank, float *buf, hipStream_t st);
 // hl (`parts` parts of scale * sum; and buf, if given) from partial sums
 // [S][nsp][T][R] by slot-sorted position.  order (nullable): receives the row
 // order of the tile GEMM.
@@ -117,7 +122,7 @@ static __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 
 // wait_barrier.
 __device__ __forceinline__ void dma16(uint32_t lds, const void *src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(lds), "v"(src) : "memory", "m0");
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_barrier() {
