@@ -567,28 +567,20 @@ def alloc_linear_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, dev
 # The layer and gradient wrappers run once per layer of a step, next to kernels
 # of a few microseconds, so their checks touch each tensor attribute once.
 
-class _OnDevice:
-    """Makes `dev` (an index) the current device for a call, if it is not."""
-
-    def __init__(self, dev):
-        self.dev = dev
-
-    def __enter__(self):
-        torch = _torch()
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            _torch().cuda.set_device(self.prev)
-
-
-def _raw_stream(stream, dev):
-    """The stream handle of a call on device `dev` (its current stream)."""
+def _call(name, dev, stream, *args):
+    """The entry point `name` on device `dev` (made current for the call if it is
+    not), on `stream` or the device's current stream."""
+    cuda = _torch().cuda
     if stream is None:
-        return _torch().cuda.current_stream(dev).cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        stream = cuda.current_stream(dev)
+    if not isinstance(stream, int):
+        stream = stream.cuda_stream
+    prev = cuda.current_device()
+    if prev == dev:
+        _check(getattr(lib(), name)(*args, stream), name)
+        return
+    with cuda.device(dev):
+        _check(getattr(lib(), name)(*args, stream), name)
 
 
 def _one_device(tensors):
@@ -655,12 +647,9 @@ def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bi
         _need_vec(bias, sum(N), _torch().bfloat16, "bias")
     dev = _one_device((y, x, W, *A, *B, idx, slot_rank, scale, buf, bias, ws))
     S = len(N)
-    with _OnDevice(dev):
-        _check(lib().lora_linear(_ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
-                                 W.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B),
-                                 (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale),
-                                 _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes,
-                                 _raw_stream(stream, dev)), "lora_linear")
+    _call("lora_linear", dev, stream, _ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
+          W.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B), (_i64 * S)(*N), S, L, R, _ptr(idx),
+          _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
 
 
 def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
@@ -684,14 +673,11 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
     if len(set(outs)) != len(outs):
         raise ValueError("dx, dA and dB must be different tensors")
     dev = _one_device((dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws))
-    with _OnDevice(dev):
-        _check(lib().lora_linear_backward(
-            _ptr(dx), 0 if dx is None else dx.stride(0), None if dA is None else _ptr_array(dA),
-            None if dB is None else _ptr_array(dB), _ptr(dy), dy.stride(0), _ptr(x), x.stride(0),
-            T, K, _ptr(W), 0 if W is None else W.stride(0), _ptr_array(A), _ptr_array(B),
-            (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf),
-            LORA_DT_BF16, flags, _ptr(ws), ws.nbytes, _raw_stream(stream, dev)),
-            "lora_linear_backward")
+    _call("lora_linear_backward", dev, stream, _ptr(dx), 0 if dx is None else dx.stride(0),
+          None if dA is None else _ptr_array(dA), None if dB is None else _ptr_array(dB), _ptr(dy),
+          dy.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
+          _ptr_array(A), _ptr_array(B), (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank),
+          _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
 
 
 # ---------------------------------------------------------------------------
@@ -741,9 +727,8 @@ def lora_grad_norm(norm, grads: Sequence, ws, stream=None):
     _check_ws(ws)
     if _one_device((norm, ws)) != dev:
         _need_device((norm, grads[0], ws))
-    with _OnDevice(dev):
-        _check(lib().lora_grad_norm(_ptr(norm), ptrs, m, len(m), L, _dtype_code(grads[0]), _ptr(ws),
-                                    ws.nbytes, _raw_stream(stream, dev)), "lora_grad_norm")
+    _call("lora_grad_norm", dev, stream, _ptr(norm), ptrs, m, len(m), L, _dtype_code(grads[0]),
+          _ptr(ws), ws.nbytes)
 
 
 def lora_grad_clip(out: Sequence, grads: Sequence, norm, max_norm, stream=None):
@@ -758,7 +743,5 @@ def lora_grad_clip(out: Sequence, grads: Sequence, norm, max_norm, stream=None):
     _need_vec(max_norm, L, torch.float32, "max_norm")
     if _one_device((norm, max_norm)) != dev or odev != dev:
         _need_device((norm, max_norm, grads[0], out[0]))
-    with _OnDevice(dev):
-        _check(lib().lora_grad_clip(optrs, ptrs, m, len(m), L, _ptr(norm), _ptr(max_norm),
-                                    _dtype_code(grads[0]), _raw_stream(stream, dev)),
-               "lora_grad_clip")
+    _call("lora_grad_clip", dev, stream, optrs, ptrs, m, len(m), L, _ptr(norm), _ptr(max_norm),
+          _dtype_code(grads[0]))

@@ -56,13 +56,13 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         if (wg > (size_t)kLinWgPartMax) wg = (size_t)kLinWgPartMax;
         if (4 * wg > part) part = 4 * wg;
     }
-    // the tile GEMM's sums: K splits (at most 8) of at most kLinSplitTiles tiles
-    // of 128 x 128, or one sum of a direct batch (T N <= kLinDirectBytes / 16)
+    // the tile GEMM's sums: at most 8 K splits (of kLinSplitTiles tiles of
+    // 128 x 128), at most kLinJoinMax
     size_t cols = 0;
     for (int s = 0; s < S; ++s) cols += (size_t)N[s];
     if (cols < (size_t)K) cols = (size_t)K;
-    size_t sums = 8 * (size_t)T * cols;
-    if (sums > (size_t)kLinSplitTiles * 16384) sums = (size_t)kLinSplitTiles * 16384;
+    size_t sums = kLinMaxSplits * (size_t)T * cols;
+    if (sums > (size_t)kLinJoinMax) sums = (size_t)kLinJoinMax;
     if (4 * sums > part) part = 4 * sums;
     o = align256(o + part);
     w.pad = o;
@@ -145,10 +145,13 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     uint16_t *hl = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
     int32_t *order = nullptr;
     const bool direct = lin_direct(T, K, N, S, R, L);
+    const bool join = direct || lin_join_delta(T, K, N, S, R, L);
     float *u = buf, *clear = nullptr;
-    if (direct) {
-        // fp32 rank vectors by token, in buf if it is wanted
-        if (!u) u = reinterpret_cast<float *>(wp + wl.hl_u);
+    // fp32 rank vectors by token, in buf if it is wanted
+    if (join && !u) u = reinterpret_cast<float *>(wp + wl.hl_u);
+    if (lin_one(T, R)) {
+        clear = buf;
+    } else if (direct) {
         if (lin_grouped(T, K, R, L)) {
             float *part = reinterpret_cast<float *>(wp + wl.part);
             CHECK(launched(launch_grp_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, part, nullptr, nullptr, st)));
@@ -165,7 +168,8 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
         if (!(flags & LORA_FLAG_SEGMENTS_READY))
             CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
         CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
-        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl, kLinPartsFwd, buf, order, st)));
+        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, join ? nullptr : hl,
+                                         kLinPartsFwd, join ? u : buf, order, st)));
     }
     LinArgs a{};
     a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
@@ -173,12 +177,13 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
     a.part = reinterpret_cast<float *>(wp + wl.part);
-    a.join_delta = direct;
+    a.join_delta = join;
     a.u = u; a.scale = scale; a.clear = clear;
     a.hl = hl; a.hl_row = kLinPartsFwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
     a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) {
         a.lora[s] = static_cast<const uint16_t *>(B[s]);
+        a.la[s] = static_cast<const uint16_t *>(A[s]);
         a.n[s] = N[s];
         a.off[s] = sl.off[s];
     }

@@ -130,9 +130,16 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     }
     __syncthreads();
     if (a.accumulate && !s_any) return;
-    // (delta in the join, or in the last split)
-    const bool no_delta = MIXED && (a.join_delta || blockIdx.y + 1 < gridDim.y);
-    const int n_lt = no_delta ? 0 : __builtin_amdgcn_readfirstlane(s_nt) * (NN ? a.S : 1);
+    // rank-vector K tiles (MIXED: none when the join adds the delta, else this
+    // split's share)
+    int n_lt = 0, lt0 = 0;
+    if (!MIXED || !a.join_delta) {
+        n_lt = __builtin_amdgcn_readfirstlane(s_nt) * (NN ? a.S : 1);
+        if (MIXED) {
+            lt0 = n_lt * (int)blockIdx.y / a.ksp;
+            n_lt = n_lt * ((int)blockIdx.y + 1) / a.ksp - lt0;
+        }
+    }
 
     // K tiles: the projection's (per slice in the gradient), then per slot
     // (and slice) the [high | low] rank vectors.
@@ -142,7 +149,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
             for (int s = 0; s < a.S; ++s) nk += (int)((a.n[s] + BK - 1) / BK);
         else
             nk = (a.K + BK - 1) / BK;
-        // MIXED: this split's share of them (the last takes the rank vectors')
+        // MIXED: this split's share of them
         if (MIXED) {
             const int per = (nk + a.ksp - 1) / a.ksp;
             k0 = min((int)blockIdx.y * per, nk);
@@ -160,7 +167,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         u.s = s_first;
         ++u.d;
     };
-    Cursor ld = {0, s_first, 0}, use = {0, s_first, 0};
+    Cursor ld = {0, s_first, 0};
+    for (; lt0 > 0; --lt0) step(ld);
+    Cursor use = ld;
 
     // DMA lanes: fixed rows, global units XOR-ed.
     auto pswz = [](int row) { return (row >> 1) & 7; };
@@ -295,8 +304,22 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         else wait_barrier<0>();
     };
 
-    for (int i = 0; i < NST; ++i)
-        if (i < nv) issue(i, i);
+    auto loads = [&](uint32_t pl, int j, int n) __attribute__((always_inline)) {
+        // share j of n of a whole base tile's DMA
+#pragma unroll
+        for (int i = j * PI / n; i < (j + 1) * PI / n; ++i) dma16(pl + i * NW * 1024, pptr[i] + po);
+#pragma unroll
+        for (int i = j * QI / n; i < (j + 1) * QI / n; ++i) dma16(pl + PB + i * NW * 1024, qptr[i] + qo);
+    };
+    if (nk >= NST && rem >= NST * BK) {
+        for (int i = 0; i < NST; ++i) {
+            loads(lds0 + i * (PB + QB), 0, 1);
+            advance();
+        }
+    } else {
+        for (int i = 0; i < NST; ++i)
+            if (i < nv) issue(i, i);
+    }
     if (nv >= NST) wait_barrier<(NST - 1) * (PI + QI)>();
     else wait_barrier<0>();
     for (int v = 0; v < nv; ++v) {
@@ -310,18 +333,12 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[set][i], fp[set][j], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             };
-            // share j of n of a fragment set's reads, or of a tile's DMA
+            // share j of n of a fragment set's reads
             auto reads = [&](int set, const char *st, int kk, int j, int n) {
 #pragma unroll
                 for (int i = j * MB / n; i < (j + 1) * MB / n; ++i) fp[set][i] = pfrag(st, i, kk);
 #pragma unroll
                 for (int i = j * NB / n; i < (j + 1) * NB / n; ++i) fq[set][i] = qfrag(st, i, kk);
-            };
-            auto loads = [&](uint32_t pl, int j, int n) {
-#pragma unroll
-                for (int i = j * PI / n; i < (j + 1) * PI / n; ++i) dma16(pl + i * NW * 1024, pptr[i] + po);
-#pragma unroll
-                for (int i = j * QI / n; i < (j + 1) * QI / n; ++i) dma16(pl + PB + i * NW * 1024, qptr[i] + qo);
             };
             constexpr int RG = MB / 4 > 0 ? MB / 4 : 1;   // MFMA groups that carry the second set's reads
             constexpr int LG = MB - RG - (MB > 4);        // and a tile's DMA
@@ -357,24 +374,25 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         if (!base) step(use);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            bf16x8_t q[NB];
+            bf16x8_t q[NB], p[MB];
 #pragma unroll
             for (int i = 0; i < NB; ++i) q[i] = qfrag(st, i, kk);
+#pragma unroll
+            for (int j = 0; j < MB; ++j) p[j] = pfrag(st, j, kk);
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
                 const int rs = s_slot[(wm * MB + j) * 16 + (MIXED ? l16 : 0)];
                 const bool mine = base || (rs == slot && (MIXED || s_whole[wm * MB + j]));
                 if (__ballot(mine) == 0) continue;
-                const bf16x8_t p = pfrag(st, j, kk);
                 if (!MIXED || __ballot(!mine && rs != -2) == 0) {
 #pragma unroll
                     for (int i = 0; i < NB; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p, acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p[j], acc[i][j], 0, 0, 0);
                 } else {
 #pragma unroll
                     for (int i = 0; i < NB; ++i) {
                         const floatx4_t z = {0.f, 0.f, 0.f, 0.f};
-                        const floatx4_t t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p, z, 0, 0, 0);
+                        const floatx4_t t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p[j], z, 0, 0, 0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
                     }
@@ -498,12 +516,23 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     }
     __syncthreads();
     constexpr int LPR = BN / 4, RPW = 64 / LPR > 0 ? 64 / LPR : 1;   // lanes per row, rows per wave store
-    for (int r0 = w * RPW; r0 < BM; r0 += NW * RPW) {
-        const int row = r0 + lane / LPR, cl = (lane % LPR) * 4;
-        const uint2 v = *reinterpret_cast<const uint2 *>(
-            s_stage + row * (BN * 2) + (((cl >> 3) ^ (row & (UO - 1))) << 4) + ((cl & 4) << 1));
-        if (s_slot[row] != -2 && c0 + cl < cend)
-            *reinterpret_cast<uint2 *>(a.out + (int64_t)s_tok[row] * a.ldo + obase + c0 + cl) = v;
+    constexpr int EU = BM / (NW * RPW) < 16 ? BM / (NW * RPW) : 16;  // stores in flight
+    const int cl = (lane % LPR) * 4;
+    if (c0 + cl >= cend) return;
+    for (int r0 = w * RPW + lane / LPR; r0 < BM; r0 += NW * RPW * EU) {
+        uint2 v[EU];
+        int tok[EU], sl[EU];
+#pragma unroll
+        for (int i = 0; i < EU; ++i) {
+            const int row = r0 + i * NW * RPW;
+            v[i] = *reinterpret_cast<const uint2 *>(
+                s_stage + row * (BN * 2) + (((cl >> 3) ^ (row & (UO - 1))) << 4) + ((cl & 4) << 1));
+            tok[i] = s_tok[row];
+            sl[i] = s_slot[row];
+        }
+#pragma unroll
+        for (int i = 0; i < EU; ++i)
+            if (sl[i] != -2) __builtin_nontemporal_store(__builtin_bit_cast(unsigned long, v[i]), reinterpret_cast<unsigned long *>(a.out + (int64_t)tok[i] * a.ldo + obase + c0 + cl));
     }
 }
 
@@ -698,47 +727,323 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
         make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
 }
 
+// One token: one launch.  Work-group = 16 output columns, as k_lin_few, and the
+// rank vector of the token's slot beside them (16 NRB lora_a rows of the slice,
+// the same for every work-group and so read from L2): W and lora_a rows meet
+// the same x fragments.  Against k_lin_shrink and k_lin_few (QKV of 4096,
+// rank 16): 16.1 against 22.8 us a call.
+template <int NRB, int U>
+__global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
+    __shared__ float s_sum[kFewWaves][1 + NRB][16];
+    __shared__ float s_u[16 * NRB];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int l16 = lane & 15, g = lane >> 4;
+    int sc = 0;
+    while (sc + 1 < a.S && (int)blockIdx.x >= a.tile_start[sc + 1]) ++sc;
+    const int tile = blockIdx.x - a.tile_start[sc];
+    const int64_t c0 = (int64_t)tile * 16, cend = a.n[sc];
+    const int slot = slot_of_token(a.idx, a.slot_rank, a.L, 0);
+    const uint16_t *wr = a.w + (a.off[sc] + min(c0 + l16, cend - 1)) * a.ldw;
+    const uint16_t *ar[NRB];
+#pragma unroll
+    for (int i = 0; i < NRB; ++i)
+        ar[i] = a.la[sc] + ((int64_t)max(slot, 0) * a.R + min(i * 16 + l16, a.R - 1)) * a.K;
+    floatx4_t acc = {0.f, 0.f, 0.f, 0.f}, au[NRB];
+#pragma unroll
+    for (int i = 0; i < NRB; ++i) au[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    for (int kb = w * 64; kb < a.K; kb += U * kFewWaves * 64) {
+        uint4 wv[U][2], xv[U][2], av[U][2][NRB];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kb + u * kFewWaves * 64 + h * 32 + g * 8, kc = k < a.K ? k : 0;
+                wv[u][h] = ldg<uint4>(wr + kc);
+                xv[u][h] = ldg<uint4>(a.p + kc);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kb + u * kFewWaves * 64 + h * 32 + g * 8, kc = k < a.K ? k : 0;
+#pragma unroll
+                for (int i = 0; i < NRB; ++i) av[u][h][i] = ldg<uint4>(ar[i] + kc);
+            }
+        __builtin_amdgcn_sched_barrier(0);        // every load of the round in flight
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = kb + u * kFewWaves * 64 + h * 32 + g * 8 < a.K;
+                const bf16x8_t x = frag(in ? xv[u][h] : z);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? wv[u][h] : z), x, acc, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < NRB; ++i)
+                    au[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? av[u][h][i] : z), x, au[i], 0, 0, 0);
+            }
+    }
+    // every result column is the token: column 0's lanes give the sums
+    if (l16 == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s_sum[w][0][4 * g + e] = acc[e];
+#pragma unroll
+            for (int i = 0; i < NRB; ++i) s_sum[w][1 + i][4 * g + e] = au[i][e];
+        }
+    }
+    __syncthreads();
+    const int rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    if (tid < 16 * NRB) {
+        float u = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFewWaves; ++i) u += s_sum[i][1 + (tid >> 4)][tid & 15];
+        if (tid >= rank) u = 0.f;
+        s_u[tid] = u;
+        if (a.clear && tile == 0 && tid < a.R) a.clear[(int64_t)sc * a.R + tid] = u;
+    }
+    __syncthreads();
+    if (w) return;
+    const int64_t c = c0 + l16, col = a.off[sc] + min(c, cend - 1);
+    float d = 0.f;
+    if (slot >= 0) {
+        const uint16_t *b = a.lora[sc] + ((int64_t)slot * cend + min(c, cend - 1)) * a.R;
+#pragma unroll
+        for (int i = 0; i < (NRB + 1) / 2; ++i) {
+            const int j = i * 32 + g * 8;
+            if (j < rank) {
+                const uint4 v = ldg<uint4>(b + j);
+                const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    d += s_u[j + 2 * q] * bf16_lo(bw[q]);
+                    d += s_u[j + 2 * q + 1] * bf16_hi(bw[q]);
+                }
+            }
+        }
+        d += __shfl_xor(d, 16);
+        d += __shfl_xor(d, 32);
+        d *= a.scale[slot];
+    }
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFewWaves; ++i) y += s_sum[i][0][l16];
+    if (a.bias) y += bf16_to_f32(a.bias[col]);
+    if (g == 0 && c < cend) a.out[col] = (uint16_t)f32_to_bf16_rne(y + d);
+}
+
 // The K splits of a tile GEMM, summed in order, bias (and with join_delta the
-// forward's delta) added, rounded once.
+// forward's delta) added, rounded once.  Wave = 16 rows x 64 columns in the
+// layout of a 16x16 MFMA result (row lane % 16, 4 columns).  The delta: for each
+// slot among the 16 rows, its lora_b rows straight from global memory into
+// fragments (the next step's loads in flight), times the rows' scaled rank
+// vectors split into two bf16 parts, kept by the slot's own rows only.
+constexpr int kJoinRows = 16;
+constexpr int kJoinCols = 256;
 __global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
-    const int m = blockIdx.y;
-    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    const int t = a.order ? a.order[m] : m;
-    const int slot = a.join_delta ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -1;
-    if (a.clear && slot < 0 && blockIdx.x == 0) {
+    constexpr int NB = 4;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+    const int m = blockIdx.y * kJoinRows + l16;
+    const bool real = m < a.T;
+    const int mc = min(m, a.T - 1);
+    const int t = a.order ? a.order[mc] : mc;
+    const int slot = a.join_delta && real ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -1;
+    if (a.clear && blockIdx.x == 0 && real && slot < 0) {
         // the rank vectors of a token without a slot, which the grouped shrink leaves
+        for (int s = 0; s < a.S; ++s)
+            for (int j = threadIdx.x >> 4; j < a.R; j += 16) a.clear[((int64_t)s * a.T + t) * a.R + j] = 0.f;
+    }
+    const int64_t c0 = (int64_t)blockIdx.x * kJoinCols + w * (NB * 16);
+    if (c0 >= a.part_ld) return;
+    floatx4_t v[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) v[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < a.ksp; ++k) {
+        const float *p = a.part + ((int64_t)k * a.T + mc) * a.part_ld;
+        floatx4_t o[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) o[i] = ldg<floatx4_t>(p + min(c0 + i * 16 + 4 * g, a.part_ld - 4));
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] += o[i][e];
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] += bf16_to_f32(a.bias[min(c0 + i * 16 + 4 * g, a.part_ld - 4) + e]);
+    }
+    if (a.join_delta) {
+        // a lane's lora_b row of each 16-column block and its slice, by selects
+        // (an index that differs between lanes would load the arguments from
+        // memory one after the other).  A block may straddle slices: columns
+        // 4 g..+3 of a result lane are of one slice, found the same way.
+        const uint16_t *row[NB];
+        int64_t n[NB];
+        int sb[NB], first = 0, last = 0;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int64_t c = min(c0 + i * 16 + l16, a.part_ld - 1), cv = min(c0 + i * 16 + 4 * g, a.part_ld - 4);
+            int64_t o = 0;
+            n[i] = a.n[0];
+            row[i] = a.lora[0];
+            sb[i] = 0;
+#pragma unroll
+            for (int s = 1; s < kMaxSlices; ++s)
+                if (s < a.S) {
+                    if (c >= a.off[s]) { o = a.off[s]; n[i] = a.n[s]; row[i] = a.lora[s]; }
+                    if (cv >= a.off[s]) sb[i] = s;
+                }
+            row[i] += (c - o) * a.R;
+        }
+        for (int s = 1; s < a.S; ++s) {
+            if (c0 >= a.off[s]) first = s;
+            if (min(c0 + NB * 16, a.part_ld) - 1 >= a.off[s]) last = s;
+        }
+        const int rank_own = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+        const float sc = slot < 0 ? 0.f : a.scale[slot];
+        unsigned long long todo = __ballot(slot >= 0) & 0xffff;
+        int cur = -1, rank = 0, k0 = 0;
+        auto pop = [&]() {
+            const int l = __ffsll(todo) - 1;
+            cur = __builtin_amdgcn_readlane(slot, l);
+            rank = __builtin_amdgcn_readlane(rank_own, l);
+            todo &= ~__ballot(slot == cur);
+            k0 = 0;
+        };
+        auto fetch = [&](uint4 (&q)[NB]) {
+            const int k = k0 + g * 8;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                q[i] = k < rank ? ldg<uint4>(row[i] + (int64_t)cur * n[i] * a.R + k) : make_uint4(0, 0, 0, 0);
+        };
+        uint4 q[NB], qn[NB];
+        floatx4_t d[NB];
+        if (todo) {
+            pop();
+            fetch(q);
+        }
+        while (cur >= 0) {
+            const int at = cur, kb = k0;
+            const bool mine = slot == at;
+            if (kb == 0) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) d[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+            }
+            k0 += 32;
+            if (k0 >= rank) {
+                if (todo) pop();
+                else cur = -1;
+            }
+            if (cur >= 0) fetch(qn);
+            const int k = kb + g * 8;
+            for (int s = first; s <= last; ++s) {
+                uint32_t part[8][3];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part[e][0] = part[e][1] = 0;
+                if (mine && k < rank_own) {
+                    const float *u = a.u + ((int64_t)s * a.T + t) * a.R + k;
+                    const floatx4_t u0 = ldg<floatx4_t>(u), u1 = ldg<floatx4_t>(u + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        split_bf16(sc * u0[e], part[e]);
+                        split_bf16(sc * u1[e], part[4 + e]);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bf16x8_t p = frag(make_uint4(part[0][h] | part[1][h] << 16, part[2][h] | part[3][h] << 16,
+                                                       part[4][h] | part[5][h] << 16, part[6][h] | part[7][h] << 16));
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const floatx4_t r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(q[i]), p, d[i], 0, 0, 0);
+                        if (first == last) d[i] = r;
+                        else if (sb[i] == s) d[i] = r;
+                    }
+                }
+            }
+            if (cur != at) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] = mine ? v[i][e] + d[i][e] : v[i][e];
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) q[i] = qn[i];
+        }
+    }
+    if (!real) return;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int64_t c = c0 + i * 16 + 4 * g;
+        if (c < a.part_ld)
+            *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ldo + c) =
+                make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
+    }
+}
+
+// The same for a direct batch, whose rows are in token order: 16 rows then name
+// up to 16 slots, and one after the other they cost the MFMA form above more
+// than it saves (256 tokens of 8 slots, 6144 columns, rank 16: 22.8 against
+// 12.6 us).  Work-group = one token x 512 columns, 2 per thread, so that a
+// wave's lora_b loads cover whole lines: fp32 FMAs with the token's rank vector.
+__global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
+    const int t = blockIdx.y;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+    const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
+    if (a.clear && slot < 0 && blockIdx.x == 0) {
         for (int s = 0; s < a.S; ++s)
             for (int j = threadIdx.x; j < a.R; j += 256) a.clear[((int64_t)s * a.T + t) * a.R + j] = 0.f;
     }
     if (c >= a.part_ld) return;
-    floatx4_t v = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < a.ksp; ++k) {
-        const floatx4_t o = *reinterpret_cast<const floatx4_t *>(a.part + ((int64_t)k * a.T + m) * a.part_ld + c);
+    float v0 = 0.f, v1 = 0.f;
+    float2 o[kLinMaxSplits];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += o[e];
-    }
+    for (int k = 0; k < kLinMaxSplits; ++k)
+        if (k < a.ksp) o[k] = *reinterpret_cast<const float2 *>(a.part + ((int64_t)k * a.T + t) * a.part_ld + c);
+#pragma unroll
+    for (int k = 0; k < kLinMaxSplits; ++k)
+        if (k < a.ksp) {
+            v0 += o[k].x;
+            v1 += o[k].y;
+        }
     if (a.bias) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(a.bias[c + e]);
+        v0 += bf16_to_f32(a.bias[c]);
+        v1 += bf16_to_f32(a.bias[c + 1]);
     }
     if (slot >= 0) {
         // the column's slice by selects (an index that differs between lanes
         // would load the arguments from memory, one after the other)
         int s = 0;
-        int64_t o = 0, n = a.n[0];
-        const uint16_t *lora = a.lora[0];
+        int64_t off = 0, n = a.n[0];
+        const uint16_t *b = a.lora[0];
 #pragma unroll
         for (int i = 1; i < kMaxSlices; ++i)
-            if (i < a.S && c >= a.off[i]) {
-                s = i;
-                o = a.off[i];
-                n = a.n[i];
-                lora = a.lora[i];
+            if (i < a.S && c >= a.off[i]) { s = i; off = a.off[i]; n = a.n[i]; b = a.lora[i]; }
+        b += ((int64_t)slot * n + c - off) * a.R;
+        const float *u = a.u + ((int64_t)s * a.T + t) * a.R;
+        const int rank = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll 2
+        for (int j = 0; j < rank; j += 8) {
+            const floatx4_t u0 = ldg<floatx4_t>(u + j), u1 = ldg<floatx4_t>(u + j + 4);
+            const uint4 b0 = ldg<uint4>(b + j), b1 = ldg<uint4>(b + a.R + j);
+            const float uv[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+            const uint32_t w0[4] = {b0.x, b0.y, b0.z, b0.w}, w1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                d0 += uv[2 * q] * bf16_lo(w0[q]);
+                d0 += uv[2 * q + 1] * bf16_hi(w0[q]);
+                d1 += uv[2 * q] * bf16_lo(w1[q]);
+                d1 += uv[2 * q + 1] * bf16_hi(w1[q]);
             }
-        add_delta(v, a, lora + ((int64_t)slot * n + c - o) * a.R, s, t, slot);
+        }
+        const float sc = a.scale[slot];
+        v0 += sc * d0;
+        v1 += sc * d1;
     }
-    *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.ldo + c) =
-        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.ldo + c) = pack_bf16x2(v0, v1);
 }
 
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
@@ -832,7 +1137,7 @@ __global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
         if (j + e >= r) sum[e] = 0.f;
         v[e] = j + e < r ? sc * sum[e] : 0.f;
     }
-    store_parts(a.hl + row * a.parts * a.R, a.parts, a.R, j, v);
+    if (a.hl) store_parts(a.hl + row * a.parts * a.R, a.parts, a.R, j, v);
     if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
 }
 
@@ -864,7 +1169,18 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + 1023) / 1024), (unsigned)a.T), dim3(256), 0, st, a);
+    if (a.join_delta && !a.order)
+        hipLaunchKernelGGL(k_lin_join_rows, dim3((unsigned)((cols + 511) / 512), (unsigned)a.T), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols),
+                                            (unsigned)((a.T + kJoinRows - 1) / kJoinRows)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int NRB, int U>
+hipError_t run_one(LinArgs a, hipStream_t st) {
+    const int n = column_tiles(a, 16);
+    hipLaunchKernelGGL((k_lin_one<NRB, U>), dim3((unsigned)n), dim3(kFewWaves * 64), 0, st, a);
     return hipGetLastError();
 }
 
@@ -895,12 +1211,13 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
+    if (!gradient && lin_one(a.T, a.R)) return a.R <= 16 ? run_one<1, 8>(a, st) : run_one<2, 4>(a, st);
     if (!gradient && a.T <= kLinFewTokens) {
         if (a.T <= 16) return run_few<1, 1, 8>(a, st);
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
         return run_few<4, 2, 2>(a, st);
     }
-    if (a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)   // (not with join_delta)
+    if (!a.join_delta && a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
         return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
     // Few tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
     // each), joined by a second launch.
@@ -913,7 +1230,7 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     auto splits = [&](int64_t t) {
         int64_t k = kLinSplitTiles / t;
         if (k > nk / 8) k = nk / 8;
-        if (k > 8) k = 8;
+        if (k > kLinMaxSplits) k = kLinMaxSplits;
         return (int)(k < 1 ? 1 : k);
     };
     const int64_t t128 = tiles(a.T, a.K, a.n, a.S, gradient, 128), t64 = tiles(a.T, a.K, a.n, a.S, gradient, 64);
@@ -923,11 +1240,26 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     return run_tile<64, 64, 2, 2, 4, true>(a, gradient, splits(t64), st);
 }
 
+// Whether a sorted forward batch leaves the delta to the join: when the
+// rank-vector K tiles that a 128-token tile is expected to meet (its share of
+// the slots, and one for a slot that continues) pass an eighth of its base K
+// tiles, and the fp32 sums stay within kLinJoinMax.  (1024 tokens over 128
+// slots of ranks up to 128, 8192 x 8192: see k_lin_join's figures in the
+// table of the layer cases.)
+bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) n += N[s];
+    const double slots = 128.0 * (T < L ? T : L) / T + 1.0;
+    return slots * ((2 * R + 63) / 64) > K / 64 / 8.0 && (int64_t)T * n <= kLinJoinMax;
+}
+
+// One token of rank at most 32 takes the one launch of k_lin_one.
+bool lin_one(int32_t T, int32_t R) { return T == 1 && R <= 32; }
+
 // Whether a forward batch takes the direct path: rank vectors by k_lin_shrink
 // (no segment build) and the delta in k_lin_few or the join.  Both read their
 // lora rows once per token block or token, so their bytes bound it: past
-// kLinDirectBytes either the segment build and the tiles' own rank-vector K
-// tiles are the faster.
+// kLinDirectBytes of either the sorted rows are the faster.
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     if (T <= kLinFewTokens) return true;
     if (T > kLinDirectTokens) return false;

@@ -26,10 +26,11 @@ struct LinArgs {
     int32_t accumulate;       // out += delta (no base product); rows without a slot untouched
     int32_t m_tiles, n_tiles;
     int32_t ksp;              // K splits; with part, fp32 sums go to part [ksp][T][part_ld]
-    int32_t join_delta;       // the join adds the delta (direct path), not the tiles
-    const float *u;           // direct path: fp32 rank vectors [S][T][R]
+    int32_t join_delta;       // the join adds the delta, not the tiles
+    const float *u;           // fp32 rank vectors [S][T][R] of the join and of k_lin_few
     const float *scale;
-    float *clear;             // join: u rows of tokens without a slot to clear, or null
+    float *clear;             // join: u rows of tokens without a slot to clear, or null (k_lin_one: u)
+    const uint16_t *la[kMaxSlices];     // k_lin_one: lora_a [L][R][K]
     float *part;
     int64_t part_ld;
     const uint16_t *lora[kMaxSlices];   // forward: lora_b [L][N_s][R]; gradient: lora_a [L][R][K]
@@ -41,6 +42,8 @@ struct LinArgs {
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
 constexpr int kLinFewTokens = 64;       // forward batches of at most this many tokens: k_lin_few
+constexpr int kLinMaxSplits = 8;
+bool lin_one(int32_t T, int32_t R);
 constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits (k T cols <= this * 128^2)
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
@@ -52,6 +55,8 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
 // The direct path: rank vectors in one launch without segments.
 constexpr int kLinDirectTokens = 1024;
 constexpr int64_t kLinDirectBytes = 128 << 20;
+constexpr int64_t kLinJoinMax = 1 << 25;   // fp32 sums of a call (T N, with its K splits)
+bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,
