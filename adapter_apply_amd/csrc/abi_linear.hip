@@ -50,11 +50,11 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     size_t kt = (size_t)T + 65536;
     if (kt > 16 * (size_t)T) kt = 16 * (size_t)T;
     if (4 * (size_t)S * R * kt > part) part = 4 * (size_t)S * R * kt;
-    // the weight gradients' token splits (none up to 511 tokens)
+    // the token splits of both weight gradients (none up to 511 tokens)
     if (T > 256) {
         size_t wg = (size_t)131072 * R;
         if (wg > (size_t)kLinWgPartMax) wg = (size_t)kLinWgPartMax;
-        if (4 * wg > part) part = 4 * wg;
+        if (2 * 4 * wg > part) part = 2 * 4 * wg;
     }
     // the tile GEMM's sums: at most 8 K splits (of kLinSplitTiles tiles of
     // 128 x 128), at most kLinJoinMax
@@ -168,8 +168,8 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
         if (!(flags & LORA_FLAG_SEGMENTS_READY))
             CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
         CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
-        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, join ? nullptr : hl,
-                                         kLinPartsFwd, join ? u : buf, order, st)));
+        const LinVectors v{part, nsp, nullptr, join ? nullptr : hl, kLinPartsFwd, join ? u : buf};
+        CHECK(launched(launch_lin_vectors(&v, 1, T, S, L, R, idx, slot_rank, scale, seg, order, st)));
     }
     LinArgs a{};
     a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
@@ -250,46 +250,47 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         CHECK(launched(launch_lin_pad(dy, lddy, T, S, m, pad, ldp, st)));
         p = pad;
     }
+    // rank vectors in parts: scale * u for dB, v for dx and dA
+    LinVectors job[2];
+    int n_jobs = 0;
     if (dB) {
-        if (buf) {
-            CHECK(launched(launch_lin_split(buf, T, S, L, R, idx, slot_rank, scale, seg, hl_u, kLinPartsBwd, nullptr, st)));
+        LinVectors v{nullptr, 0, buf, hl_u, kLinPartsBwd, nullptr};
+        if (!buf) {
+            v.part = part;
+            CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &v.nsp, st));
+            // (before the partial sums of v take their place)
+            CHECK(launched(launch_lin_vectors(&v, 1, T, S, L, R, idx, slot_rank, scale, seg, nullptr, st)));
         } else {
-            int32_t nsp = 1;
-            CHECK(sorted_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, part, &nsp, st));
-            CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_u,
-                                             kLinPartsBwd, nullptr, nullptr, st)));
+            job[n_jobs++] = v;
         }
-        LinWgArgs a{};
-        a.p = p; a.ldp = ldp; a.hl = hl_u;
-        for (int s = 0; s < S; ++s) {
-            a.out[s] = dB[s];
-            a.m[s] = N[s];
-            a.poff[s] = poff[s];
-        }
-        a.T = T; a.S = S; a.L = L; a.R = R;
-        a.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
-        a.seg = seg; a.part = part;
-        a.nsp = lin_wg_splits(T, L, N, S, R);
-        CHECK(launched(launch_lin_wg(a, false, st)));
     }
     if (dx || dA) {
         const int32_t nsp = lin_du_splits(T, L, N, S, R);
         CHECK(launched(launch_lin_du(p, ldp, poff, T, sl, S, L, R, slot_rank, seg, part, nsp, st)));
-        CHECK(launched(launch_lin_reduce(part, nsp, T, S, L, R, idx, slot_rank, scale, seg, hl_v, kLinPartsBwd, nullptr,
-                                         dx ? order : nullptr, st)));
+        job[n_jobs++] = LinVectors{part, nsp, nullptr, hl_v, kLinPartsBwd, nullptr};
     }
-    if (dA) {
-        LinWgArgs a{};
-        a.p = static_cast<const uint16_t *>(x); a.ldp = ldx; a.hl = hl_v;
+    if (n_jobs)
+        CHECK(launched(launch_lin_vectors(job, n_jobs, T, S, L, R, idx, slot_rank, scale, seg,
+                                          dx ? order : nullptr, st)));
+    if (dA || dB) {
+        LinWgArgs wa{}, wb{};
+        wa.T = T; wa.S = S; wa.L = L; wa.R = R; wa.seg = seg;
+        wa.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
+        wb = wa;
+        wa.p = static_cast<const uint16_t *>(x); wa.ldp = ldx; wa.hl = hl_v;
+        wb.p = p; wb.ldp = ldp; wb.hl = hl_u;
         for (int s = 0; s < S; ++s) {
-            a.out[s] = dA[s];
-            a.m[s] = K;
+            wa.out[s] = dA ? dA[s] : nullptr;
+            wa.m[s] = K;
+            wb.out[s] = dB ? dB[s] : nullptr;
+            wb.m[s] = N[s];
+            wb.poff[s] = poff[s];
         }
-        a.T = T; a.S = S; a.L = L; a.R = R;
-        a.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
-        a.seg = seg; a.part = part;
-        a.nsp = lin_wg_splits(T, L, a.m, S, R);
-        CHECK(launched(launch_lin_wg(a, true, st)));
+        wa.nsp = lin_wg_splits(T, L, wa.m, S, R);
+        wb.nsp = lin_wg_splits(T, L, N, S, R);
+        wa.part = part;
+        wb.part = part + (dA && wa.nsp > 1 ? wa.nsp * lin_wg_part(L, wa.m, S, R) : 0);
+        CHECK(launched(launch_lin_wg(dA ? &wa : nullptr, dB ? &wb : nullptr, st)));
     }
     if (dx) {
         LinArgs a{};

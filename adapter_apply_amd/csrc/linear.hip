@@ -727,41 +727,63 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
         make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
 }
 
-// One token: one launch.  Work-group = 16 output columns, as k_lin_few, and the
-// rank vector of the token's slot beside them (16 NRB lora_a rows of the slice,
-// the same for every work-group and so read from L2): W and lora_a rows meet
-// the same x fragments.  Against k_lin_shrink and k_lin_few (QKV of 4096,
-// rank 16): 16.1 against 22.8 us a call.
-template <int NRB, int U>
+// One token: one launch.  Work-group = 16 CT output columns, as k_lin_few, and
+// the rank vector of the token's slot beside them (16 NRB lora_a rows of the
+// slice, the same for every work-group and so read from L2): W and lora_a rows
+// meet the same x fragments.  QKV of 4096, rank 16: 18.0 us against 22 of
+// k_lin_shrink and k_lin_few; two column blocks halve the lora_a reads (one:
+// 20.2, four leave CUs idle: 23.2).
+template <int CT, int NRB, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
-    __shared__ float s_sum[kFewWaves][1 + NRB][16];
+    __shared__ float s_sum[kFewWaves][CT + NRB][16];
     __shared__ float s_u[16 * NRB];
+    __shared__ int s_own[1];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
     int sc = 0;
     while (sc + 1 < a.S && (int)blockIdx.x >= a.tile_start[sc + 1]) ++sc;
     const int tile = blockIdx.x - a.tile_start[sc];
-    const int64_t c0 = (int64_t)tile * 16, cend = a.n[sc];
-    const int slot = slot_of_token(a.idx, a.slot_rank, a.L, 0);
-    const uint16_t *wr = a.w + (a.off[sc] + min(c0 + l16, cend - 1)) * a.ldw;
-    const uint16_t *ar[NRB];
+    const int64_t c0 = (int64_t)tile * (16 * CT), cend = a.n[sc];
+    const uint16_t *wr[CT], *ar[NRB];
 #pragma unroll
-    for (int i = 0; i < NRB; ++i)
-        ar[i] = a.la[sc] + ((int64_t)max(slot, 0) * a.R + min(i * 16 + l16, a.R - 1)) * a.K;
-    floatx4_t acc = {0.f, 0.f, 0.f, 0.f}, au[NRB];
+    for (int i = 0; i < CT; ++i) wr[i] = a.w + (a.off[sc] + min(c0 + i * 16 + l16, cend - 1)) * a.ldw;
+    uint4 bv[CT][(NRB + 1) / 2];
+    int slot = -1, rank = 0;
+    float sc_own = 0.f;
+    floatx4_t acc[CT], au[NRB];
+#pragma unroll
+    for (int i = 0; i < CT; ++i) acc[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NRB; ++i) au[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
     const uint4 z = make_uint4(0, 0, 0, 0);
     for (int kb = w * 64; kb < a.K; kb += U * kFewWaves * 64) {
-        uint4 wv[U][2], xv[U][2], av[U][2][NRB];
+        uint4 wv[U][2][CT], xv[U][2], av[U][2][NRB];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = kb + u * kFewWaves * 64 + h * 32 + g * 8, kc = k < a.K ? k : 0;
-                wv[u][h] = ldg<uint4>(wr + kc);
+#pragma unroll
+                for (int i = 0; i < CT; ++i) wv[u][h][i] = ldg<uint4>(wr[i] + kc);
                 xv[u][h] = ldg<uint4>(a.p + kc);
             }
+        __builtin_amdgcn_sched_barrier(0);
+        if (kb == w * 64) {
+            // the slot's loads, one after the other, behind those of W
+            slot = slot_of_token(a.idx, a.slot_rank, a.L, 0);
+            const int so = max(slot, 0);
+            rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[so], a.R) : a.R;
+            sc_own = a.scale[so];
+#pragma unroll
+            for (int i = 0; i < NRB; ++i)
+                ar[i] = a.la[sc] + ((int64_t)so * a.R + min(i * 16 + l16, a.R - 1)) * a.K;
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                const uint16_t *b = a.lora[sc] + ((int64_t)so * cend + min(c0 + i * 16 + l16, cend - 1)) * a.R;
+#pragma unroll
+                for (int j = 0; j < (NRB + 1) / 2; ++j) bv[i][j] = ldg<uint4>(b + min(j * 32 + g * 8, a.R - 8));
+            }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -777,7 +799,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
             for (int h = 0; h < 2; ++h) {
                 const bool in = kb + u * kFewWaves * 64 + h * 32 + g * 8 < a.K;
                 const bf16x8_t x = frag(in ? xv[u][h] : z);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? wv[u][h] : z), x, acc, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? wv[u][h][i] : z), x, acc[i], 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < NRB; ++i)
                     au[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? av[u][h][i] : z), x, au[i], 0, 0, 0);
@@ -787,49 +811,55 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
     if (l16 == 0) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s_sum[w][0][4 * g + e] = acc[e];
 #pragma unroll
-            for (int i = 0; i < NRB; ++i) s_sum[w][1 + i][4 * g + e] = au[i][e];
+            for (int i = 0; i < CT; ++i) s_sum[w][i][4 * g + e] = acc[i][e];
+#pragma unroll
+            for (int i = 0; i < NRB; ++i) s_sum[w][CT + i][4 * g + e] = au[i][e];
         }
     }
+    if (w == 0 && lane == 0) {
+        s_own[0] = rank;                          // (a wave without a K step knows no slot)
+    }
     __syncthreads();
-    const int rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    rank = s_own[0];
     if (tid < 16 * NRB) {
         float u = 0.f;
 #pragma unroll
-        for (int i = 0; i < kFewWaves; ++i) u += s_sum[i][1 + (tid >> 4)][tid & 15];
+        for (int i = 0; i < kFewWaves; ++i) u += s_sum[i][CT + (tid >> 4)][tid & 15];
         if (tid >= rank) u = 0.f;
         s_u[tid] = u;
         if (a.clear && tile == 0 && tid < a.R) a.clear[(int64_t)sc * a.R + tid] = u;
     }
     __syncthreads();
     if (w) return;
-    const int64_t c = c0 + l16, col = a.off[sc] + min(c, cend - 1);
-    float d = 0.f;
-    if (slot >= 0) {
-        const uint16_t *b = a.lora[sc] + ((int64_t)slot * cend + min(c, cend - 1)) * a.R;
 #pragma unroll
-        for (int i = 0; i < (NRB + 1) / 2; ++i) {
-            const int j = i * 32 + g * 8;
-            if (j < rank) {
-                const uint4 v = ldg<uint4>(b + j);
-                const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < CT; ++i) {
+        const int64_t c = c0 + i * 16 + l16;
+        float d = 0.f, y = 0.f;
+        if (slot >= 0) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    d += s_u[j + 2 * q] * bf16_lo(bw[q]);
-                    d += s_u[j + 2 * q + 1] * bf16_hi(bw[q]);
+            for (int jb = 0; jb < (NRB + 1) / 2; ++jb) {
+                const int j = jb * 32 + g * 8;
+                if (j < rank) {
+                    const uint32_t bw[4] = {bv[i][jb].x, bv[i][jb].y, bv[i][jb].z, bv[i][jb].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        d += s_u[j + 2 * q] * bf16_lo(bw[q]);
+                        d += s_u[j + 2 * q + 1] * bf16_hi(bw[q]);
+                    }
                 }
             }
+            d += __shfl_xor(d, 16);
+            d += __shfl_xor(d, 32);
+            d *= sc_own;
         }
-        d += __shfl_xor(d, 16);
-        d += __shfl_xor(d, 32);
-        d *= a.scale[slot];
-    }
-    float y = 0.f;
 #pragma unroll
-    for (int i = 0; i < kFewWaves; ++i) y += s_sum[i][0][l16];
-    if (a.bias) y += bf16_to_f32(a.bias[col]);
-    if (g == 0 && c < cend) a.out[col] = (uint16_t)f32_to_bf16_rne(y + d);
+        for (int k = 0; k < kFewWaves; ++k) y += s_sum[k][i][l16];
+        if (g == 0 && c < cend) {
+            if (a.bias) y += bf16_to_f32(a.bias[a.off[sc] + c]);
+            a.out[a.off[sc] + c] = (uint16_t)f32_to_bf16_rne(y + d);
+        }
+    }
 }
 
 // The K splits of a tile GEMM, summed in order, bias (and with join_delta the
@@ -1052,14 +1082,11 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
 // slot.
 constexpr int kRedThreads = 256;
 struct LinReduceArgs {
-    const float *part;
-    const float *in;        // the caller's rank vectors, by token (part null)
-    int32_t nsp, T, S, L, R, parts;
+    LinVectors job[2];
+    int32_t n_jobs, T, S, L, R;
     const int32_t *idx, *slot_rank;
     const float *scale;
     SegPtrs seg;
-    uint16_t *hl;
-    float *buf;
     int32_t *order;
 };
 
@@ -1067,7 +1094,7 @@ struct LinReduceArgs {
 // the tokens without a slot in token order.  A work-group writes 256 positions
 // of the slots' runs and places its 256 tokens without a slot, whose number
 // before it is counted from idx (a bitmap of the slots in use in LDS).
-__global__ __launch_bounds__(kRedThreads) void k_lin_order(LinReduceArgs a) {
+__device__ __forceinline__ void row_order(const LinReduceArgs &a) {
     constexpr int NW = kRedThreads / 64;
     __shared__ unsigned s_act[kMaxSlots / 32];
     __shared__ int s_cnt[NW], s_before[NW];
@@ -1103,42 +1130,49 @@ __global__ __launch_bounds__(kRedThreads) void k_lin_order(LinReduceArgs a) {
     if (t < run_end) a.order[t] = a.seg.perm[t];
 }
 
-__global__ __launch_bounds__(kRedThreads) void k_lin_reduce(LinReduceArgs a) {
-    const int rq = a.R / 4;                                   // 4 ranks per thread
+// grid.y: a slice of a job, then the row order.
+__global__ __launch_bounds__(kRedThreads) void k_lin_vectors(LinReduceArgs a) {
+    if ((int)blockIdx.y == a.S * a.n_jobs) {
+        if ((int)blockIdx.x * kRedThreads < a.T) row_order(a);
+        return;
+    }
+    const LinVectors &v = a.job[blockIdx.y / a.S];
+    const int s = blockIdx.y % a.S;
+    const unsigned rq = a.R / 4;                              // 4 ranks per thread
     const int64_t q = (int64_t)blockIdx.x * kRedThreads + threadIdx.x;
-    const int s = blockIdx.y;
-    const int64_t i = q / rq;
+    const int64_t i = q < UINT32_MAX ? (int64_t)((unsigned)q / rq) : q / rq;
     const int j = (int)(q - i * rq) * 4;
     if (i >= a.T) return;
     // as a token: buf of tokens without a slot
-    if (a.buf && slot_of_token(a.idx, a.slot_rank, a.L, (int)i) < 0)
-        *reinterpret_cast<floatx4_t *>(a.buf + ((int64_t)s * a.T + i) * a.R + j) = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    if (v.buf && slot_of_token(a.idx, a.slot_rank, a.L, (int)i) < 0)
+        *reinterpret_cast<floatx4_t *>(v.buf + ((int64_t)s * a.T + i) * a.R + j) = floatx4_t{0.f, 0.f, 0.f, 0.f};
     // as a slot-sorted position
     if (i >= a.seg.header[0]) return;
     const int t = a.seg.perm[i];
     const int slot = a.idx[t];
     const int r = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
     floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
-    if (a.part) {
-        for (int k = 0; k < a.nsp; ++k) {
+    if (v.part) {
+#pragma unroll 4
+        for (int k = 0; k < v.nsp; ++k) {
             const floatx4_t o = *reinterpret_cast<const floatx4_t *>(
-                a.part + (((int64_t)s * a.nsp + k) * a.T + i) * a.R + j);
+                v.part + (((int64_t)s * v.nsp + k) * a.T + i) * a.R + j);
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] += o[e];
         }
     } else {
-        sum = *reinterpret_cast<const floatx4_t *>(a.in + ((int64_t)s * a.T + t) * a.R + j);
+        sum = *reinterpret_cast<const floatx4_t *>(v.in + ((int64_t)s * a.T + t) * a.R + j);
     }
     const float sc = a.scale[slot];
     const int64_t row = (int64_t)s * a.T + t;
-    float v[4];
+    float x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (j + e >= r) sum[e] = 0.f;
-        v[e] = j + e < r ? sc * sum[e] : 0.f;
+        x[e] = j + e < r ? sc * sum[e] : 0.f;
     }
-    if (a.hl) store_parts(a.hl + row * a.parts * a.R, a.parts, a.R, j, v);
-    if (a.buf) *reinterpret_cast<floatx4_t *>(a.buf + row * a.R + j) = sum;
+    if (v.hl) store_parts(v.hl + row * v.parts * a.R, v.parts, a.R, j, x);
+    if (v.buf) *reinterpret_cast<floatx4_t *>(v.buf + row * a.R + j) = sum;
 }
 
 // Column tiles of width b by slice; returns their number.
@@ -1177,10 +1211,10 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int NRB, int U>
+template <int CT, int NRB, int U>
 hipError_t run_one(LinArgs a, hipStream_t st) {
-    const int n = column_tiles(a, 16);
-    hipLaunchKernelGGL((k_lin_one<NRB, U>), dim3((unsigned)n), dim3(kFewWaves * 64), 0, st, a);
+    const int n = column_tiles(a, 16 * CT);
+    hipLaunchKernelGGL((k_lin_one<CT, NRB, U>), dim3((unsigned)n), dim3(kFewWaves * 64), 0, st, a);
     return hipGetLastError();
 }
 
@@ -1211,7 +1245,7 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (!gradient && lin_one(a.T, a.R)) return a.R <= 16 ? run_one<1, 8>(a, st) : run_one<2, 4>(a, st);
+    if (!gradient && lin_one(a.T, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
     if (!gradient && a.T <= kLinFewTokens) {
         if (a.T <= 16) return run_few<1, 1, 8>(a, st);
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
@@ -1286,38 +1320,17 @@ hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, c
     return hipGetLastError();
 }
 
-static hipError_t run_reduce(LinReduceArgs a, hipStream_t st) {
-    if (a.order) {
-        hipLaunchKernelGGL(k_lin_order, dim3((unsigned)((a.T + kRedThreads - 1) / kRedThreads)),
-                           dim3(kRedThreads), 0, st, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const int64_t items = (int64_t)a.T * (a.R / 4);
-    const dim3 grid((unsigned)((items + kRedThreads - 1) / kRedThreads), (unsigned)a.S);
-    hipLaunchKernelGGL(k_lin_reduce, grid, dim3(kRedThreads), 0, st, a);
+hipError_t launch_lin_vectors(const LinVectors *jobs, int n_jobs, int32_t T, int32_t S, int32_t L, int32_t R,
+                              const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                              const SegPtrs &seg, int32_t *order, hipStream_t st) {
+    LinReduceArgs a{};
+    for (int i = 0; i < n_jobs; ++i) a.job[i] = jobs[i];
+    a.n_jobs = n_jobs; a.T = T; a.S = S; a.L = L; a.R = R;
+    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg; a.order = order;
+    const int64_t items = (int64_t)T * (R / 4);              // R >= 8: at least T threads
+    const dim3 grid((unsigned)((items + kRedThreads - 1) / kRedThreads), (unsigned)(S * n_jobs + (order ? 1 : 0)));
+    hipLaunchKernelGGL(k_lin_vectors, grid, dim3(kRedThreads), 0, st, a);
     return hipGetLastError();
-}
-
-hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
-                             const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                             const SegPtrs &seg, uint16_t *hl, int32_t parts, float *buf, int32_t *order,
-                             hipStream_t st) {
-    LinReduceArgs a{};
-    a.part = part; a.nsp = nsp; a.T = T; a.S = S; a.L = L; a.R = R;
-    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg;
-    a.hl = hl; a.parts = parts; a.buf = buf; a.order = order;
-    return run_reduce(a, st);
-}
-
-hipError_t launch_lin_split(const float *buf, int32_t T, int32_t S, int32_t L, int32_t R,
-                            const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                            const SegPtrs &seg, uint16_t *hl, int32_t parts, int32_t *order, hipStream_t st) {
-    LinReduceArgs a{};
-    a.in = buf; a.T = T; a.S = S; a.L = L; a.R = R;
-    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale; a.seg = seg;
-    a.hl = hl; a.parts = parts; a.order = order;
-    return run_reduce(a, st);
 }
 
 }  // namespace aa

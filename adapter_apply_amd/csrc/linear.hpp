@@ -61,17 +61,23 @@ bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, in
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,
                              const int32_t *slot_rank, float *buf, hipStream_t st);
-// hl (`parts` parts of scale * sum; and buf, if given) from partial sums
-// [S][nsp][T][R] by slot-sorted position.  order (nullable): receives the row
-// order of the tile GEMM.
-hipError_t launch_lin_reduce(const float *part, int32_t nsp, int32_t T, int32_t S, int32_t L, int32_t R,
-                             const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                             const SegPtrs &seg, uint16_t *hl, int32_t parts, float *buf, int32_t *order,
-                             hipStream_t st);
-// hl from a caller's fp32 rank vectors [S][T][R]; order as above.
-hipError_t launch_lin_split(const float *buf, int32_t T, int32_t S, int32_t L, int32_t R,
-                            const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                            const SegPtrs &seg, uint16_t *hl, int32_t parts, int32_t *order, hipStream_t st);
+// Rank vectors of the tokens that have a slot, from partial sums [S][nsp][T][R]
+// by slot-sorted position or from a buffer [S][T][R] by token: to hl in `parts`
+// bf16 parts of scale * sum, and to buf unscaled (zero for tokens without a
+// slot).  hl, buf nullable.
+struct LinVectors {
+    const float *part;
+    int32_t nsp;
+    const float *in;        // part null
+    uint16_t *hl;
+    int32_t parts;
+    float *buf;
+};
+// One or two of them in one launch, with the row order of the tile GEMM (order,
+// nullable).
+hipError_t launch_lin_vectors(const LinVectors *jobs, int n_jobs, int32_t T, int32_t S, int32_t L, int32_t R,
+                              const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                              const SegPtrs &seg, int32_t *order, hipStream_t st);
 
 // Gradient side (linear_bwd.hip).
 struct PadMap {
@@ -108,7 +114,11 @@ struct LinWgArgs {
 // Partial sums of the token splits stay within this many elements.
 constexpr int64_t kLinWgPartMax = 16 << 20;
 int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *M, int32_t S, int32_t R);
-hipError_t launch_lin_wg(LinWgArgs a, bool transposed, hipStream_t st);
+// Elements of one split's partial sums.
+int64_t lin_wg_part(int32_t L, const int64_t *M, int32_t S, int32_t R);
+// dA (transposed) and dB in one launch, and the sum of their splits in another;
+// either may be null.
+hipError_t launch_lin_wg(const LinWgArgs *dA, const LinWgArgs *dB, hipStream_t st);
 
 // Gradient norm and clip (grad.hip).
 hipError_t launch_grad_norm(const void *const *g, const int64_t *m, int32_t n, int32_t L, int32_t dtype,

@@ -160,16 +160,23 @@ __global__ __launch_bounds__(256) void k_lin_du(DuArgs a) {
 constexpr int kWgCols = 128;
 constexpr int kWgTokens = 1024;       // token indexes staged at a time
 
+template <int RB>
+struct WgLds {
+    static constexpr int kStage = 64 * kWgCols * 2 + kLinPartsBwd * 64 * RB * 2;
+    __attribute__((aligned(16))) char stage[2][kStage];
+    int tok[kWgTokens];
+};
+
 template <int RB, bool TRANSPOSED>
-__global__ __launch_bounds__(256) void k_lin_wg(LinWgArgs a, int nrb) {
+__device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgLds<RB> &sh) {
     constexpr int NP = kLinPartsBwd;
     constexpr int PB = 64 * kWgCols * 2, QB = 64 * RB * 2;      // bytes of a stage's p rows and of one part
     constexpr int CPP = kWgCols / 8, CPQ = RB / 8, RPP = 64 / CPP, RPQ = 64 / CPQ;
     constexpr int PI = PB / 4096, QN = NP * QB / 1024, NB = RB / 16;
-    __shared__ __attribute__((aligned(16))) char s_stage[2][PB + NP * QB];
-    __shared__ int s_tok[kWgTokens];
+    auto &s_stage = sh.stage;
+    auto &s_tok = sh.tok;
     int s = 0;
-    const int mt_all = blockIdx.x / nrb, r0 = (blockIdx.x - mt_all * nrb) * RB;
+    const int mt_all = bx / nrb, r0 = (bx - mt_all * nrb) * RB;
     while (s + 1 < a.S && mt_all >= a.tile_start[s + 1]) ++s;
     const int64_t m0 = (int64_t)(mt_all - a.tile_start[s]) * kWgCols, M = a.m[s];
     const int slot = blockIdx.y;
@@ -265,14 +272,31 @@ __global__ __launch_bounds__(256) void k_lin_wg(LinWgArgs a, int nrb) {
         }
 }
 
-// Sum of the token splits, in order.
-__global__ __launch_bounds__(256) void k_lin_wsum(LinWgArgs a) {
+struct WgJobs {
+    LinWgArgs a, b;      // dA (transposed), dB
+    int32_t na, nrb;     // work-groups of a along x
+};
+template <int RB>
+__global__ __launch_bounds__(256) void k_lin_wg(WgJobs j) {
+    __shared__ WgLds<RB> sh;
+    const int bx = blockIdx.x;
+    if (bx < j.na) {
+        if ((int)blockIdx.z < j.a.nsp) wg_tile<RB, true>(j.a, j.nrb, bx, sh);
+    } else if ((int)blockIdx.z < j.b.nsp) {
+        wg_tile<RB, false>(j.b, j.nrb, bx - j.na, sh);
+    }
+}
+
+// Sum of the token splits, in order (z: dA, dB).
+__global__ __launch_bounds__(256) void k_lin_wsum(WgJobs j) {
+    const LinWgArgs &a = blockIdx.z ? j.b : j.a;
     const int s = blockIdx.y;
     const int64_t q = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (q >= (int64_t)a.L * a.R * a.m[s]) return;
+    if (a.nsp <= 1 || q >= (int64_t)a.L * a.R * a.m[s]) return;
     floatx4_t *dst = reinterpret_cast<floatx4_t *>(a.out[s] + q);
     floatx4_t v = {0.f, 0.f, 0.f, 0.f};
     if (a.accumulate) v = *dst;
+#pragma unroll 4
     for (int k = 0; k < a.nsp; ++k) {
         const floatx4_t o = *reinterpret_cast<const floatx4_t *>(a.part + k * a.part_stride + a.part_off[s] + q);
 #pragma unroll
@@ -283,15 +307,6 @@ __global__ __launch_bounds__(256) void k_lin_wsum(LinWgArgs a) {
 
 int du_rb(int32_t R) { return R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 int wg_rb(int32_t R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
-
-template <bool TRANSPOSED>
-void run_wg(const LinWgArgs &a, int rb, dim3 grid, int nrb, hipStream_t st) {
-    switch (rb) {
-        case 16: hipLaunchKernelGGL((k_lin_wg<16, TRANSPOSED>), grid, dim3(256), 0, st, a, nrb); break;
-        case 32: hipLaunchKernelGGL((k_lin_wg<32, TRANSPOSED>), grid, dim3(256), 0, st, a, nrb); break;
-        default: hipLaunchKernelGGL((k_lin_wg<64, TRANSPOSED>), grid, dim3(256), 0, st, a, nrb); break;
-    }
-}
 
 }  // namespace
 
@@ -360,26 +375,48 @@ int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *M, int32_t S, int32_t
     return k < 1 ? 1 : (int32_t)k;
 }
 
-hipError_t launch_lin_wg(LinWgArgs a, bool transposed, hipStream_t st) {
-    const int rb = wg_rb(a.R), nrb = (a.R + rb - 1) / rb;
-    int c = 0;
-    int64_t off = 0, widest = 0;
-    for (int s = 0; s < a.S; ++s) {
-        a.tile_start[s] = c;
-        c += (int)((a.m[s] + kWgCols - 1) / kWgCols);
-        a.part_off[s] = off;
-        off += (int64_t)a.L * a.R * a.m[s];
-        widest = a.m[s] > widest ? a.m[s] : widest;
+int64_t lin_wg_part(int32_t L, const int64_t *M, int32_t S, int32_t R) {
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) n += (int64_t)L * R * M[s];
+    return n;
+}
+
+hipError_t launch_lin_wg(const LinWgArgs *dA, const LinWgArgs *dB, hipStream_t st) {
+    WgJobs j{};
+    const LinWgArgs &any = dA ? *dA : *dB;
+    const int rb = wg_rb(any.R);
+    j.nrb = (any.R + rb - 1) / rb;
+    int nx = 0, nsp = 1;
+    int64_t widest = 0;
+    auto fill = [&](const LinWgArgs &in, LinWgArgs &a) {
+        a = in;
+        int c = 0;
+        int64_t off = 0;
+        for (int s = 0; s < a.S; ++s) {
+            a.tile_start[s] = c;
+            c += (int)((a.m[s] + kWgCols - 1) / kWgCols);
+            a.part_off[s] = off;
+            off += (int64_t)a.L * a.R * a.m[s];
+            if (a.nsp > 1 && a.m[s] > widest) widest = a.m[s];
+        }
+        for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
+        a.part_stride = off;
+        if (a.nsp > nsp) nsp = a.nsp;
+        nx += c * j.nrb;
+    };
+    if (dA) fill(*dA, j.a);
+    j.na = nx;
+    if (dB) fill(*dB, j.b);
+    const dim3 grid((unsigned)nx, (unsigned)any.L, (unsigned)nsp);
+    switch (rb) {
+        case 16: hipLaunchKernelGGL(k_lin_wg<16>, grid, dim3(256), 0, st, j); break;
+        case 32: hipLaunchKernelGGL(k_lin_wg<32>, grid, dim3(256), 0, st, j); break;
+        default: hipLaunchKernelGGL(k_lin_wg<64>, grid, dim3(256), 0, st, j); break;
     }
-    for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
-    a.part_stride = off;
-    const dim3 grid((unsigned)(c * nrb), (unsigned)a.L, (unsigned)a.nsp);
-    if (transposed) run_wg<true>(a, rb, grid, nrb, st);
-    else run_wg<false>(a, rb, grid, nrb, st);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.nsp == 1) return e;
-    const int64_t units = (int64_t)a.L * a.R * widest / 4;
-    hipLaunchKernelGGL(k_lin_wsum, dim3((unsigned)((units + 255) / 256), (unsigned)a.S), dim3(256), 0, st, a);
+    if (e != hipSuccess || nsp == 1) return e;
+    const int64_t units = (int64_t)any.L * any.R * widest / 4;
+    hipLaunchKernelGGL(k_lin_wsum, dim3((unsigned)((units + 255) / 256), (unsigned)any.S, 2), dim3(256), 0, st, j);
     return hipGetLastError();
 }
 
