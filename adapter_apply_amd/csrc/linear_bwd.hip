@@ -153,24 +153,27 @@ __global__ __launch_bounds__(256) void k_lin_du(DuArgs a) {
 }
 
 // Weight gradients: work-group = (128 columns of a slice, RB ranks, slot,
-// token split), 4 waves of 32 columns, 64 tokens per stage (both operands
+// token split), 4 waves of 32 columns, 32 tokens per stage (both operands
 // through transposed reads; the rank vectors' three bf16 parts, which hold the
 // whole fp32 value, add into the same accumulators).  Slots without tokens
 // write zeros.
 constexpr int kWgCols = 128;
 constexpr int kWgTokens = 1024;       // token indexes staged at a time
+constexpr int kWgStep = 32;           // tokens per stage
+constexpr int kWgStages = 3;
 
 template <int RB>
 struct WgLds {
-    static constexpr int kStage = 64 * kWgCols * 2 + kLinPartsBwd * 64 * RB * 2;
-    __attribute__((aligned(16))) char stage[2][kStage];
+    static constexpr int kStage = kWgStep * kWgCols * 2 + kLinPartsBwd * kWgStep * RB * 2;
+    __attribute__((aligned(16))) char stage[kWgStages][kStage];
     int tok[kWgTokens];
 };
 
 template <int RB, bool TRANSPOSED>
 __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgLds<RB> &sh) {
     constexpr int NP = kLinPartsBwd;
-    constexpr int PB = 64 * kWgCols * 2, QB = 64 * RB * 2;      // bytes of a stage's p rows and of one part
+    constexpr int TK = kWgStep, NST = kWgStages;
+    constexpr int PB = TK * kWgCols * 2, QB = TK * RB * 2;      // bytes of a stage's p rows and of one part
     constexpr int CPP = kWgCols / 8, CPQ = RB / 8, RPP = 64 / CPP, RPQ = 64 / CPQ;
     constexpr int PI = PB / 4096, QN = NP * QB / 1024, NB = RB / 16;
     auto &s_stage = sh.stage;
@@ -185,7 +188,7 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
     int b = a.seg.slot_start[slot], e = a.seg.slot_start[slot + 1];
     {
         // this split's share, in whole stages
-        const int per = ((e - b + a.nsp - 1) / a.nsp + 63) / 64 * 64;
+        const int per = ((e - b + a.nsp - 1) / a.nsp + TK - 1) / TK * TK;
         b = min(b + (int)blockIdx.z * per, e);
         e = min(b + per, e);
     }
@@ -200,7 +203,7 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
         for (int j = 0; j < NB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     for (int cb = b; cb < e; cb += kWgTokens) {
-        const int cnt = min(kWgTokens, e - cb), nst = (cnt + 63) / 64;
+        const int cnt = min(kWgTokens, e - cb), nst = (cnt + TK - 1) / TK;
         __syncthreads();
         for (int i = tid; i < cnt; i += 256) s_tok[i] = a.seg.perm[cb + i];
         __syncthreads();
@@ -208,7 +211,7 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
             const uint32_t pl = lds_addr(&s_stage[stage][0]) + w * 1024, ql = pl + PB;
 #pragma unroll
             for (int i = 0; i < PI; ++i) {
-                const int row = (i * 4 + w) * RPP + lane / CPP, tk = v * 64 + row;
+                const int row = (i * 4 + w) * RPP + lane / CPP, tk = v * TK + row;
                 const int64_t c = m0 + ((lane % CPP) ^ tr_swz<CPP>(row)) * 8;
                 const bool in = tk < cnt && c < M;
                 dma16(pl + i * 4096,
@@ -218,20 +221,31 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
             for (int i = 0; i < (QN + 3) / 4; ++i) {
                 const int q = i * 4 + w;                       // DMA instruction: part, rows
                 if (QN % 4 && q >= QN) break;
-                const int part = q / (QB / 1024), row = (q % (QB / 1024)) * RPQ + lane / CPQ, tk = v * 64 + row;
+                const int part = q / (QB / 1024), row = (q % (QB / 1024)) * RPQ + lane / CPQ, tk = v * TK + row;
                 const int j = r0 + ((lane % CPQ) ^ tr_swz<CPQ>(row)) * 8;
                 const bool in = tk < cnt && j < a.R;
                 dma16(ql + i * 4096,
                       in ? (const void *)(hl + (int64_t)s_tok[in ? tk : 0] * hlr + part * a.R + j) : zero);
             }
         };
-        issue(0, 0);
-        for (int v = 0; v < nst; ++v) {
-            wait_barrier<0>();
-            if (v + 1 < nst) issue(v + 1, (v + 1) & 1);
-            const char *st = s_stage[v & 1];
+        // a wave issues at least kLoads per stage, so waiting for all but
+        // NST - 2 times that many leaves no load of the oldest stage open
+        constexpr int kLoads = PI + QN / 4;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
+        for (int i = 0; i < NST - 1; ++i)
+            if (i < nst) issue(i, i);
+        int stage = 0;
+        for (int v = 0; v < nst; ++v) {
+            if (v + NST - 2 < nst) wait_barrier<(NST - 2) * kLoads>();
+            else wait_barrier<0>();
+            if (v + NST - 1 < nst) {
+                const int ns = stage + NST - 1;
+                issue(v + NST - 1, ns >= NST ? ns - NST : ns);
+            }
+            const char *st = s_stage[stage];
+            if (++stage == NST) stage = 0;
+#pragma unroll
+            for (int kk = 0; kk < TK / 32; ++kk) {
                 bf16x8_t p[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) p[i] = tr_frag<CPP>(st, w * 32 + i * 16, kk, lane);
