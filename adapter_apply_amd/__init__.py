@@ -10,8 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from itertools import repeat
-from operator import attrgetter
+from array import array
 from typing import Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -686,25 +685,31 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
 
 def _check_grads(grads, name):
     """(device index or -1, slots, elements per slot, pointers) of a list of
-    stacked tensors.  A model has hundreds of them, so every check runs over the
-    whole list at once."""
+    stacked tensors; the last two are arrays whose memory the C call reads.  A
+    model has hundreds of tensors, so each attribute is touched once."""
     torch = _torch()
     if len(grads) < 1:
         raise ValueError(f"{name} must hold at least one tensor")
-    Tensor = torch.Tensor
-    dt = grads[0].dtype
-    _need_dtype(grads[0], (torch.float32, torch.bfloat16), f"{name}[0]")
-    if 0 in map(Tensor.dim, grads):
-        raise ValueError(f"{name} must hold tensors stacked over slots")
-    L = grads[0].size(0)
-    if (set(map(attrgetter("dtype"), grads)) != {dt} or not all(map(Tensor.is_contiguous, grads)) or
-            set(map(Tensor.size, grads, repeat(0))) != {L}):
-        raise ValueError(f"{name} must hold contiguous {dt} tensors stacked over {L} slots")
-    m = (_i64 * len(grads))(*[e // L if L else 0 for e in map(Tensor.numel, grads)])
-    devs = set(map(Tensor.get_device, grads))
-    if len(devs) != 1:
+    t = grads[0]
+    _need_dtype(t, (torch.float32, torch.bfloat16), f"{name}[0]")
+    try:
+        dt, dev, L = t.dtype, t.get_device(), t.shape[0]
+        bad = [t for t in grads if t.dtype is not dt or t.get_device() != dev or
+               not t.is_contiguous() or t.shape[0] != L]
+    except IndexError:
+        raise ValueError(f"{name} must hold tensors stacked over slots") from None
+    if L < 1:
+        raise ValueError(f"{name} must hold tensors of at least one slot")
+    if bad:
         _need_device(grads)
-    return devs.pop(), L, m, (_vp * len(grads))(*map(Tensor.data_ptr, grads))
+        raise ValueError(f"{name} must hold contiguous {dt} tensors stacked over {L} slots (got "
+                         f"{bad[0].dtype} {list(bad[0].shape)})")
+    return (dev, L, array("q", [t.numel() // L for t in grads]),
+            array("Q", [t.data_ptr() for t in grads]))
+
+
+def _addr(a):
+    return a.buffer_info()[0]
 
 
 def lora_grad_workspace_size(m: Sequence[int], L: int) -> int:
@@ -715,7 +720,7 @@ def lora_grad_workspace_size(m: Sequence[int], L: int) -> int:
 
 
 def alloc_grad_workspace(grads: Sequence, device=None):
-    """Workspace of lora_grad_norm over these tensors."""
+    """A zero-filled workspace of lora_grad_norm over these tensors."""
     _, L, m, _ = _check_grads(grads, "grads")
     return _aligned_ws(lora_grad_workspace_size(m, L), device or grads[0].device)
 
@@ -727,7 +732,7 @@ def lora_grad_norm(norm, grads: Sequence, ws, stream=None):
     _check_ws(ws)
     if _one_device((norm, ws)) != dev:
         _need_device((norm, grads[0], ws))
-    _call("lora_grad_norm", dev, stream, _ptr(norm), ptrs, m, len(m), L, _dtype_code(grads[0]),
+    _call("lora_grad_norm", dev, stream, _ptr(norm), _addr(ptrs), _addr(m), len(m), L, _dtype_code(grads[0]),
           _ptr(ws), ws.nbytes)
 
 
@@ -737,11 +742,11 @@ def lora_grad_clip(out: Sequence, grads: Sequence, norm, max_norm, stream=None):
     torch = _torch()
     dev, L, m, ptrs = _check_grads(grads, "grads")
     odev, Lo, mo, optrs = (dev, L, m, ptrs) if out is grads else _check_grads(out, "out")
-    if Lo != L or len(mo) != len(m) or bytes(mo) != bytes(m) or out[0].dtype != grads[0].dtype:
+    if Lo != L or mo != m or out[0].dtype != grads[0].dtype:
         raise ValueError("out must match grads in number, sizes and dtype")
     _need_vec(norm, L, torch.float32, "norm")
     _need_vec(max_norm, L, torch.float32, "max_norm")
     if _one_device((norm, max_norm)) != dev or odev != dev:
         _need_device((norm, max_norm, grads[0], out[0]))
-    _call("lora_grad_clip", dev, stream, optrs, ptrs, m, len(m), L, _ptr(norm), _ptr(max_norm),
+    _call("lora_grad_clip", dev, stream, _addr(optrs), _addr(ptrs), _addr(m), len(m), L, _ptr(norm), _ptr(max_norm),
           _dtype_code(grads[0]))

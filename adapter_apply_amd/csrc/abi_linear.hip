@@ -330,7 +330,7 @@ lora_status_t lora_grad_workspace_size(const int64_t *m, int32_t n, int32_t L, s
     if (n < 0 || L < 1 || L > LORA_MAX_SLOTS) return LORA_E_SHAPE;
     const int64_t items = grad_items(m, n, L);
     if (items < 0) return LORA_E_SHAPE;
-    *bytes = align256(sizeof(double) * (size_t)(items > 0 ? items : 1));
+    *bytes = kGradCountBytes + align256(sizeof(double) * (size_t)items);
     return LORA_OK;
 }
 
@@ -342,7 +342,8 @@ lora_status_t lora_grad_norm(float *norm, const void *const *g, const int64_t *m
     size_t need = 0;
     CHECK(lora_grad_workspace_size(m, n, L, &need));
     CHECK(check_ws(ws, ws_bytes, need));
-    return launched(launch_grad_norm(g, m, n, L, dtype, static_cast<double *>(ws), norm,
+    double *part = reinterpret_cast<double *>(static_cast<char *>(ws) + kGradCountBytes);
+    return launched(launch_grad_norm(g, m, n, L, dtype, static_cast<int32_t *>(ws), part, norm,
                                      static_cast<hipStream_t>(stream)));
 }
 

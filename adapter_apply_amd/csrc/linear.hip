@@ -1110,7 +1110,7 @@ __device__ __forceinline__ void row_order(const LinReduceArgs &a) {
     __syncthreads();
     auto none = [&](int s) { return s < 0 || s >= a.L || !(s_act[s >> 5] >> (s & 31) & 1); };
     int before = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < base; i += kRedThreads) before += none(a.idx[i]);
     for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
     const bool mine = t < a.T && none(a.idx[t]);

@@ -122,7 +122,9 @@ hipError_t launch_lin_wg(const LinWgArgs *dA, const LinWgArgs *dB, hipStream_t s
 
 // Gradient norm and clip (grad.hip).
 hipError_t launch_grad_norm(const void *const *g, const int64_t *m, int32_t n, int32_t L, int32_t dtype,
-                            double *part, float *norm, hipStream_t st);
+                            int32_t *count, double *part, float *norm, hipStream_t st);
+// Bytes of the workspace's counts, before its partial sums.
+constexpr size_t kGradCountBytes = sizeof(int32_t) * kMaxSlots;
 hipError_t launch_grad_clip(void *const *out, const void *const *g, const int64_t *m, int32_t n,
                             int32_t L, const float *norm, const float *max_norm, int32_t dtype,
                             hipStream_t st);

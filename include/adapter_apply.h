@@ -484,7 +484,9 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
  *         (faster when rows start at 16-byte addresses).
  * ------------------------------------------------------------------------ */
 
-/* Workspace bytes of lora_grad_norm; its contents need no preparation. */
+/* Workspace bytes of lora_grad_norm: 256-byte aligned, zero-filled once by
+ * lora_workspace_init (every call leaves its counts zero), calls that share it
+ * ordered on one stream, not shared with other entry points. */
 lora_status_t lora_grad_workspace_size(const int64_t *m, int32_t n, int32_t L, size_t *bytes);
 
 /* norm[l] = sqrt(sum over i, e < m[i] of g[i][l][e]^2), summed in 64 bits in a

@@ -140,7 +140,7 @@ def test_workspace_size_refusals():
     assert size(1, 0, i64(64), 1, 16, 4, C.byref(n)) == aa.LORA_E_SHAPE
     assert size(0, 64, i64(64), 1, 16, 4, C.byref(n)) == aa.LORA_OK
     gsize = aa.lib().lora_grad_workspace_size
-    assert gsize(i64(5, 0), 2, 3, C.byref(n)) == aa.LORA_OK and n.value == 256
+    assert gsize(i64(5, 0), 2, 3, C.byref(n)) == aa.LORA_OK and n.value % 256 == 0 and n.value > 0
     assert gsize(i64(-1), 1, 3, C.byref(n)) == aa.LORA_E_SHAPE
     assert gsize(i64(1), 1, 0, C.byref(n)) == aa.LORA_E_SHAPE
     assert gsize(None, 1, 1, C.byref(n)) == aa.LORA_E_NULL
@@ -271,7 +271,8 @@ def test_binding_refuses_cpu_tensors():
 
 @pytest.mark.parametrize("grads", [
     [], [torch.zeros(L, 8, dtype=torch.float16)], [torch.zeros(L, 8), torch.zeros(L + 1, 8)],
-    [torch.zeros(L, 8), torch.zeros(L, 8, dtype=BF)], [torch.zeros(8, L).T]], ids=range(5))
+    [torch.zeros(L, 8), torch.zeros(L, 8, dtype=BF)], [torch.zeros(8, L).T],
+    [torch.zeros(())], [torch.zeros(L, 8), torch.zeros(())], [torch.zeros(0, 8)]], ids=range(8))
 def test_grad_binding_refuses(grads):
     with pytest.raises(ValueError):
         aa.lora_grad_norm(torch.zeros(L), grads, torch.zeros(256, dtype=torch.uint8))
