@@ -11,6 +11,10 @@
 // of the fp32 buffer's, well below the bf16 rounding of the output.
 #include "linear.hpp"
 
+#ifndef LIN_RF
+#define LIN_RF 2
+#define LIN_R2 6
+#endif
 namespace aa {
 
 namespace {
@@ -327,33 +331,46 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         next_slice();
         if (v + NST < nk && rem >= BK) {
             bf16x8_t fq[2][NB], fp[2][MB];
-            auto mfmas = [&](int set, int j) {
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[set][i], fp[set][j], acc[i][j], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
+            // One MFMA, then item n of what goes beside the MFMAs: single reads and
+            // DMA instructions between single MFMAs, since a clump of them is longer
+            // than an MFMA runs.
+            auto mfma1 = [&](int set, int n) __attribute__((always_inline)) {
+                const int j = n / NB, i = n % NB;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[set][i], fp[set][j], acc[i][j], 0, 0, 0);
             };
-            // share j of n of a fragment set's reads
-            auto reads = [&](int set, const char *st, int kk, int j, int n) {
-#pragma unroll
-                for (int i = j * MB / n; i < (j + 1) * MB / n; ++i) fp[set][i] = pfrag(st, i, kk);
-#pragma unroll
-                for (int i = j * NB / n; i < (j + 1) * NB / n; ++i) fq[set][i] = qfrag(st, i, kk);
+            // a fragment set's reads: first the Q fragments, which every MFMA group
+            // of the next half needs, then the P fragments
+            auto read1 = [&](int set, const char *st, int kk, int i) __attribute__((always_inline)) {
+                if (i < NB) fq[set][i] = qfrag(st, i, kk);
+                else fp[set][i - NB] = pfrag(st, i - NB, kk);
             };
-            constexpr int RG = MB / 4 > 0 ? MB / 4 : 1;   // MFMA groups that carry the second set's reads
-            constexpr int LG = MB - RG - (MB > 4);        // and a tile's DMA
-            reads(0, stage_ptr(v), 0, 0, 1);
+            auto load1 = [&](uint32_t pl, int i) __attribute__((always_inline)) {
+                if (i < PI) dma16(pl + i * NW * 1024, pptr[i] + po);
+                else dma16(pl + PB + (i - PI) * NW * 1024, qptr[i - PI] + qo);
+            };
+            constexpr int M = MB * NB, RD = NB + MB, LD = PI + QI;
+            constexpr int M1 = M * LIN_RF / 8;            // MFMAs beside the first half's reads
+            constexpr int M2 = M - M1;                    // and its DMA
+            constexpr int M3 = M * LIN_R2 / 8;            // MFMAs beside the second half's reads
+#pragma unroll
+            for (int i = 0; i < RD; ++i) read1(0, stage_ptr(v), 0, i);
             do {
                 const char *st = stage_ptr(v);
                 const uint32_t pl = lds0 + (v % NST) * (PB + QB);
                 // first half: the stage's second fragment set, after which the
                 // stage is free for the tile NST ahead
 #pragma unroll
-                for (int j = 0; j < MB; ++j) {
-                    if (j < RG) reads(1, st, 1, j, RG);
-                    if (j == RG) meet_reads();
-                    if (j >= RG && j < RG + LG) loads(pl, j - RG, LG);
-                    mfmas(0, j);
+                for (int n = 0; n < M; ++n) {
+                    if (n < M1) {
+#pragma unroll
+                        for (int i = n * RD / M1; i < (n + 1) * RD / M1; ++i) read1(1, st, 1, i);
+                    } else {
+                        if (n == M1) meet_reads();
+#pragma unroll
+                        for (int i = (n - M1) * LD / M2; i < (n - M1 + 1) * LD / M2; ++i) load1(pl, i);
+                    }
+                    mfma1(0, n);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 advance();
                 ++v;
@@ -361,9 +378,13 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
                 // second half: the next tile's first set
                 const char *nx = stage_ptr(v);
 #pragma unroll
-                for (int j = 0; j < MB; ++j) {
-                    reads(0, nx, 0, j, MB);
-                    mfmas(1, j);
+                for (int n = 0; n < M; ++n) {
+                    if (n < M3) {
+#pragma unroll
+                        for (int i = n * RD / M3; i < (n + 1) * RD / M3; ++i) read1(0, nx, 0, i);
+                    }
+                    mfma1(1, n);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             } while (v + NST < nk && rem >= BK);
         }
