@@ -16,7 +16,7 @@ inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 // one-launch segment build, which needs them zero and leaves them zero.
 struct LinWs {
     SegLayout seg;
-    size_t order;       // int32 [T]: row order of the tile GEMM
+    size_t order;       // int32 [2][T]: row order of the tile GEMM and the rows' slots
     size_t hl_u;        // bf16 [S][T][kLinPartsBwd R]: scale * u in parts
     size_t hl_v;        // the same of v
     size_t part;        // fp32 partial sums
@@ -31,7 +31,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     w.seg = seg_layout(T, L);
     size_t o = w.seg.end;
     const size_t tsr = (size_t)T * S * R;
-    w.order = o; o = align256(o + sizeof(int32_t) * (size_t)T);
+    w.order = o; o = align256(o + 2 * sizeof(int32_t) * (size_t)T);
     w.hl_u = o;  o = align256(o + 2 * kLinPartsBwd * tsr);
     w.hl_v = o;  o = align256(o + 2 * kLinPartsBwd * tsr);
     w.part = o;

@@ -11,10 +11,6 @@
 // of the fp32 buffer's, well below the bf16 rounding of the output.
 #include "linear.hpp"
 
-#ifndef LIN_RF
-#define LIN_RF 2
-#define LIN_R2 6
-#endif
 namespace aa {
 
 namespace {
@@ -95,7 +91,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         const int m = m0 + i;
         const int pos = min(m, a.T - 1);
         const int t = a.order ? a.order[pos] : pos;
-        const int sl = m >= a.T ? -2 : MIXED && a.join_delta ? -1 : slot_of_token(a.idx, a.slot_rank, a.L, t);
+        int sl = -2;
+        if (m < a.T)
+            sl = MIXED && a.join_delta ? -1 : a.order ? a.order[a.T + pos] : slot_of_token(a.idx, a.slot_rank, a.L, t);
         s_tok[i] = t;
         s_slot[i] = sl;
         // MIXED: every slot; else the slots that have a 16-token block of their own
@@ -349,9 +347,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
                 else dma16(pl + PB + (i - PI) * NW * 1024, qptr[i - PI] + qo);
             };
             constexpr int M = MB * NB, RD = NB + MB, LD = PI + QI;
-            constexpr int M1 = M * LIN_RF / 8;            // MFMAs beside the first half's reads
+            constexpr int M1 = M / 4;                     // MFMAs beside the first half's reads
             constexpr int M2 = M - M1;                    // and its DMA
-            constexpr int M3 = M * LIN_R2 / 8;            // MFMAs beside the second half's reads
+            constexpr int M3 = M * 3 / 4;                 // MFMAs beside the second half's reads
 #pragma unroll
             for (int i = 0; i < RD; ++i) read1(0, stage_ptr(v), 0, i);
             do {
@@ -446,28 +444,37 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
                 for (int i = 0; i < NB; ++i) t[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
                 for (int s = NN ? 0 : sc; s < (NN ? a.S : sc + 1); ++s) {
                     const uint16_t *hl = a.hl + ((int64_t)s * a.T + s_tok[row]) * a.hl_row;
-                    for (int k0 = 0; k0 < 2 * a.R; k0 += 32) {
-                        const int k = k0 + g * 8, kr = k < a.R ? k : k - a.R;
-                        uint4 p = make_uint4(0, 0, 0, 0);
-                        if (mine && k < 2 * a.R) p = ldg<uint4>(hl + k);
+                    constexpr int KU = NN ? 1 : 4;            // steps whose loads are in flight together
+                    const int r8 = ((a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R) + 7) & ~7;
+                    for (int k0 = 0; k0 < 2 * r8; k0 += 32 * KU) {
+                        uint4 p[KU], q[KU][NB];
 #pragma unroll
-                        for (int i = 0; i < NB; ++i) {
-                            const int64_t n = min(c0 + (wn * NB + i) * 16 + l16, cend - 1);
-                            uint4 q = make_uint4(0, 0, 0, 0);
-                            if (k < 2 * a.R) {
+                        for (int u = 0; u < KU; ++u) {
+                            const int k = k0 + u * 32 + g * 8, kr = k < r8 ? k : k - r8;
+                            const bool in = k < 2 * r8;
+                            p[u] = mine && in ? ldg<uint4>(hl + (k < r8 ? k : kr + a.R)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < NB; ++i) {
+                                const int64_t n = min(c0 + (wn * NB + i) * 16 + l16, cend - 1);
+                                q[u][i] = make_uint4(0, 0, 0, 0);
+                                if (!in) continue;
                                 if (NN) {
                                     const uint16_t *c = a.lora[s] + ((int64_t)slot * a.R + kr) * a.K + n;
                                     uint32_t v[8];
 #pragma unroll
                                     for (int e = 0; e < 8; ++e) v[e] = c[(int64_t)e * a.K];
-                                    q = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
-                                                   v[6] | v[7] << 16);
+                                    q[u][i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                                                         v[6] | v[7] << 16);
                                 } else {
-                                    q = ldg<uint4>(a.lora[s] + ((int64_t)slot * cend + n) * a.R + kr);
+                                    q[u][i] = ldg<uint4>(a.lora[s] + ((int64_t)slot * cend + n) * a.R + kr);
                                 }
                             }
-                            t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(q), frag(p), t[i], 0, 0, 0);
                         }
+#pragma unroll
+                        for (int u = 0; u < KU; ++u)
+#pragma unroll
+                            for (int i = 0; i < NB; ++i)
+                                t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(q[u][i]), frag(p[u]), t[i], 0, 0, 0);
                     }
                 }
 #pragma unroll
@@ -1112,7 +1119,7 @@ struct LinReduceArgs {
 };
 
 // The row order of the tile GEMM: each slot's tokens, slots ascending, then
-// the tokens without a slot in token order.  A work-group writes 256 positions
+// the tokens without a slot in token order; and each row's slot (or -1) after it.  A work-group writes 256 positions
 // of the slots' runs and places its 256 tokens without a slot, whose number
 // before it is counted from idx (a bitmap of the slots in use in LDS).
 __device__ __forceinline__ void row_order(const LinReduceArgs &a) {
@@ -1147,8 +1154,13 @@ __device__ __forceinline__ void row_order(const LinReduceArgs &a) {
         for (int i = 0; i < NW; ++i) pos += s_before[i];
         for (int i = 0; i < w; ++i) pos += s_cnt[i];
         a.order[pos] = t;
+        a.order[a.T + pos] = -1;
     }
-    if (t < run_end) a.order[t] = a.seg.perm[t];
+    if (t < run_end) {
+        const int tok = a.seg.perm[t];
+        a.order[t] = tok;
+        a.order[a.T + t] = a.idx[tok];
+    }
 }
 
 // grid.y: a slice of a job, then the row order.

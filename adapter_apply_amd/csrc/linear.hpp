@@ -19,7 +19,7 @@ struct LinArgs {
     int64_t ldo;
     const uint16_t *hl;       // bf16 [S][T][hl_row]: scaled rank vectors' parts (the first two are used)
     int32_t hl_row;           // kLinParts* R
-    const int32_t *order;     // row -> token, slot-sorted, or null (identity)
+    const int32_t *order;     // [T] row -> token, slot-sorted, then [T] the rows' slots; or null (token order)
     const int32_t *idx;
     const int32_t *slot_rank;
     int32_t T, K, S, L, R;
