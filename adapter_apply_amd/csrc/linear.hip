@@ -249,29 +249,35 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         const int slot = __builtin_amdgcn_readfirstlane(s_list[ld.d]), r8 = __builtin_amdgcn_readfirstlane(s_r8[ld.d]);
         step(ld);
         const int pj = c * BK + plc * 8;
-        const uint16_t *hl = a.hl + (int64_t)s * a.T * a.hl_row;
+        const uint16_t *hl = a.hl + (int64_t)s * a.T * a.hl_row + (pj < r8 ? pj : pj - r8 + R);
+        const bool pin = pj < 2 * r8;
 #pragma unroll
         for (int i = 0; i < PI; ++i) {
             const int row = prow0 + i * (NW * 64 / UP);
-            const bool in = s_slot[row] == slot && pj < 2 * r8;
+            const bool in = s_slot[row] == slot && pin;
             dma16(pl + i * NW * 1024,
-                  in ? (const void *)(hl + (int64_t)s_tok[row] * a.hl_row + (pj < r8 ? pj : pj - r8 + R)) : zero);
+                  in ? (const void *)(hl + (uint64_t)(unsigned)s_tok[row] * (unsigned)a.hl_row) : zero);
         }
-        const uint16_t *lo = a.lora[s];
+        // (32-bit lane offsets from scalar bases)
+        if (NN) {
+            const uint16_t *lo = a.lora[s] + (int64_t)slot * R * a.K + c0;
+            const int cmax = (int)min(cend - c0, (int64_t)BN) - 8;
 #pragma unroll
-        for (int i = 0; i < QI; ++i) {
-            const void *src = zero;
-            if (NN) {
-                const int j2 = c * BK + qrow(i);
-                const int64_t col = c0 + qlc(i) * 8;
-                if (j2 < 2 * r8)
-                    src = lo + ((int64_t)slot * R + (j2 < r8 ? j2 : j2 - r8)) * a.K + (col < cend ? col : 0);
-            } else {
-                const int j2 = c * BK + qlc(i) * 8;
-                const int64_t n = min(c0 + qrow(i), cend - 1);
-                if (j2 < 2 * r8) src = lo + ((int64_t)slot * cend + n) * R + (j2 < r8 ? j2 : j2 - r8);
+            for (int i = 0; i < QI; ++i) {
+                const int j2 = c * BK + qrow(i), col = qlc(i) * 8;
+                const unsigned j = j2 < r8 ? j2 : j2 - r8;
+                dma16(ql + i * NW * 1024,
+                      j2 < 2 * r8 ? (const void *)(lo + (uint64_t)j * (unsigned)a.K + (col <= cmax ? col : 0)) : zero);
             }
-            dma16(ql + i * NW * 1024, src);
+        } else {
+            const uint16_t *lo = a.lora[s] + ((int64_t)slot * cend + c0) * R;
+            const int rmax = (int)min(cend - c0, (int64_t)BN) - 1;
+            const int j2 = c * BK + qlc(0) * 8;              // the same unit in each of a lane's rows
+            lo += j2 < r8 ? j2 : j2 - r8;
+#pragma unroll
+            for (int i = 0; i < QI; ++i)
+                dma16(ql + i * NW * 1024,
+                      j2 < 2 * r8 ? (const void *)(lo + min(qrow(i), rmax) * R) : zero);
         }
     };
 
