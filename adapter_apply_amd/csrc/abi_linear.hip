@@ -286,8 +286,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
             wb.m[s] = N[s];
             wb.poff[s] = poff[s];
         }
-        wa.nsp = lin_wg_splits(T, L, wa.m, S, R);
-        wb.nsp = lin_wg_splits(T, L, N, S, R);
+        wa.nsp = wb.nsp = lin_wg_splits(T, L, dA ? wa.m : nullptr, dB ? N : nullptr, S, R);
         wa.part = part;
         wb.part = part + (dA && wa.nsp > 1 ? wa.nsp * lin_wg_part(L, wa.m, S, R) : 0);
         CHECK(launched(launch_lin_wg(dA ? &wa : nullptr, dB ? &wb : nullptr, st)));

@@ -113,7 +113,8 @@ struct LinWgArgs {
 };
 // Partial sums of the token splits stay within this many elements.
 constexpr int64_t kLinWgPartMax = 16 << 20;
-int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *M, int32_t S, int32_t R);
+// MA, MB: the slices' columns of dA and dB (nullable).
+int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *MA, const int64_t *MB, int32_t S, int32_t R);
 // Elements of one split's partial sums.
 int64_t lin_wg_part(int32_t L, const int64_t *M, int32_t S, int32_t R);
 // dA (transposed) and dB in one launch, and the sum of their splits in another;

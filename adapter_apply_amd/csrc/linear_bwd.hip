@@ -371,19 +371,24 @@ hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, 
     return hipGetLastError();
 }
 
-// Token splits while the (column tile, rank block, slot) work-groups are few:
-// about 1024 work-groups, splits of at least 256 tokens on average, partial
-// sums within kLinWgPartMax elements.
-int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *M, int32_t S, int32_t R) {
-    if (L > T) return 1;
+// Token splits while the (column tile, rank block, slot) work-groups of both
+// gradients are few: about 1024 work-groups, splits of at least 256 of a slot's
+// tokens on average (shorter ones cost their launch more than they save: 1501
+// tokens over 7 slots, 1652 x 1352, rank 40: 81 us with three splits, 74
+// without), partial sums within kLinWgPartMax elements each.
+int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *MA, const int64_t *MB, int32_t S, int32_t R) {
     int64_t tiles = 0, cols = 0;
-    for (int s = 0; s < S; ++s) {
-        tiles += (M[s] + kWgCols - 1) / kWgCols;
-        cols += M[s];
+    for (const int64_t *M : {MA, MB}) {
+        int64_t c = 0;
+        for (int s = 0; M && s < S; ++s) {
+            tiles += (M[s] + kWgCols - 1) / kWgCols;
+            c += M[s];
+        }
+        if (c > cols) cols = c;
     }
     const int rb = wg_rb(R);
     int64_t k = 1024 / (tiles * L * ((R + rb - 1) / rb));
-    if (k > T / 256) k = T / 256;
+    if (k > T / L / 256) k = T / L / 256;
     if (k > 16) k = 16;
     while (k > 1 && k * L * R * cols > kLinWgPartMax) --k;
     return k < 1 ? 1 : (int32_t)k;

@@ -37,7 +37,8 @@ SHAPES = [
     (2100, 136, (5000, 700), 64, 300, 0),
     (2100, 1032, (5000, 260), 16, 4, 0),   # 256-wide forward tiles
     (2100, 5640, (100, 36), 72, 12, 4),    # 256-wide gradient tiles
-    (4500, 64, (60,), 16, 2, 0),
+    (4500, 64, (60,), 16, 2, 0),           # token splits of the weight gradients
+    (9000, 72, (20, 12), 40, 1, 4),
 ]
 
 
