@@ -304,13 +304,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         return frag(*reinterpret_cast<const uint4 *>(st + PB + row * (BK * 2) + (((kk * 4 + g) ^ pswz(row)) << 4)));
     };
     auto stage_ptr = [&](int v) { return s_stage + (v % NST) * (PB + QB); };
-    // Tile v's reads are done: wait for tile v + 1 (the tiles after it may
-    // stay in flight) and meet.
     auto meet_reads = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
-    auto meet = [&](int v) {
-        if (v + NST - 1 < nv) wait_barrier<(NST - 2) * (PI + QI)>();
-        else wait_barrier<0>();
-    };
 
     auto loads = [&](uint32_t pl, int j, int n) __attribute__((always_inline)) {
         // share j of n of a whole base tile's DMA
@@ -397,37 +391,45 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         const bool base = v < nk;
         const int slot = base ? 0 : __builtin_amdgcn_readfirstlane(s_list[use.d]);
         if (!base) step(use);
+        bf16x8_t q[KK][NB], p[KK][MB];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            bf16x8_t q[NB], p[MB];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) q[i] = qfrag(st, i, kk);
+            for (int i = 0; i < NB; ++i) q[kk][i] = qfrag(st, i, kk);
 #pragma unroll
-            for (int j = 0; j < MB; ++j) p[j] = pfrag(st, j, kk);
+            for (int j = 0; j < MB; ++j) p[kk][j] = pfrag(st, j, kk);
+        }
+        // the stage is free for the tile NST ahead
+        if (v + 1 < nv) {
+            meet_reads();
+            if (v + NST < nv) issue(v + NST, v % NST);
+        }
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-                const int rs = s_slot[(wm * MB + j) * 16 + (MIXED ? l16 : 0)];
-                const bool mine = base || (rs == slot && (MIXED || s_whole[wm * MB + j]));
-                if (__ballot(mine) == 0) continue;
-                if (!MIXED || __ballot(!mine && rs != -2) == 0) {
+        for (int j = 0; j < MB; ++j) {
+            const int rs = s_slot[(wm * MB + j) * 16 + (MIXED ? l16 : 0)];
+            const bool mine = base || (rs == slot && (MIXED || s_whole[wm * MB + j]));
+            if (__ballot(mine) == 0) continue;
+            if (!MIXED || __ballot(!mine && rs != -2) == 0) {
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
                     for (int i = 0; i < NB; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p[j], acc[i][j], 0, 0, 0);
-                } else {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[kk][i], p[kk][j], acc[i][j], 0, 0, 0);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const floatx4_t z = {0.f, 0.f, 0.f, 0.f};
-                        const floatx4_t t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[i], p[j], z, 0, 0, 0);
+                for (int i = 0; i < NB; ++i) {
+                    floatx4_t t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
-                    }
+                    for (int kk = 0; kk < KK; ++kk)
+                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[kk][i], p[kk][j], t, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = mine ? acc[i][j][e] + t[e] : acc[i][j][e];
                 }
             }
         }
-        if (v + 1 < nv) {
-            meet(v);
-            if (v + NST < nv) issue(v + NST, v % NST);
-        }
+        // tile v + 1 has landed
+        if (v + NST < nv) wait_barrier<(NST - 1) * (PI + QI)>();
+        else wait_barrier<0>();
     }
 
     // 16-token blocks that hold several slots: each slot's part from global
