@@ -92,13 +92,6 @@ SegPtrs lin_seg(void *ws, size_t ws_bytes, const LinWs &w, int32_t T, int32_t L)
     return seg;
 }
 
-// Direct batches whose rank vectors the slot-grouped kernels find (more than
-// one launch of k_lin_few takes, whole 64-column steps, in-kernel discovery).
-bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L) {
-    return T > kLinFewTokens && grp_discovers(T, L) && R % 16 == 0 && R <= kGrpMaxPartialRank && K % 64 == 0 &&
-           grp_kchunks(K) <= kMaxKcGrp;
-}
-
 // x A^T by slot-sorted position in the workspace's partial sums; returns the
 // number of K splits.
 lora_status_t sorted_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl, int32_t S,
@@ -149,10 +142,10 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     float *u = buf, *clear = nullptr;
     // fp32 rank vectors by token, in buf if it is wanted
     if (join && !u) u = reinterpret_cast<float *>(wp + wl.hl_u);
-    if (lin_one(T, R)) {
+    if (lin_one(T, N, S, R)) {
         clear = buf;
     } else if (direct) {
-        if (lin_grouped(T, K, R, L)) {
+        if (lin_grouped(T, K, N, S, R, L)) {
             float *part = reinterpret_cast<float *>(wp + wl.part);
             CHECK(launched(launch_grp_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, part, nullptr, nullptr, st)));
             CHECK(launched(launch_grp_reduce(T, S, L, R, idx, slot_rank, part, grp_kchunks(K), u, nullptr, st)));

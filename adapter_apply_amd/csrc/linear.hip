@@ -1286,16 +1286,23 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (!gradient && lin_one(a.T, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
-    if (!gradient && a.T <= kLinFewTokens) {
-        if (a.T <= 16) return run_few<1, 1, 8>(a, st);
+    if (!gradient && lin_one(a.T, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
+    if (!gradient && lin_few(a.T, a.K, a.n, a.S)) {
+        // (a round of eight steps is 4096 of K, and steps past K load too: 2048
+        // columns of K 2048, 16 tokens: 13.2 us with four steps, 16.5 with eight)
+        if (a.T <= 16) return a.K > 2048 ? run_few<1, 1, 8>(a, st) : run_few<1, 1, 4>(a, st);
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
         return run_few<4, 2, 2>(a, st);
     }
     if (!a.join_delta && a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
         return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
     // Few tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
-    // each), joined by a second launch.
+    // each), joined by a second launch.  Tiles of 64 x 64 read each operand
+    // twice as often, which shows once all their K tiles together pass some
+    // 20000 (256 tokens, K x N: 2048 x 2048 26.1 against 27.6 us with 128 x 128,
+    // 4096 x 4096 46.3 against 49.0, 4096 x 6144 49.1 against 46.8, 14336 x 4096
+    // 86.9 against 79.5), or once they no longer run at the same time (the gradient
+    // of 1501 tokens, 1652 x 1352, 528 of them: 61.4 against 53.1).
     int64_t nk = (a.K + 63) / 64;
     if (gradient) {
         nk = 0;
@@ -1310,38 +1317,82 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     };
     const int64_t t128 = tiles(a.T, a.K, a.n, a.S, gradient, 128), t64 = tiles(a.T, a.K, a.n, a.S, gradient, 64);
     if (t128 >= 192) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, 1, st);
-    if (t128 * splits(t128) >= kLinSplitTiles / 2)
+    if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 20480))
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, splits(t128), st);
     return run_tile<64, 64, 2, 2, 4, true>(a, gradient, splits(t64), st);
 }
 
 // Whether a sorted forward batch leaves the delta to the join: when the
 // rank-vector K tiles that a 128-token tile is expected to meet (its share of
-// the slots, and one for a slot that continues) pass an eighth of its base K
-// tiles, and the fp32 sums stay within kLinJoinMax.  (1024 tokens over 128
-// slots of ranks up to 128, 8192 x 8192: see k_lin_join's figures in the
-// table of the layer cases.)
+// the slots, and one for a slot that continues) pass a share of its base K
+// tiles, and the fp32 sums stay within kLinJoinMax.  The share is larger where
+// writing and reading the sums weighs more than a few tiles' tail.  With the
+// delta in the tiles against the join, K 4096, share in brackets: 512 tokens,
+// 6144 columns, rank 64, 32 slots [.28] 99.8 against 82.3 us, rank 128, 16
+// slots [.31] 99.8 against 85.3; 1024 tokens, 4096 columns, rank 128, 16 slots
+// [.19] 89.6 against 94.2; 2048 tokens, 4096 columns, rank 128, 64 slots [.31]
+// 148 against 154; K 8192, 1024 tokens, 8192 columns, rank 128, 128 slots
+// [.53] 343 against 309.
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     int64_t n = 0;
     for (int s = 0; s < S; ++s) n += N[s];
+    if ((int64_t)T * n > kLinJoinMax || (T + kJoinRows - 1) / kJoinRows > 65535) return false;
     const double slots = 128.0 * (T < L ? T : L) / T + 1.0;
-    return slots * ((2 * R + 63) / 64) > K / 64 / 8.0 && (int64_t)T * n <= kLinJoinMax;
+    return slots * ((2 * R + 63) / 64) > K / 64 * ((int64_t)T * n <= 1 << 22 ? 0.25 : 0.4);
 }
 
-// One token of rank at most 32 takes the one launch of k_lin_one.
-bool lin_one(int32_t T, int32_t R) { return T == 1 && R <= 32; }
+// One token of rank at most 32 takes the one launch of k_lin_one, while its
+// work-groups, each reading the slot's lora_a rows, are not too many.  Against
+// k_lin_shrink and k_lin_few, us: K 4096, 6144 columns 16.6 and 21.8 at rank 16,
+// 19.9 and 22.3 at rank 32; 16384 columns 29.7 and 31.5 at rank 8, 36.7 and 33.7
+// at rank 32; 28672 columns 52.4 and 47.5.
+bool lin_one(int32_t T, const int64_t *N, int32_t S, int32_t R) {
+    if (T != 1 || R > 32) return false;
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) n += N[s];
+    return n <= (R <= 16 ? 16384 : 8192);
+}
 
-// Whether a forward batch takes the direct path: rank vectors by k_lin_shrink
-// (no segment build) and the delta in k_lin_few or the join.  Both read their
-// lora rows once per token block or token, so their bytes bound it: past
-// kLinDirectBytes of either the sorted rows are the faster.
+// Whether k_lin_few (or k_lin_one) takes a forward batch.  Its work-groups read
+// x over and over, so the tiles overtake it as tokens times W grow; with 17
+// tokens and more a work-group is 32 columns wide and loses its width of the
+// card sooner.  k_lin_few against the tiles and the join, us, rank 16, 8 slots:
+// K x N of 4096 x 6144: 8 tokens 25.7 and 27.5, 16 tokens 29.6 and 28.9, 64
+// tokens 39.3 and 31.5; 8192 x 8192: 2 tokens 40.7 and 40.4, 16 tokens 51.1 and
+// 46.3; 1352 x 1652: 64 tokens 16.1 and 17.6.  A short K leaves its work-groups
+// little to read: 1024 x 65536, one token: 55.0 and 33.4.
+bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S) {
+    if (T > kLinFewTokens) return false;
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) n += N[s];
+    return n <= 32768 && T * n * K <= (T <= 16 ? 1 << 29 : 1 << 27);
+}
+
+// Direct batches whose rank vectors the slot-grouped kernels find (whole
+// 64-column steps, in-kernel discovery).
+bool lin_grouped(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    return T > 8 && !lin_few(T, K, N, S) && grp_discovers(T, L) && R % 16 == 0 && R <= kGrpMaxPartialRank &&
+           K % 64 == 0 && grp_kchunks(K) <= kMaxKcGrp;
+}
+
+// Whether a forward batch takes the direct path: rank vectors without a segment
+// build, and the delta in k_lin_few or k_lin_join_rows.  k_lin_join_rows reads
+// lora_b rows once per token, and k_lin_shrink lora_a rows once per block of 16
+// tokens, so their bytes bound it.  Direct against sorted (the faster of its two
+// forms), us, K 4096, 6144 columns: 128 tokens, rank 32, 16 slots (50 MB of
+// lora_b) 45.0 and 52.8; 192 tokens (75 MB) 53.2 and 55.5; 256 tokens (100 MB)
+// 58.1 and 56.7; 512 tokens (201 MB) 89.4 and 70.5.  With k_lin_shrink, rank 24:
+// 192 tokens of 4 slots (75 MB of lora_a) 52.0 and 56.3, 128 of 8 (100 MB) 47.6
+// and 48.4, 192 of 8 (151 MB) 57.8 and 56.3, 256 of 8 (201 MB) 64.8 and 57.4.
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
-    if (T <= kLinFewTokens) return true;
+    if (lin_few(T, K, N, S)) return true;
     if (T > kLinDirectTokens) return false;
     int64_t n = 0;
     for (int s = 0; s < S; ++s) n += N[s];
+    if ((int64_t)T * n * R * 2 > kLinDirectBytesB) return false;
+    if (lin_grouped(T, K, N, S, R, L)) return true;
     const int64_t slots = L < 16 ? L : 16, blocks = (T + 15) / 16, ranks = (int64_t)S * ((R + 15) / 16);
-    return blocks * slots * ranks * K * 64 <= kLinDirectBytes && (int64_t)T * n * R * 2 <= kLinDirectBytes;
+    return blocks * slots * ranks * K * 64 <= kLinDirectBytesA;
 }
 
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,

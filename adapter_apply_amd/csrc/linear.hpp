@@ -18,7 +18,7 @@ struct LinArgs {
     uint16_t *out;
     int64_t ldo;
     const uint16_t *hl;       // bf16 [S][T][hl_row]: scaled rank vectors' parts (the first two are used)
-    int32_t hl_row;           // kLinParts* R
+    int32_t hl_row;           // its row: kLinPartsFwd R or kLinPartsBwd R
     const int32_t *order;     // [T] row -> token, slot-sorted, then [T] the rows' slots; or null (token order)
     const int32_t *idx;
     const int32_t *slot_rank;
@@ -41,9 +41,11 @@ struct LinArgs {
 };
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
-constexpr int kLinFewTokens = 64;       // forward batches of at most this many tokens: k_lin_few
+constexpr int kLinFewTokens = 64;       // most tokens of k_lin_few
 constexpr int kLinMaxSplits = 8;
-bool lin_one(int32_t T, int32_t R);
+bool lin_one(int32_t T, const int64_t *N, int32_t S, int32_t R);
+bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S);
+bool lin_grouped(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits (k T cols <= this * 128^2)
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
@@ -52,9 +54,10 @@ constexpr int kLinPartsBwd = 3;
 // Whether the sizes stay within what one launch's grid takes.
 bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
 
-// The direct path: rank vectors in one launch without segments.
+// The direct path: no segment build.
 constexpr int kLinDirectTokens = 1024;
-constexpr int64_t kLinDirectBytes = 128 << 20;
+constexpr int64_t kLinDirectBytesA = 128 << 20;
+constexpr int64_t kLinDirectBytesB = 80 << 20;
 constexpr int64_t kLinJoinMax = 1 << 25;   // fp32 sums of a call (T N, with its K splits)
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);

@@ -4,13 +4,15 @@ Bounds count roundings.  A storage rounding is at most finfo(t).eps / 2 of the
 value (bf16 2^-8); an fp32 sum of n products is within n * 2^-23 of the sum of
 magnitudes (twice the round-to-nearest bound, so that it holds for an
 accumulator that truncates); a rank vector that enters a product as two bf16
-parts is within 2^-16 of its value (2^-8 of a remainder that is at most 2^-8).
+parts is within 2^-16 of its value (2^-8 of a remainder that is at most 2^-8), as three within
+2^-24 (the fp32 gradients).
 """
 import torch
 
 F64 = torch.float64
 U32 = 2.0 ** -23
 SPLIT = 2.0 ** -16
+SPLIT3 = 2.0 ** -24
 
 
 def normal(g, shape, std, dtype=torch.bfloat16):
@@ -113,14 +115,14 @@ class Layer:
                 D[m] += vm @ a.abs()
                 dA[s][i, :r] = v.T @ x[m]
                 # v: a sum of n products, scaled, split; then a sum over the tokens
-                eA[s][i, :r] = ((n + 2 * len(m) + 40) * U32 + SPLIT) * (vm.T @ x[m].abs())
+                eA[s][i, :r] = ((n + 2 * len(m) + 40) * U32 + SPLIT3) * (vm.T @ x[m].abs())
                 if buf is None:
                     u, um, k = x[m] @ a.T, x[m].abs() @ a.abs().T, self.K
                 else:
                     u = buf[s, m, :r].to(F64)
                     um, k = u.abs(), 0
                 dB[s][i, :, :r] = sc * (d.T @ u)
-                eB[s][i, :, :r] = ((k + 2 * len(m) + 40) * U32 + SPLIT) * sc * (d.abs().T @ um)
+                eB[s][i, :, :r] = ((k + 2 * len(m) + 40) * U32 + SPLIT3) * sc * (d.abs().T @ um)
         acc = (2 * n_all + 2 * self.R * self.S + 40) * U32 * (M + D) + SPLIT * D
         return dx, dx.abs() * 2.0 ** -8 + 1.01 * acc, dA, eA, dB, eB
 

@@ -17,11 +17,15 @@ SHAPES = [
     (1, 8, (4,), 8, 1, 0),                 # one launch
     (1, 4096, (512, 128, 128), 16, 8, 0),
     (1, 72, (36, 20), 32, 3, 4),
+    (1, 64, (16400,), 16, 2, 0),           # one token, many columns
     (1, 640, (100,), 40, 2, 0),            # up to 64 tokens
+    (2, 24, (32800, 4), 8, 3, 0),          # few tokens, too many columns for one launch: tiles
     (3, 72, (36,), 24, 3, 0),
     (16, 64, (64, 64), 16, 4, 8),
     (17, 136, (100, 36, 4), 40, 5, 4),
     (64, 256, (264,), 64, 130, 8),
+    (12, 4096, (14336,), 32, 6, 4),        # up to 64 tokens, a large projection: tiles
+    (33, 8256, (1100, 36), 48, 5, 0),
     (65, 8200, (68,), 16, 5, 0),           # direct, K splits
     (100, 512, (64, 100), 32, 7, 4),       # direct, grouped rank vectors
     (200, 520, (68, 132), 8, 9, 4),
@@ -131,6 +135,23 @@ def test_accumulate_and_parts():
     # the split sums are added to what was there one after the other
     for p, q in zip(sA + sB, dA + dB):
         assert torch.allclose(p, 2 * q, rtol=0, atol=float(q.abs().max()) * 20 * 2.0 ** -23)
+
+
+def test_more_than_a_million_tokens():
+    """A narrow layer over more 16-token blocks than one dimension of a grid
+    takes."""
+    T, K, N, R, L = (1 << 20) + 40, 8, (4,), 8, 3
+    c = Layer(T, K, N, R, L, seed=2)
+    y_ref, y_tol, b_ref, b_tol = c.forward()
+    full, y, buf = run_forward(c)
+    within(y, y_ref, y_tol, "y")
+    within(buf, b_ref, b_tol, "buf")
+    dx_ref, dx_tol, dA_ref, eA, dB_ref, eB = c.backward()
+    dx = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    dA, dB = run_backward(c, dx)
+    within(dx, dx_ref, dx_tol, "dx")
+    within(dA[0], dA_ref[0], eA[0], "dA")
+    within(dB[0], dB_ref[0], eB[0], "dB")
 
 
 def test_no_tokens():
