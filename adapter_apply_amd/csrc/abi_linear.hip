@@ -2,6 +2,9 @@
 // gradient, and of the per-adapter gradient norm and clip: argument checks (all
 // before any launch), workspace carving and launches.  Declarations and
 // contracts: include/adapter_apply.h.
+#include <memory>
+#include <new>
+
 #include "checks.hpp"
 #include "linear.hpp"
 
@@ -214,6 +217,16 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
     CHECK(check_ptrs(B, S));
     if (!al(dx, 16) || !al(dy, 16) || !al(x, 16) || !al(W, 16) || !al(buf, 16)) return LORA_E_ALIGN;
     CHECK(check_ws(ws, ws_bytes, wl.end));
+    const void *outs[2 * kMaxSlices + 1];
+    int n_out = 0;
+    if (dx) outs[n_out++] = dx;
+    for (int s = 0; s < S; ++s) {
+        if (dA) outs[n_out++] = dA[s];
+        if (dB) outs[n_out++] = dB[s];
+    }
+    for (int i = 1; i < n_out; ++i)
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return LORA_E_SHAPE;
 
     char *wp = static_cast<char *>(ws);
     const Slices sl = make_slices(A, B, N, S, 0);
@@ -317,6 +330,34 @@ static lora_status_t check_grads(const void *const *g, const int64_t *m, int32_t
     return LORA_OK;
 }
 
+// Every output at an address of its own, and at a gradient's only if it is that
+// tensor's: else work-groups of two tensors would scale the same elements.
+static lora_status_t check_outputs(const void *const *out, const void *const *g, const int64_t *m, int32_t n) {
+    size_t size = 16;
+    while (size < 2 * (size_t)n) size *= 2;
+    struct Entry { const void *p; int32_t i; };
+    const std::unique_ptr<Entry[]> table(new (std::nothrow) Entry[size]());
+    if (!table) return LORA_E_RUNTIME;
+    // the entry of address p, or the empty one where it belongs
+    auto find = [&](const void *p) -> Entry & {
+        size_t h = (size_t)((reinterpret_cast<uintptr_t>(p) >> 1) * 0x9E3779B97F4A7C15ull >> 20) & (size - 1);
+        while (table[h].p && table[h].p != p) h = (h + 1) & (size - 1);
+        return table[h];
+    };
+    for (int32_t i = 0; i < n; ++i) {
+        if (m[i] == 0) continue;
+        Entry &e = find(out[i]);
+        if (e.p) return LORA_E_SHAPE;
+        e = Entry{out[i], i};
+    }
+    for (int32_t i = 0; i < n; ++i) {
+        if (m[i] == 0) continue;
+        const Entry &e = find(g[i]);
+        if (e.p && e.i != i) return LORA_E_SHAPE;
+    }
+    return LORA_OK;
+}
+
 lora_status_t lora_grad_workspace_size(const int64_t *m, int32_t n, int32_t L, size_t *bytes) {
     if (!bytes || (n > 0 && !m)) return LORA_E_NULL;
     if (n < 0 || L < 1 || L > LORA_MAX_SLOTS) return LORA_E_SHAPE;
@@ -345,6 +386,7 @@ lora_status_t lora_grad_clip(void *const *out, const void *const *g, const int64
     CHECK(check_grads(const_cast<const void *const *>(out), m, n, L, dtype));
     if (!norm || !max_norm) return LORA_E_NULL;
     if (!al(norm, 4) || !al(max_norm, 4)) return LORA_E_ALIGN;
+    CHECK(check_outputs(const_cast<const void *const *>(out), g, m, n));
     return launched(launch_grad_clip(out, g, m, n, L, norm, max_norm, dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -246,7 +246,7 @@ hipError_t launch_grad_norm(const void *const *g, const int64_t *m, int32_t n, i
     const int64_t per_slot = grad_items(m, n, 1);
     // One launch fewer while the counting costs less than a launch: the counts
     // of a slot are adds to one address, one after the other (320 tensors, 13824
-    // items: 4 x 41 us with counts, 4 x 24 and 3 us without).
+    // items: 4 x 50 us with counts, 4 x 21 and 5 us without).
     const bool joined = per_slot > 0 && per_slot * L <= kCountItems;
     if (!joined) count = nullptr;
     int64_t item0 = 0;

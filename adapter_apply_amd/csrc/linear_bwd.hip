@@ -374,7 +374,7 @@ hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, 
 // Token splits while the (column tile, rank block, slot) work-groups of both
 // gradients are few: about 1024 work-groups, splits of at least 256 of a slot's
 // tokens on average (shorter ones cost their launch more than they save: 1501
-// tokens over 7 slots, 1652 x 1352, rank 40: 81 us with three splits, 74
+// tokens over 7 slots, 1652 x 1352, rank 40: 78 us with three splits, 71
 // without), partial sums within kLinWgPartMax elements each.
 int32_t lin_wg_splits(int32_t T, int32_t L, const int64_t *MA, const int64_t *MB, int32_t S, int32_t R) {
     int64_t tiles = 0, cols = 0;

@@ -461,8 +461,8 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
  * dA, dB: host arrays of S device pointers, fp32 [L][R][K] and [L][N[s]][R],
  * or NULL (not wanted; at least one of dx, dA, dB is).  They are overwritten
  * entirely, zeros for slots without tokens and ranks j >= slot_rank[i], or
- * added to with LORA_FLAG_ACCUMULATE.  T == 0 clears them too.  No two output
- * pointers may be equal.
+ * added to with LORA_FLAG_ACCUMULATE.  T == 0 clears them too.  Two equal
+ * output pointers: LORA_E_SHAPE.
  * buf: u as lora_linear left it, or NULL (computed again from x and A; read
  * for dB only).  Deterministic: no atomics on sums.
  * flags: LORA_FLAG_SEGMENTS_READY, LORA_FLAG_ACCUMULATE.
@@ -497,7 +497,8 @@ lora_status_t lora_grad_norm(float *norm, const void *const *g, const int64_t *m
 /* out[i][l][e] = round(g[i][l][e] * min(1, max_norm[l] / (norm[l] + 1e-6))).
  * norm, max_norm: device float [L]; norm as lora_grad_norm left it, or joined
  * over several groups of tensors.  out[i] may be g[i] (in place), else it must
- * not overlap any g.  A NaN norm gives NaN, an infinite one zero times g. */
+ * not overlap any g (an out[i] equal to another out or to another tensor's g,
+ * for instance a tied parameter listed twice: LORA_E_SHAPE).  A NaN norm gives NaN, an infinite one zero times g. */
 lora_status_t lora_grad_clip(void *const *out, const void *const *g, const int64_t *m, int32_t n, int32_t L,
                              const float *norm, const float *max_norm, int32_t dtype, void *stream);
 

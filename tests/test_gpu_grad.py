@@ -97,6 +97,21 @@ def test_bad_slot_stays_alone():
             assert bool(((o[i].double() - want).abs() <= want.abs() * 6 * 2.0 ** -24).all())
 
 
+def test_the_same_tensor_twice():
+    """The norm counts it twice; the clip refuses it, also among empty tensors."""
+    g = make([(50, 20), (333,), (0,)], 2, torch.float32)
+    norm, once = torch.empty((2,), device="cuda"), torch.empty((2,), device="cuda")
+    for n, t in ((once, g[:1]), (norm, [g[0], g[0]])):
+        aa.lora_grad_norm(n, t, aa.alloc_grad_workspace(t))
+    assert bool(((norm.double() - once.double() * 2 ** 0.5).abs() <= once.double() * 2.0 ** -23).all())
+    keep = g[0].clone()
+    with pytest.raises(Exception, match="shape|SHAPE|size"):
+        aa.lora_grad_clip([g[0], g[1], g[0]], [g[0], g[1], g[0]], norm, norm * 0.1)
+    assert torch.equal(g[0], keep)
+    aa.lora_grad_clip([g[2], g[0], g[2]], [g[2], g[0], g[2]], once, once * 4)
+    assert torch.equal(g[0], keep)
+
+
 def test_graph_and_stream():
     grads = make([(50, 20), (9000,)], 3, torch.float32)
     ws = aa.alloc_grad_workspace(grads)

@@ -184,6 +184,27 @@ def test_norm_and_clip_more_refusals():
     assert clip(hole(2, 0), FAKE) == aa.LORA_E_NULL
 
 
+@needs_no_gpu
+def test_equal_outputs_are_refused():
+    """Nothing is launched when two outputs are one: the same gradient twice, a
+    tensor listed twice for the clip, an output that is another one's input."""
+    other = dict(dx=FAKE + 0x4000000, dA=ptrs(3, FAKE + 0x1000000), dB=ptrs(3, FAKE + 0x2000000))
+    for kw in (dict(dA=ptrs(3, FAKE + 0x2000000)), dict(dx=FAKE + 0x1100000),
+               dict(dA=(C.c_void_p * 3)(FAKE, FAKE + 4096, FAKE))):
+        assert backward(**dict(other, **kw)) == aa.LORA_E_SHAPE
+    lib = aa.lib()
+
+    def clip(out, g, m):
+        arr = lambda v: (C.c_void_p * len(v))(*v)
+        return lib.lora_grad_clip(arr(out), arr(g), i64(*m), len(m), 3, FAKE, FAKE, aa.LORA_DT_F32, None)
+
+    at = [FAKE + 4096 * i for i in range(1, 400)]
+    assert clip(at[:2] + at[:1], at[:2] + at[:1], (64, 64, 64)) == aa.LORA_E_SHAPE
+    assert clip(at[:2], at[1:3], (64, 64)) == aa.LORA_E_SHAPE
+    assert clip([at[5], at[5]], at[:2], (64, 64)) == aa.LORA_E_SHAPE
+    assert clip(at[:200] + [at[77]], at[200:] + [at[0]] * 2, (8,) * 201) == aa.LORA_E_SHAPE
+
+
 # --------------------------------------------------------------------------
 # the binding
 # --------------------------------------------------------------------------
