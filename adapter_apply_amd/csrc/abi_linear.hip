@@ -272,7 +272,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
     }
     if (dx || dA) {
         const int32_t nsp = lin_du_splits(T, L, N, S, R);
-        CHECK(launched(launch_lin_du(p, ldp, poff, T, sl, S, L, R, slot_rank, seg, part, nsp, st)));
+        CHECK(launched(launch_lin_du(p, ldp, poff, T, sl, S, L, R, seg, part, nsp, st)));
         job[n_jobs++] = LinVectors{part, nsp, nullptr, hl_v, kLinPartsBwd, nullptr};
     }
     if (n_jobs)
@@ -280,7 +280,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
                                           dx ? order : nullptr, st)));
     if (dA || dB) {
         LinWgArgs wa{}, wb{};
-        wa.T = T; wa.S = S; wa.L = L; wa.R = R; wa.seg = seg;
+        wa.T = T; wa.S = S; wa.L = L; wa.R = R; wa.slot_rank = slot_rank; wa.seg = seg;
         wa.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
         wb = wa;
         wa.p = static_cast<const uint16_t *>(x); wa.ldp = ldx; wa.hl = hl_v;

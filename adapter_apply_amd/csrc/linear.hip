@@ -93,7 +93,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         const int t = a.order ? a.order[pos] : pos;
         int sl = -2;
         if (m < a.T)
-            sl = MIXED && a.join_delta ? -1 : a.order ? a.order[a.T + pos] : slot_of_token(a.idx, a.slot_rank, a.L, t);
+            sl = MIXED && a.join_delta ? -1 : a.order[a.T + pos];
         s_tok[i] = t;
         s_slot[i] = sl;
         // MIXED: every slot; else the slots that have a 16-token block of their own
@@ -568,7 +568,10 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         }
 #pragma unroll
         for (int i = 0; i < EU; ++i)
-            if (sl[i] != -2) __builtin_nontemporal_store(__builtin_bit_cast(unsigned long, v[i]), reinterpret_cast<unsigned long *>(a.out + (int64_t)tok[i] * a.ldo + obase + c0 + cl));
+            if (sl[i] != -2)
+                __builtin_nontemporal_store(
+                    __builtin_bit_cast(unsigned long, v[i]),
+                    reinterpret_cast<unsigned long *>(a.out + (int64_t)tok[i] * a.ldo + obase + c0 + cl));
     }
 }
 
@@ -773,7 +776,7 @@ template <int CT, int NRB, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
     __shared__ float s_sum[kFewWaves][CT + NRB][16];
     __shared__ float s_u[16 * NRB];
-    __shared__ int s_own[1];
+    __shared__ int s_own;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
     int sc = 0;
@@ -853,11 +856,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
             for (int i = 0; i < NRB; ++i) s_sum[w][CT + i][4 * g + e] = au[i][e];
         }
     }
-    if (w == 0 && lane == 0) {
-        s_own[0] = rank;                          // (a wave without a K step knows no slot)
-    }
+    if (tid == 0) s_own = rank;                   // (a wave without a K step knows no slot)
     __syncthreads();
-    rank = s_own[0];
+    rank = s_own;
     if (tid < 16 * NRB) {
         float u = 0.f;
 #pragma unroll
@@ -912,13 +913,8 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
     const int m = blockIdx.y * kJoinRows + l16;
     const bool real = m < a.T;
     const int mc = min(m, a.T - 1);
-    const int t = a.order ? a.order[mc] : mc;
-    const int slot = a.join_delta && real ? slot_of_token(a.idx, a.slot_rank, a.L, t) : -1;
-    if (a.clear && blockIdx.x == 0 && real && slot < 0) {
-        // the rank vectors of a token without a slot, which the grouped shrink leaves
-        for (int s = 0; s < a.S; ++s)
-            for (int j = threadIdx.x >> 4; j < a.R; j += 16) a.clear[((int64_t)s * a.T + t) * a.R + j] = 0.f;
-    }
+    const int t = a.order[mc];
+    const int slot = a.join_delta && real ? a.order[a.T + mc] : -1;
     const int64_t c0 = (int64_t)blockIdx.x * kJoinCols + w * (NB * 16);
     if (c0 >= a.part_ld) return;
     floatx4_t v[NB];
@@ -1059,6 +1055,7 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
     const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
     if (a.clear && slot < 0 && blockIdx.x == 0) {
+        // the rank vectors of a token without a slot, which the grouped shrink leaves
         for (int s = 0; s < a.S; ++s)
             for (int j = threadIdx.x; j < a.R; j += 256) a.clear[((int64_t)s * a.T + t) * a.R + j] = 0.f;
     }
@@ -1127,9 +1124,10 @@ struct LinReduceArgs {
 };
 
 // The row order of the tile GEMM: each slot's tokens, slots ascending, then
-// the tokens without a slot in token order; and each row's slot (or -1) after it.  A work-group writes 256 positions
-// of the slots' runs and places its 256 tokens without a slot, whose number
-// before it is counted from idx (a bitmap of the slots in use in LDS).
+// the tokens without a slot in token order; and each row's slot (or -1) after
+// it.  A work-group writes 256 positions of the slots' runs and places its 256
+// tokens without a slot, whose number before it is counted from idx (a bitmap
+// of the slots in use in LDS).
 __device__ __forceinline__ void row_order(const LinReduceArgs &a) {
     constexpr int NW = kRedThreads / 64;
     __shared__ unsigned s_act[kMaxSlots / 32];

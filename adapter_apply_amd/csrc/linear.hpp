@@ -93,8 +93,8 @@ hipError_t launch_lin_pad(const void *dy, int64_t lddy, int32_t T, int32_t S, co
 // Partial sums [S][nsp][T][R] of dy . lora_b by slot-sorted position.
 int32_t lin_du_splits(int32_t T, int32_t L, const int64_t *N, int32_t S, int32_t R);
 hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, int32_t T,
-                         const Slices &sl, int32_t S, int32_t L, int32_t R, const int32_t *slot_rank,
-                         const SegPtrs &seg, float *part, int32_t nsp, hipStream_t st);
+                         const Slices &sl, int32_t S, int32_t L, int32_t R, const SegPtrs &seg, float *part,
+                         int32_t nsp, hipStream_t st);
 // One weight gradient family: out_s[slot][..] = sum over the slot's tokens of
 // rows p (M_s columns at poff[s]) times rank vectors hl.  transposed: out is
 // [L][R][M] (lora_a), else [L][M_s][R] (lora_b).
@@ -107,6 +107,7 @@ struct LinWgArgs {
     int64_t poff[kMaxSlices];
     int32_t T, S, L, R;
     int32_t accumulate;
+    const int32_t *slot_rank;
     SegPtrs seg;
     float *part;               // fp32 partial sums of the token splits
     int32_t nsp;

@@ -266,6 +266,7 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
 
     float *out = a.nsp > 1 ? a.part + (int64_t)blockIdx.z * a.part_stride + a.part_off[s] : a.out[s];
     const bool add = a.accumulate && a.nsp == 1;
+    const int rank = a.slot_rank ? a.slot_rank[slot] : a.R;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -277,6 +278,11 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
             const int64_t o = TRANSPOSED ? ((int64_t)slot * a.R + r) * M + m : ((int64_t)slot * M + m) * a.R + r;
             floatx4_t *dst = reinterpret_cast<floatx4_t *>(out + o);
             floatx4_t v = acc[i][j];
+            // ranks past the slot's own are zero, whatever the rows hold (an
+            // infinity times the zero rank vector is NaN)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (r + (TRANSPOSED ? 0 : q) >= rank) v[q] = 0.f;
             if (add) {
                 const floatx4_t old = *dst;
 #pragma unroll
@@ -349,9 +355,8 @@ int32_t lin_du_splits(int32_t T, int32_t L, const int64_t *N, int32_t S, int32_t
 }
 
 hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, int32_t T,
-                         const Slices &sl, int32_t S, int32_t L, int32_t R, const int32_t *slot_rank,
-                         const SegPtrs &seg, float *part, int32_t nsp, hipStream_t st) {
-    (void)slot_rank;
+                         const Slices &sl, int32_t S, int32_t L, int32_t R, const SegPtrs &seg, float *part,
+                         int32_t nsp, hipStream_t st) {
     DuArgs a{};
     a.dy = dy; a.lddy = lddy; a.T = T; a.S = S; a.L = L; a.R = R; a.seg = seg; a.part = part;
     a.nsp = nsp;

@@ -220,6 +220,24 @@ def test_bad_adapter_stays_alone(T, K, N, bad):
             assert torch.equal(p[i], q[i]), i
 
 
+@pytest.mark.parametrize("T", [40, 4500])
+def test_bad_rows_keep_padded_ranks_zero(T):
+    """An infinity in a token's x and dy leaves zeros at the ranks past its
+    slot's own, and every other slot's gradient."""
+    c = Layer(T, 136, (100, 36), 24, 3, seed=12)
+    c.rank[:] = torch.tensor([24, 5, 13], device="cuda")
+    clean = run_backward(c, None)
+    hit = torch.nonzero(c.idx == 1).flatten()[0]
+    c.x[hit, 3] = float("inf")
+    c.dy[hit, 7] = float("nan")
+    dA, dB = run_backward(c, None)
+    for s in range(c.S):
+        for i in (0, 2):
+            assert torch.equal(dA[s][i], clean[0][s][i]) and torch.equal(dB[s][i], clean[1][s][i])
+        assert bool(dA[s][1, :5].isnan().any())
+        assert bool((dA[s][1, 5:] == 0).all()) and bool((dB[s][1, :, 5:] == 0).all())
+
+
 @pytest.mark.parametrize("T", [33, 900])
 def test_another_stream_and_repeats(T):
     """Calls on a stream of their own, and repeats, give the same bits."""
