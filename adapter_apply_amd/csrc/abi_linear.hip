@@ -64,7 +64,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     size_t cols = 0;
     for (int s = 0; s < S; ++s) cols += (size_t)N[s];
     if (cols < (size_t)K) cols = (size_t)K;
-    size_t sums = kLinMaxSplits * (size_t)T * cols;
+    size_t sums = kLinMaxSplits * (size_t)T * 2 * cols;     // (wide batches: up to as many columns more)
     if (sums > (size_t)kLinJoinMax) sums = (size_t)kLinJoinMax;
     if (4 * sums > part) part = 4 * sums;
     o = align256(o + part);
@@ -142,17 +142,18 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     int32_t *order = nullptr;
     const bool direct = lin_direct(T, K, N, S, R, L);
     const bool join = direct || lin_join_delta(T, K, N, S, R, L);
-    float *u = buf, *clear = nullptr;
+    const bool wide = direct && lin_wide(T, K, N, S, R, L);
+    float *u = buf, *u_out = nullptr;
     // fp32 rank vectors by token, in buf if it is wanted
     if (join && !u) u = reinterpret_cast<float *>(wp + wl.hl_u);
-    if (lin_one(T, N, S, R)) {
-        clear = buf;
+    if (lin_one(T, K, N, S, R) || wide) {
+        u_out = buf;
     } else if (direct) {
-        if (lin_grouped(T, K, N, S, R, L)) {
+        if (!lin_few(T, K, N, S, R, L) && lin_grouped(T, K, R, L)) {
             float *part = reinterpret_cast<float *>(wp + wl.part);
             CHECK(launched(launch_grp_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, part, nullptr, nullptr, st)));
             CHECK(launched(launch_grp_reduce(T, S, L, R, idx, slot_rank, part, grp_kchunks(K), u, nullptr, st)));
-            clear = buf;
+            u_out = buf;
         } else {
             CHECK(launched(launch_lin_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, u, st)));
         }
@@ -174,7 +175,7 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
     a.part = reinterpret_cast<float *>(wp + wl.part);
     a.join_delta = join;
-    a.u = u; a.scale = scale; a.clear = clear;
+    a.wide = wide; a.u = u; a.scale = scale; a.buf = u_out;
     a.hl = hl; a.hl_row = kLinPartsFwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
     a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) {

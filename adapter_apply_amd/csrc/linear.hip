@@ -77,12 +77,30 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         nt = r / rows;
         mt = g * gm + r - nt * rows;
     }
-    int sc = 0;                                   // forward: the tile's slice
-    if (!NN)
+    // forward: the tile's slice, whose rows of W start at qb; or, past those of a
+    // wide batch, its lora_a rows of every slot
+    int sc = 0;
+    const uint16_t *qb = a.w;
+    int64_t ldq = a.ldw, c0 = (int64_t)nt * BN, cend = a.K, obase = 0;   // columns: first, end, slice's first in out
+    if (!NN) {
         while (sc + 1 < a.S && nt >= a.tile_start[sc + 1]) ++sc;
+        if (MIXED && nt >= a.tile_start[a.S]) {
+            const int per = (a.L * a.R + BN - 1) / BN;
+            nt -= a.tile_start[a.S];
+            sc = nt / per;
+            c0 = (int64_t)(nt - sc * per) * BN;
+            cend = a.L * a.R;
+            qb = a.la[sc];
+            ldq = a.K;
+            obase = a.cols + sc * cend;
+        } else {
+            c0 = (int64_t)(nt - a.tile_start[sc]) * BN;
+            cend = a.n[sc];
+            qb += a.off[sc] * ldq;
+            obase = a.off[sc];
+        }
+    }
     const int m0 = mt * BM;
-    const int64_t c0 = (int64_t)(NN ? nt : nt - a.tile_start[sc]) * BN;   // column inside the slice
-    const int64_t cend = NN ? a.K : a.n[sc];
 
     if (tid < 32) s_bits[tid] = 0;
     if (tid == 0) s_any = 0;
@@ -197,7 +215,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
                 qptr[i] += (int64_t)qrow(i) * a.ldw + (col < cend ? col : 0);
             } else {
                 const int64_t n = min(c0 + qrow(i), cend - 1);
-                qptr[i] += (a.off[sc] + n) * a.ldw + qlc(i) * 8;
+                qptr[i] = qb + n * ldq + qlc(i) * 8;
             }
         }
     }
@@ -494,7 +512,6 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     }
 
     // One rounding per output element; a split leaves its fp32 sums by row.
-    const int64_t obase = NN ? 0 : a.off[sc];
     if (MIXED && a.part) {
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
@@ -865,7 +882,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
         for (int i = 0; i < kFewWaves; ++i) u += s_sum[i][CT + (tid >> 4)][tid & 15];
         if (tid >= rank) u = 0.f;
         s_u[tid] = u;
-        if (a.clear && tile == 0 && tid < a.R) a.clear[(int64_t)sc * a.R + tid] = u;
+        if (a.buf && tile == 0 && tid < a.R) a.buf[(int64_t)sc * a.R + tid] = u;
     }
     __syncthreads();
     if (w) return;
@@ -1045,26 +1062,12 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
     }
 }
 
-// The same for a direct batch, whose rows are in token order: 16 rows then name
-// up to 16 slots, and one after the other they cost the MFMA form above more
-// than it saves (256 tokens of 8 slots, 6144 columns, rank 16: 22.8 against
-// 12.6 us).  Work-group = one token x 512 columns, 2 per thread, so that a
-// wave's lora_b loads cover whole lines: fp32 FMAs with the token's rank vector.
-__global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
-    const int t = blockIdx.y;
-    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
-    const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
-    if (a.clear && slot < 0 && blockIdx.x == 0) {
-        // the rank vectors of a token without a slot, which the grouped shrink leaves
-        for (int s = 0; s < a.S; ++s)
-            for (int j = threadIdx.x; j < a.R; j += 256) a.clear[((int64_t)s * a.T + t) * a.R + j] = 0.f;
-    }
-    if (c >= a.part_ld) return;
+// Two columns c, c + 1 of one token: the sum of the splits o, bias, delta (the
+// rank vector from u), rounded once.
+__device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int slot, int rank,
+                                         const float2 (&o)[kLinMaxSplits], const float *u, int64_t ldu) {
+    if (c >= a.cols) return;
     float v0 = 0.f, v1 = 0.f;
-    float2 o[kLinMaxSplits];
-#pragma unroll
-    for (int k = 0; k < kLinMaxSplits; ++k)
-        if (k < a.ksp) o[k] = *reinterpret_cast<const float2 *>(a.part + ((int64_t)k * a.T + t) * a.part_ld + c);
 #pragma unroll
     for (int k = 0; k < kLinMaxSplits; ++k)
         if (k < a.ksp) {
@@ -1085,13 +1088,13 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
         for (int i = 1; i < kMaxSlices; ++i)
             if (i < a.S && c >= a.off[i]) { s = i; off = a.off[i]; n = a.n[i]; b = a.lora[i]; }
         b += ((int64_t)slot * n + c - off) * a.R;
-        const float *u = a.u + ((int64_t)s * a.T + t) * a.R;
-        const int rank = a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
         float d0 = 0.f, d1 = 0.f;
 #pragma unroll 2
         for (int j = 0; j < rank; j += 8) {
-            const floatx4_t u0 = ldg<floatx4_t>(u + j), u1 = ldg<floatx4_t>(u + j + 4);
             const uint4 b0 = ldg<uint4>(b + j), b1 = ldg<uint4>(b + a.R + j);
+            const float *up = u + s * ldu + j;
+            const floatx4_t u0 = *reinterpret_cast<const floatx4_t *>(up);
+            const floatx4_t u1 = *reinterpret_cast<const floatx4_t *>(up + 4);
             const float uv[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
             const uint32_t w0[4] = {b0.x, b0.y, b0.z, b0.w}, w1[4] = {b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -1108,7 +1111,54 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
     }
     *reinterpret_cast<uint32_t *>(a.out + (int64_t)t * a.ldo + c) = pack_bf16x2(v0, v1);
 }
-
+// The same for a direct batch, whose rows are in token order: 16 rows then name
+// up to 16 slots, and one after the other they cost the MFMA form above more
+// than it saves (256 tokens of 8 slots, 6144 columns, rank 16: 22.8 against
+// 12.6 us).  Work-group = one token x 512 columns, 2 per thread, so that a
+// wave's lora_b loads cover whole lines: fp32 FMAs with the token's rank vector.
+// In a wide batch every work-group first sums the splits of its token's rank
+// vector.
+__global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
+    const int t = blockIdx.y;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+    const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
+    const float *pt = a.part + (int64_t)t * a.part_ld;
+    const int64_t split = (int64_t)a.T * a.part_ld;
+    float2 o[kLinMaxSplits];
+#pragma unroll
+    for (int k = 0; k < kLinMaxSplits; ++k)
+        if (k < a.ksp) o[k] = *reinterpret_cast<const float2 *>(pt + k * split + min(c, a.cols - 2));
+    const int rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
+    if (a.wide) {
+        __shared__ __attribute__((aligned(16))) float s_u[kLinWideRanks];
+        const int LR = a.L * a.R;
+        for (int q = threadIdx.x; q < a.S * a.R; q += 256) {
+            const int s = q / a.R, j = q - s * a.R;
+            float u = 0.f;
+            if (j < rank) {
+                const float *p = pt + a.cols + s * LR + slot * a.R + j;
+                float w[kLinMaxSplits];
+#pragma unroll
+                for (int k = 0; k < kLinMaxSplits; ++k)
+                    if (k < a.ksp) w[k] = p[k * split];
+#pragma unroll
+                for (int k = 0; k < kLinMaxSplits; ++k)
+                    if (k < a.ksp) u += w[k];
+            }
+            s_u[q] = u;
+            if (a.buf && blockIdx.x == 0) a.buf[((int64_t)s * a.T + t) * a.R + j] = u;
+        }
+        __syncthreads();
+        join_row(a, t, c, slot, rank, o, s_u, a.R);
+        return;
+    }
+    if (a.buf && slot < 0 && blockIdx.x == 0) {
+        // the rank vectors of a token without a slot, which the grouped shrink leaves
+        for (int s = 0; s < a.S; ++s)
+            for (int j = threadIdx.x; j < a.R; j += 256) a.buf[((int64_t)s * a.T + t) * a.R + j] = 0.f;
+    }
+    join_row(a, t, c, slot, rank, o, a.u + (int64_t)t * a.R, (int64_t)a.T * a.R);
+}
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
 // own, scales, splits into bf16 parts, and clears buf for tokens without a
@@ -1235,7 +1285,11 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
         cols = 0;
         for (int s = 0; s < a.S; ++s) cols += a.n[s];
     }
-    a.part_ld = cols;
+    a.cols = a.part_ld = cols;
+    if (a.wide) {
+        a.part_ld += (int64_t)a.S * a.L * a.R;
+        a.n_tiles += a.S * ((a.L * a.R + BN - 1) / BN);
+    }
     if (ksp == 1 && !a.join_delta) a.part = nullptr;
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
     if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
@@ -1284,8 +1338,8 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (!gradient && lin_one(a.T, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
-    if (!gradient && lin_few(a.T, a.K, a.n, a.S)) {
+    if (!gradient && lin_one(a.T, a.K, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
+    if (!gradient && lin_few(a.T, a.K, a.n, a.S, a.R, a.L)) {
         // (a round of eight steps is 4096 of K, and steps past K load too: 2048
         // columns of K 2048, 16 tokens: 13.2 us with four steps, 16.5 with eight)
         if (a.T <= 16) return a.K > 2048 ? run_few<1, 1, 8>(a, st) : run_few<1, 1, 4>(a, st);
@@ -1313,7 +1367,11 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         if (k > kLinMaxSplits) k = kLinMaxSplits;
         return (int)(k < 1 ? 1 : k);
     };
-    const int64_t t128 = tiles(a.T, a.K, a.n, a.S, gradient, 128), t64 = tiles(a.T, a.K, a.n, a.S, gradient, 64);
+    int64_t t128 = tiles(a.T, a.K, a.n, a.S, gradient, 128), t64 = tiles(a.T, a.K, a.n, a.S, gradient, 64);
+    if (a.wide) {
+        t128 += (int64_t)a.S * ((a.L * a.R + 127) / 128) * ((a.T + 127) / 128);
+        t64 += (int64_t)a.S * ((a.L * a.R + 63) / 64) * ((a.T + 63) / 64);
+    }
     if (t128 >= 192) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, 1, st);
     if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 20480))
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, splits(t128), st);
@@ -1351,44 +1409,77 @@ bool lin_one(int32_t T, const int64_t *N, int32_t S, int32_t R) {
     return n <= (R <= 16 ? 16384 : 8192);
 }
 
-// Whether k_lin_few (or k_lin_one) takes a forward batch.  Its work-groups read
-// x over and over, so the tiles overtake it as tokens times W grow; with 17
-// tokens and more a work-group is 32 columns wide and loses its width of the
-// card sooner.  k_lin_few against the tiles and the join, us, rank 16, 8 slots:
-// K x N of 4096 x 6144: 8 tokens 25.7 and 27.5, 16 tokens 29.6 and 28.9, 64
-// tokens 39.3 and 31.5; 8192 x 8192: 2 tokens 40.7 and 40.4, 16 tokens 51.1 and
-// 46.3; 1352 x 1652: 64 tokens 16.1 and 17.6.  A short K leaves its work-groups
-// little to read: 1024 x 65536, one token: 55.0 and 33.4.
-bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S) {
-    if (T > kLinFewTokens) return false;
+// The further columns of a wide batch, x A^T of every slot, in whole 64-column
+// tiles; 0 when they would be more than the layer's own (or their vectors more
+// than the join holds).
+static int64_t wide_cols(int64_t n, int32_t S, int32_t R, int32_t L) {
+    const int64_t c = (int64_t)S * ((L * R + 63) / 64) * 64;
+    return c <= n && S * R <= kLinWideRanks ? c : 0;
+}
+static int64_t columns(const int64_t *N, int32_t S) {
     int64_t n = 0;
     for (int s = 0; s < S; ++s) n += N[s];
+    return n;
+}
+
+// One token of rank at most 32 takes the one launch of k_lin_one, while its
+// work-groups, each reading the slot's lora_a rows, are not too many and K is
+// not too long for one round of loads after the other.  Against the wide tiles,
+// us: K x N of 4096 x 6144 16.6 and 18.3 at rank 16; 8192 x 8192 32.7 and 31.7;
+// 4096 x 28672 52.4 and 42.8; 14336 x 4096 43.2 and 27.2.  (Against k_lin_shrink
+// and k_lin_few, rank 32, 4096 x 16384: 36.7 and 33.7.)
+bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R) {
+    return T == 1 && R <= 32 && K <= 8192 && columns(N, S) <= (R <= 16 ? 16384 : 8192);
+}
+
+// Whether k_lin_few (or k_lin_one) takes a forward batch.  Its work-groups read
+// x over and over, so the tiles overtake it as tokens times W grow.  Against
+// the wide tiles (us, rank 16 to 24): 1352 x 1652, 16 tokens 11.0 and 12.6, 32
+// tokens 13.7 and 12.6; 2048 x 2048, 2 tokens 10.8 and 10.9, 8 tokens 12.0 and
+// 11.1; 4096 x 6144, 2 tokens 22.3 and 18.5, with as many further columns 22.3
+// and 25.8.  Where lora_a is too large for those, against k_lin_shrink and the
+// tiles: 4096 x 6144, 8 tokens 25.7 and 27.5, 16 tokens 29.6 and 28.9, 64 tokens
+// 39.3 and 31.5; 8192 x 8192, 2 tokens 40.7 and 40.4, 16 tokens 51.1 and 46.3;
+// 1024 x 65536, one token 55.0 and 33.4.
+bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    if (lin_one(T, K, N, S, R)) return true;
+    if (T > kLinFewTokens) return false;
+    const int64_t n = columns(N, S), wide = wide_cols(n, S, R, L);
+    if (wide) return (T <= 16 && n * K <= 3 << 20) || (T <= 4 && 2 * wide > n && n <= 32768);
     return n <= 32768 && T * n * K <= (T <= 16 ? 1 << 29 : 1 << 27);
+}
+
+// Direct batches whose rank vectors come out of the tiles as further columns: a
+// launch less (256 tokens, rank 16, 4096 x 6144, us: 8 slots 38.5 against 46.7
+// of the slot-grouped kernels, 128 slots 54.0 against 66.6).
+bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    return !lin_few(T, K, N, S, R, L) && wide_cols(columns(N, S), S, R, L) > 0;
 }
 
 // Direct batches whose rank vectors the slot-grouped kernels find (whole
 // 64-column steps, in-kernel discovery).
-bool lin_grouped(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
-    return T > 8 && !lin_few(T, K, N, S) && grp_discovers(T, L) && R % 16 == 0 && R <= kGrpMaxPartialRank &&
-           K % 64 == 0 && grp_kchunks(K) <= kMaxKcGrp;
+bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L) {
+    return T > 8 && grp_discovers(T, L) && R % 16 == 0 && R <= kGrpMaxPartialRank && K % 64 == 0 &&
+           grp_kchunks(K) <= kMaxKcGrp;
 }
 
 // Whether a forward batch takes the direct path: rank vectors without a segment
 // build, and the delta in k_lin_few or k_lin_join_rows.  k_lin_join_rows reads
 // lora_b rows once per token, and k_lin_shrink lora_a rows once per block of 16
-// tokens, so their bytes bound it.  Direct against sorted (the faster of its two
-// forms), us, K 4096, 6144 columns: 128 tokens, rank 32, 16 slots (50 MB of
-// lora_b) 45.0 and 52.8; 192 tokens (75 MB) 53.2 and 55.5; 256 tokens (100 MB)
-// 58.1 and 56.7; 512 tokens (201 MB) 89.4 and 70.5.  With k_lin_shrink, rank 24:
-// 192 tokens of 4 slots (75 MB of lora_a) 52.0 and 56.3, 128 of 8 (100 MB) 47.6
-// and 48.4, 192 of 8 (151 MB) 57.8 and 56.3, 256 of 8 (201 MB) 64.8 and 57.4.
+// tokens, so their bytes bound it.  Wide against sorted (us; MB of lora_b), K 4096,
+// 6144 columns: 512 tokens of rank 16 (100 MB) 58.5 and 63.5, 777 tokens (153 MB)
+// 85.8 and 81.6; 128 tokens of rank 64 (100 MB) 45.8 and 47.9, 256 tokens (201
+// MB) 76.3 and 58.7; 14336 x 4096, 777 tokens of rank 16 (102 MB) 135 and 155.
+// With the slot-grouped kernels, 4096 x 6144: 192 tokens of rank 32, 16 slots (75
+// MB) 53.2 and 55.5, 256 tokens (100 MB) 58.1 and 56.7.  With k_lin_shrink, rank
+// 24 (MB of lora_a): 128 tokens of 8 slots (100 MB) 47.6 and 48.4, 192 of 8 (151
+// MB) 57.8 and 56.3, 256 of 8 (201 MB) 64.8 and 57.4.
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
-    if (lin_few(T, K, N, S)) return true;
-    if (T > kLinDirectTokens) return false;
-    int64_t n = 0;
-    for (int s = 0; s < S; ++s) n += N[s];
-    if ((int64_t)T * n * R * 2 > kLinDirectBytesB) return false;
-    if (lin_grouped(T, K, N, S, R, L)) return true;
+    if (lin_few(T, K, N, S, R, L)) return true;
+    const bool wide = lin_wide(T, K, N, S, R, L);
+    if (T > kLinDirectTokens ||
+        T * columns(N, S) * R * 2 > (wide ? kLinWideBytesB : kLinDirectBytesB)) return false;
+    if (wide || lin_grouped(T, K, R, L)) return true;
     const int64_t slots = L < 16 ? L : 16, blocks = (T + 15) / 16, ranks = (int64_t)S * ((R + 15) / 16);
     return blocks * slots * ranks * K * 64 <= kLinDirectBytesA;
 }

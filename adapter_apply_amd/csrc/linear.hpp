@@ -29,10 +29,13 @@ struct LinArgs {
     int32_t join_delta;       // the join adds the delta, not the tiles
     const float *u;           // fp32 rank vectors [S][T][R] of the join and of k_lin_few
     const float *scale;
-    float *clear;             // join: u rows of tokens without a slot to clear, or null (k_lin_one: u)
-    const uint16_t *la[kMaxSlices];     // k_lin_one: lora_a [L][R][K]
+    int32_t wide;             // x A^T of every slot as S L R further columns of part (lin_wide)
+    float *buf;               // where u goes if it is wanted: k_lin_one, join of wide batches; of other
+                              // batches the join only clears the rows of tokens without a slot
+    const uint16_t *la[kMaxSlices];     // k_lin_one and wide: lora_a [L][R][K]
     float *part;
-    int64_t part_ld;
+    int64_t part_ld;          // its row: cols, and the further columns of wide batches
+    int64_t cols;             // columns of out
     const uint16_t *lora[kMaxSlices];   // forward: lora_b [L][N_s][R]; gradient: lora_a [L][R][K]
     int64_t n[kMaxSlices];              // N_s
     int64_t off[kMaxSlices];            // first row of slice s in w (first column in out)
@@ -43,9 +46,9 @@ struct LinArgs {
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
 constexpr int kLinFewTokens = 64;       // most tokens of k_lin_few
 constexpr int kLinMaxSplits = 8;
-bool lin_one(int32_t T, const int64_t *N, int32_t S, int32_t R);
-bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S);
-bool lin_grouped(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
+bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R);
+bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
+bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L);
 constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits (k T cols <= this * 128^2)
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
@@ -58,9 +61,12 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
 constexpr int kLinDirectTokens = 1024;
 constexpr int64_t kLinDirectBytesA = 128 << 20;
 constexpr int64_t kLinDirectBytesB = 80 << 20;
+constexpr int64_t kLinWideBytesB = 112 << 20;
 constexpr int64_t kLinJoinMax = 1 << 25;   // fp32 sums of a call (T N, with its K splits)
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
+bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
+constexpr int kLinWideRanks = 1024;     // most S R of a wide batch
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,
                              const int32_t *slot_rank, float *buf, hipStream_t st);
