@@ -59,8 +59,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         if (wg > (size_t)kLinWgPartMax) wg = (size_t)kLinWgPartMax;
         if (2 * 4 * wg > part) part = 2 * 4 * wg;
     }
-    // the tile GEMM's sums: at most 8 K splits (of kLinSplitTiles tiles of
-    // 128 x 128), at most kLinJoinMax
+    // the tile GEMM's sums: at most kLinMaxSplits of them, at most kLinJoinMax
     size_t cols = 0;
     for (int s = 0; s < S; ++s) cols += (size_t)N[s];
     if (cols < (size_t)K) cols = (size_t)K;

@@ -1291,6 +1291,7 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
         a.n_tiles += a.S * ((a.L * a.R + BN - 1) / BN);
     }
     if (ksp == 1 && !a.join_delta) a.part = nullptr;
+    if (a.part && (int64_t)ksp * a.T * a.part_ld > kLinJoinMax) return hipErrorInvalidValue;   // (no rule asks for it)
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
     if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
@@ -1348,7 +1349,7 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     }
     if (!a.join_delta && a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
         return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
-    // Few tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
+    // Fewer tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
     // each), joined by a second launch.  Tiles of 64 x 64 read each operand
     // twice as often, which shows once all their K tiles together pass some
     // 20000 (256 tokens, K x N: 2048 x 2048 26.1 against 27.6 us with 128 x 128,
@@ -1372,7 +1373,15 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         t128 += (int64_t)a.S * ((a.L * a.R + 127) / 128) * ((a.T + 127) / 128);
         t64 += (int64_t)a.S * ((a.L * a.R + 63) / 64) * ((a.T + 63) / 64);
     }
-    if (t128 >= 192) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, 1, st);
+    // From 192 tiles of 128 x 128 on a join costs more than even work-groups give
+    // (2048 tokens, 4096 x 4096: 97 us; 132 with 256 x 256, 147 with 64 x 64); where
+    // it runs anyway, two or three splits even them out up to 340 tiles (512
+    // tokens, 4096 x 6144, 204 tiles: 58.5, two splits 54.9; 1024 tokens, 14336 x
+    // 4096, 264 tiles: 198, 172 and 156; 452 tiles: 117 and 126 with two).
+    if (t128 >= 192) {
+        const int k = !a.join_delta || t128 > 340 || nk < 24 ? 1 : t128 > 256 ? 3 : 2;
+        return run_tile<128, 128, 2, 2, 2, true>(a, gradient, k, st);
+    }
     if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 20480))
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, splits(t128), st);
     return run_tile<64, 64, 2, 2, 4, true>(a, gradient, splits(t64), st);
@@ -1466,19 +1475,21 @@ bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L) {
 // Whether a forward batch takes the direct path: rank vectors without a segment
 // build, and the delta in k_lin_few or k_lin_join_rows.  k_lin_join_rows reads
 // lora_b rows once per token, and k_lin_shrink lora_a rows once per block of 16
-// tokens, so their bytes bound it.  Wide against sorted (us; MB of lora_b), K 4096,
-// 6144 columns: 512 tokens of rank 16 (100 MB) 58.5 and 63.5, 777 tokens (153 MB)
-// 85.8 and 81.6; 128 tokens of rank 64 (100 MB) 45.8 and 47.9, 256 tokens (201
-// MB) 76.3 and 58.7; 14336 x 4096, 777 tokens of rank 16 (102 MB) 135 and 155.
-// With the slot-grouped kernels, 4096 x 6144: 192 tokens of rank 32, 16 slots (75
-// MB) 53.2 and 55.5, 256 tokens (100 MB) 58.1 and 56.7.  With k_lin_shrink, rank
+// tokens, so their bytes bound it, with some 16 of sums per output.  Wide against
+// sorted (us; MB of lora_b and sums), K 4096, 6144 columns: 512 tokens of rank 16
+// (151 MB) 54.9 and 63.5, 777 tokens (229 MB) 82.1 and 81.6; 128 tokens of rank
+// 64 (113 MB) 45.8 and 47.9, 256 tokens (226 MB) 76.3 and 58.7; 28672 columns, 128
+// tokens of rank 16 (176 MB) 78.9 and 97.2, 256 of rank 8 (235 MB) 117 and 90;
+// 14336 x 4096, 777 tokens of rank 16 (153 MB) 121 and 155.
+// With the slot-grouped kernels, 4096 x 6144: 192 tokens of rank 32, 16 slots (94
+// MB) 53.2 and 55.5, 256 tokens (126 MB) 58.1 and 56.7.  With k_lin_shrink, rank
 // 24 (MB of lora_a): 128 tokens of 8 slots (100 MB) 47.6 and 48.4, 192 of 8 (151
 // MB) 57.8 and 56.3, 256 of 8 (201 MB) 64.8 and 57.4.
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     if (lin_few(T, K, N, S, R, L)) return true;
     const bool wide = lin_wide(T, K, N, S, R, L);
     if (T > kLinDirectTokens ||
-        T * columns(N, S) * R * 2 > (wide ? kLinWideBytesB : kLinDirectBytesB)) return false;
+        T * columns(N, S) * (2 * R + 16) > (wide ? kLinWideBytesB : kLinDirectBytesB)) return false;
     if (wide || lin_grouped(T, K, R, L)) return true;
     const int64_t slots = L < 16 ? L : 16, blocks = (T + 15) / 16, ranks = (int64_t)S * ((R + 15) / 16);
     return blocks * slots * ranks * K * 64 <= kLinDirectBytesA;

@@ -49,7 +49,7 @@ constexpr int kLinMaxSplits = 8;
 bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R);
 bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L);
-constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits (k T cols <= this * 128^2)
+constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
 constexpr int kLinPartsFwd = 2;
@@ -60,9 +60,11 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S);
 // The direct path: no segment build.
 constexpr int kLinDirectTokens = 1024;
 constexpr int64_t kLinDirectBytesA = 128 << 20;
-constexpr int64_t kLinDirectBytesB = 80 << 20;
-constexpr int64_t kLinWideBytesB = 112 << 20;
-constexpr int64_t kLinJoinMax = 1 << 25;   // fp32 sums of a call (T N, with its K splits)
+constexpr int64_t kLinDirectBytesB = 110 << 20;
+constexpr int64_t kLinWideBytesB = 176 << 20;
+// fp32 sums of a call: splits times T columns.  At most 1020 tiles of 128 x 128
+// (launch_lin_gemm), unsplit batches bounded by lin_join_delta and lin_direct.
+constexpr int64_t kLinJoinMax = 1 << 25;
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
