@@ -46,6 +46,11 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // them: a 16-token block of one slot takes part in that slot's K tiles only,
 // and a block of several goes through a temporary and a select, in the K
 // tiles (MIXED) or after them.
+//
+// Bound by the matrix rate: 8192 tokens, 4096 x 28672, rank 64, 16 slots 1.58 to
+// 1.71 ms; its base product alone 1.47 ms, 1.31 PFLOP/s (1.4 us per K tile of 256 x
+// 256, 1.0 at the dense peak of a 2.1 GHz clock).  Small batches are bound by L2:
+// 256 tokens, 4096 x 6144 read 200 MB of operand tiles in 24 us.
 template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED>
 __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
     constexpr int NW = WM * WN, BK = 64, KK = 2;
@@ -597,7 +602,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
 // 16 ranks of a slice), 8 waves each taking every eighth 64-column step of K
 // straight from global memory into 16x16x32 MFMA fragments; the waves' sums
 // are added in order.  Work-groups of y past the block's slots end at once;
-// y = 0 clears buf for the tokens without a slot.
+// y = 0 clears buf for the tokens without a slot.  Latency: one slot's loads and
+// sums take 7.6 us (one token, K 4096, rank 16); past some tokens the lora_a
+// reads per block of 16 (777 tokens, 1352, rank 24, 5 slots: 10.7 us).
 constexpr int kShWaves = 8;
 struct LinShrinkArgs {
     const uint16_t *x;
@@ -708,7 +715,7 @@ __device__ __forceinline__ void add_delta(floatx4_t &r, const LinArgs &a, const 
 // from global memory into 16x16x32 MFMA fragments -- W is read once, 64 bytes
 // of 16 rows per load, with U steps in flight.  The waves' sums are added in
 // order through LDS; then each thread adds the delta of one token and 4
-// columns.
+// columns.  4096 x 6144: 14 us for one token, 3.6 TB/s of W.
 constexpr int kFewWaves = 8;
 template <int TB, int CT, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
@@ -921,7 +928,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
 // layout of a 16x16 MFMA result (row lane % 16, 4 columns).  The delta: for each
 // slot among the 16 rows, its lora_b rows straight from global memory into
 // fragments (the next step's loads in flight), times the rows' scaled rank
-// vectors split into two bf16 parts, kept by the slot's own rows only.
+// vectors split into two bf16 parts, kept by the slot's own rows only.  Bound by
+// those rows: 1024 tokens of 128 slots, 8192 columns, ranks to 128: 60 us; with
+// no delta 4.2 us for 96 x 4096 in four splits.
 constexpr int kJoinRows = 16;
 constexpr int kJoinCols = 256;
 __global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
@@ -1162,7 +1171,8 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
 // own, scales, splits into bf16 parts, and clears buf for tokens without a
-// slot.
+// slot.  Latency bound: 12.8 us for 8192 tokens of 2 x 64 ranks with the row order,
+// 5.3 for 1024 of 128.
 constexpr int kRedThreads = 256;
 struct LinReduceArgs {
     LinVectors job[2];
@@ -1347,6 +1357,9 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
         return run_few<4, 2, 2>(a, st);
     }
+    // 256 x 256 from 192 tiles on, most of a tile per CU (4096 tokens, 4096 x 4096, 256
+    // tiles: 143 us, 163 with 128 x 128; 2048 tokens, 4096 x 6144, 192 tiles: 132 and
+    // 128; 128 tiles: 132 and 97).
     if (!a.join_delta && a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
         return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
     // Fewer tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
@@ -1374,12 +1387,16 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         t64 += (int64_t)a.S * ((a.L * a.R + 63) / 64) * ((a.T + 63) / 64);
     }
     // From 192 tiles of 128 x 128 on a join costs more than even work-groups give
-    // (2048 tokens, 4096 x 4096: 97 us; 132 with 256 x 256, 147 with 64 x 64); where
-    // it runs anyway, two or three splits even them out up to 340 tiles (512
-    // tokens, 4096 x 6144, 204 tiles: 58.5, two splits 54.9; 1024 tokens, 14336 x
-    // 4096, 264 tiles: 198, 172 and 156; 452 tiles: 117 and 126 with two).
+    // (2048 tokens, 4096 x 4096: 97 us; 132 with 256 x 256, 147 with 64 x 64), but
+    // for one tile per CU of many K tiles, which two splits overlap (the gradient of
+    // 1024 tokens, 28672 x 4096, 448 K tiles: 303 and 277; 6144 x 4096, 96 K tiles:
+    // 94.7 and 96.2).  Where a join runs anyway, two or three splits even the
+    // work-groups out up to 340 tiles (512 tokens, 4096 x 6144, 204 tiles: 58.5,
+    // two splits 54.9; 1024 tokens, 14336 x 4096, 264 tiles: 198, 172 and 156; 452
+    // tiles: 117 and 126 with two).
     if (t128 >= 192) {
-        const int k = !a.join_delta || t128 > 340 || nk < 24 ? 1 : t128 > 256 ? 3 : 2;
+        int k = t128 <= 256 && nk >= 192 ? 2 : 1;
+        if (a.join_delta && t128 <= 340 && nk >= 24) k = t128 > 256 ? 3 : 2;
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, k, st);
     }
     if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 20480))

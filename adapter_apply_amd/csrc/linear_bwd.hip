@@ -44,7 +44,9 @@ struct PadArgs {
     int64_t ldo;
 };
 // dy with every slice padded by zeros to whole 8-element units (widths that
-// are multiples of 4 only): 8 bytes per thread.
+// are multiples of 4 only): 8 bytes per thread.  Bound by its bytes (1501 x 1652:
+// 5.3 us); reading the unpadded rows in the kernels would cost each of them the
+// 16-byte loads.
 __global__ __launch_bounds__(kPadThreads) void k_lin_pad(PadArgs a) {
     const int64_t units = a.ldo / 4, total = units * a.T;
     for (int64_t q = (int64_t)blockIdx.x * kPadThreads + threadIdx.x; q < total;
@@ -61,7 +63,8 @@ __global__ __launch_bounds__(kPadThreads) void k_lin_pad(PadArgs a) {
 
 // v: work-group = (tile of at most 64 tokens of one slot, slice, RB ranks,
 // split of the slice's columns), 4 waves of 16 tokens.  A stage is 64 columns
-// of dy's rows and 64 rows of lora_b.
+// of dy's rows and 64 rows of lora_b, three in flight.  Bound by dy's bytes: 8192
+// tokens of 28672 columns, 470 MB in 103 us.
 struct DuArgs {
     const uint16_t *dy;
     int64_t lddy;
@@ -156,7 +159,9 @@ __global__ __launch_bounds__(256) void k_lin_du(DuArgs a) {
 // token split), 4 waves of 32 columns, 32 tokens per stage (both operands
 // through transposed reads; the rank vectors' three bf16 parts, which hold the
 // whole fp32 value, add into the same accumulators).  Slots without tokens
-// write zeros.
+// write zeros.  Bound by its bytes: 8192 tokens, 4096 -> 28672, rank 64, 16 slots,
+// some 750 MB in 164 us (250 with two stages of 64 tokens); 4096 tokens, 14336 ->
+// 4096, rank 32, 170 MB in 35 us.
 constexpr int kWgCols = 128;
 constexpr int kWgTokens = 1024;       // token indexes staged at a time
 constexpr int kWgStep = 32;           // tokens per stage
