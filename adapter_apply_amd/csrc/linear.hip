@@ -931,9 +931,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
 // vectors split into two bf16 parts, kept by the slot's own rows only.  Bound by
 // those rows: 1024 tokens of 128 slots, 8192 columns, ranks to 128: 60 us; with
 // no delta 4.2 us for 96 x 4096 in four splits.
+// (Three waves per SIMD: without a bound the compiler takes registers for two, 73
+// us; bounded to four it spills, 99.)
 constexpr int kJoinRows = 16;
 constexpr int kJoinCols = 256;
-__global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
+__global__ __launch_bounds__(256, 3) void k_lin_join(LinArgs a) {
     constexpr int NB = 4;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
     const int m = blockIdx.y * kJoinRows + l16;
