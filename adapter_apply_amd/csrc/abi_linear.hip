@@ -22,6 +22,7 @@ struct LinWs {
     size_t order;       // int32 [2][T]: row order of the tile GEMM and the rows' slots
     size_t hl_u;        // bf16 [S][T][kLinPartsBwd R]: scale * u in parts
     size_t hl_v;        // the same of v
+    size_t v;           // fp32 [S][T][R]: v by token (wide gradients)
     size_t part;        // fp32 partial sums
     size_t pad;         // dy with slices of whole 8-element units, when some N_s % 8
     size_t end;
@@ -37,6 +38,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     w.order = o; o = align256(o + 2 * sizeof(int32_t) * (size_t)T);
     w.hl_u = o;  o = align256(o + 2 * kLinPartsBwd * tsr);
     w.hl_v = o;  o = align256(o + 2 * kLinPartsBwd * tsr);
+    w.v = o;     o = align256(o + 4 * tsr);
     w.part = o;
     // the shrink's K splits: either one, or within an eighth of its input
     // bytes (pre_kspl: 8 k T S R <= in_bytes / 8)
@@ -179,7 +181,7 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
     for (int s = 0; s < S; ++s) {
         a.lora[s] = static_cast<const uint16_t *>(B[s]);
-        a.la[s] = static_cast<const uint16_t *>(A[s]);
+        a.other[s] = static_cast<const uint16_t *>(A[s]);
         a.n[s] = N[s];
         a.off[s] = sl.off[s];
     }
@@ -235,7 +237,8 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
     uint16_t *hl_v = reinterpret_cast<uint16_t *>(wp + wl.hl_v);
     float *part = reinterpret_cast<float *>(wp + wl.part);
     int32_t *order = reinterpret_cast<int32_t *>(wp + wl.order);
-    if (!(flags & LORA_FLAG_SEGMENTS_READY))
+    const bool wide = dx && W && lin_wide_gradient(T, K, N, S, R, L, dA || dB);
+    if (!(flags & LORA_FLAG_SEGMENTS_READY) && (dA || dB || !wide))
         CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
 
     // dy with whole 8-element units per slice
@@ -270,14 +273,34 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
             job[n_jobs++] = v;
         }
     }
-    if (dx || dA) {
+    LinArgs a{};
+    a.p = p; a.ldp = ldp;
+    a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
+    a.out = static_cast<uint16_t *>(dx); a.ldo = lddx;
+    a.part = part;
+    a.idx = idx; a.slot_rank = slot_rank; a.scale = scale;
+    a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
+    for (int s = 0; s < S; ++s) {
+        a.lora[s] = static_cast<const uint16_t *>(A[s]);
+        a.other[s] = static_cast<const uint16_t *>(B[s]);
+        a.n[s] = N[s];
+        a.off[s] = sl.off[s];
+        a.poff[s] = poff[s];
+    }
+    if (wide) {
+        float *v = reinterpret_cast<float *>(wp + wl.v);
+        a.wide = a.join_delta = 1;
+        a.buf = dA ? v : nullptr;
+        CHECK(launched(launch_lin_gemm(a, true, st)));
+        if (dA) job[n_jobs++] = LinVectors{nullptr, 0, v, hl_v, kLinPartsBwd, nullptr};
+    } else if (dx || dA) {
         const int32_t nsp = lin_du_splits(T, L, N, S, R);
         CHECK(launched(launch_lin_du(p, ldp, poff, T, sl, S, L, R, seg, part, nsp, st)));
         job[n_jobs++] = LinVectors{part, nsp, nullptr, hl_v, kLinPartsBwd, nullptr};
     }
     if (n_jobs)
         CHECK(launched(launch_lin_vectors(job, n_jobs, T, S, L, R, idx, slot_rank, scale, seg,
-                                          dx ? order : nullptr, st)));
+                                          dx && !wide ? order : nullptr, st)));
     if (dA || dB) {
         LinWgArgs wa{}, wb{};
         wa.T = T; wa.S = S; wa.L = L; wa.R = R; wa.slot_rank = slot_rank; wa.seg = seg;
@@ -297,21 +320,9 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         wb.part = part + (dA && wa.nsp > 1 ? wa.nsp * lin_wg_part(L, wa.m, S, R) : 0);
         CHECK(launched(launch_lin_wg(dA ? &wa : nullptr, dB ? &wb : nullptr, st)));
     }
-    if (dx) {
-        LinArgs a{};
-        a.p = p; a.ldp = ldp;
-        a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
-        a.out = static_cast<uint16_t *>(dx); a.ldo = lddx;
-        a.part = part;
-        a.hl = hl_v; a.hl_row = kLinPartsBwd * R; a.order = order; a.idx = idx; a.slot_rank = slot_rank;
-        a.T = T; a.K = K; a.S = S; a.L = L; a.R = R;
+    if (dx && !wide) {
+        a.hl = hl_v; a.hl_row = kLinPartsBwd * R; a.order = order;
         a.accumulate = W == nullptr;
-        for (int s = 0; s < S; ++s) {
-            a.lora[s] = static_cast<const uint16_t *>(A[s]);
-            a.n[s] = N[s];
-            a.off[s] = sl.off[s];
-            a.poff[s] = poff[s];
-        }
         CHECK(launched(launch_lin_gemm(a, true, st)));
     }
     return LORA_OK;

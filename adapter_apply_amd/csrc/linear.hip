@@ -82,28 +82,28 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         nt = r / rows;
         mt = g * gm + r - nt * rows;
     }
-    // forward: the tile's slice, whose rows of W start at qb; or, past those of a
-    // wide batch, its lora_a rows of every slot
+    // forward: the tile's slice, whose rows of W start at qb; past those in a wide
+    // batch (vec), every slot's lora_a rows of a slice, in the gradient its lora_b
+    // columns, whose contraction is the slice's alone
     int sc = 0;
     const uint16_t *qb = a.w;
     int64_t ldq = a.ldw, c0 = (int64_t)nt * BN, cend = a.K, obase = 0;   // columns: first, end, slice's first in out
-    if (!NN) {
+    const bool vec = MIXED && nt >= a.base_tiles;
+    if (vec) {
+        const int per = (a.L * a.R + BN - 1) / BN;
+        nt -= a.base_tiles;
+        sc = nt / per;
+        c0 = (int64_t)(nt - sc * per) * BN;
+        cend = a.L * a.R;
+        qb = a.other[sc];
+        ldq = NN ? a.R : a.K;
+        obase = a.cols + sc * cend;
+    } else if (!NN) {
         while (sc + 1 < a.S && nt >= a.tile_start[sc + 1]) ++sc;
-        if (MIXED && nt >= a.tile_start[a.S]) {
-            const int per = (a.L * a.R + BN - 1) / BN;
-            nt -= a.tile_start[a.S];
-            sc = nt / per;
-            c0 = (int64_t)(nt - sc * per) * BN;
-            cend = a.L * a.R;
-            qb = a.la[sc];
-            ldq = a.K;
-            obase = a.cols + sc * cend;
-        } else {
-            c0 = (int64_t)(nt - a.tile_start[sc]) * BN;
-            cend = a.n[sc];
-            qb += a.off[sc] * ldq;
-            obase = a.off[sc];
-        }
+        c0 = (int64_t)(nt - a.tile_start[sc]) * BN;
+        cend = a.n[sc];
+        qb += a.off[sc] * ldq;
+        obase = a.off[sc];
     }
     const int m0 = mt * BM;
 
@@ -170,7 +170,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     // (and slice) the [high | low] rank vectors.
     int nk = 0, k0 = 0;
     if (a.w) {
-        if (NN)
+        if (NN && vec)
+            nk = (int)((a.n[sc] + BK - 1) / BK);
+        else if (NN)
             for (int s = 0; s < a.S; ++s) nk += (int)((a.n[s] + BK - 1) / BK);
         else
             nk = (a.K + BK - 1) / BK;
@@ -216,8 +218,13 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         qptr[i] = a.w;
         if (a.w) {
             if (NN) {
-                const int64_t col = c0 + qlc(i) * 8;
-                qptr[i] += (int64_t)qrow(i) * a.ldw + (col < cend ? col : 0);
+                int64_t col = c0 + qlc(i) * 8;
+                if (col >= cend) col = 0;
+                if (vec) {                        // (slot, rank): whole units of one slot
+                    const int slot = (int)col / a.R;
+                    col += (a.n[sc] - 1) * slot * a.R;
+                }
+                qptr[i] = qb + qrow(i) * ldq + col;
             } else {
                 const int64_t n = min(c0 + qrow(i), cend - 1);
                 qptr[i] = qb + n * ldq + qlc(i) * 8;
@@ -229,9 +236,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
 
     // The next base K tile: steps left in its row (forward) or slice, and the
     // offsets into the P and Q rows.
-    int cs = 0;
-    int64_t rem = NN ? a.n[0] : a.K, po = NN ? a.poff[0] : 0, qo = NN ? a.off[0] * a.ldw : 0;
-    const int64_t qstep = NN ? BK * a.ldw : BK;
+    int cs = NN ? sc : 0;
+    int64_t rem = NN ? a.n[cs] : a.K, po = NN ? a.poff[cs] : 0, qo = 0;   // (off[0] is 0)
+    const int64_t qstep = NN ? BK * ldq : BK;
     auto next_slice = [&]() {
         if (NN && rem <= 0 && ++cs < a.S) {
             rem = a.n[cs];
@@ -241,11 +248,11 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     };
     auto advance = [&]() { rem -= BK; po += BK; qo += qstep; };
     if (MIXED && k0) {
-        if (NN)
+        if (NN && !vec)
             for (; (int64_t)k0 * BK >= a.n[cs]; ++cs) k0 -= (int)((a.n[cs] + BK - 1) / BK);
         rem = (NN ? a.n[cs] : a.K) - (int64_t)k0 * BK;
         po = (NN ? a.poff[cs] : 0) + (int64_t)k0 * BK;
-        qo = NN ? (a.off[cs] + (int64_t)k0 * BK) * a.ldw : (int64_t)k0 * BK;
+        qo = NN ? ((vec ? 0 : a.off[cs]) + (int64_t)k0 * BK) * ldq : (int64_t)k0 * BK;
     }
     auto issue = [&](int v, int stage) {
         // recomputed here each time: hoisted lane values would crowd the
@@ -839,7 +846,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_lin_one(LinArgs a) {
             sc_own = a.scale[so];
 #pragma unroll
             for (int i = 0; i < NRB; ++i)
-                ar[i] = a.la[sc] + ((int64_t)so * a.R + min(i * 16 + l16, a.R - 1)) * a.K;
+                ar[i] = a.other[sc] + ((int64_t)so * a.R + min(i * 16 + l16, a.R - 1)) * a.K;
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 const uint16_t *b = a.lora[sc] + ((int64_t)so * cend + min(c0 + i * 16 + l16, cend - 1)) * a.R;
@@ -1075,6 +1082,7 @@ __global__ __launch_bounds__(256, 3) void k_lin_join(LinArgs a) {
 
 // Two columns c, c + 1 of one token: the sum of the splits o, bias, delta (the
 // rank vector from u), rounded once.
+template <bool NN>
 __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int slot, int rank,
                                          const float2 (&o)[kLinMaxSplits], const float *u, int64_t ldu) {
     if (c >= a.cols) return;
@@ -1089,7 +1097,27 @@ __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int
         v0 += bf16_to_f32(a.bias[c]);
         v1 += bf16_to_f32(a.bias[c + 1]);
     }
-    if (slot >= 0) {
+    if (NN && slot >= 0) {
+        float d0 = 0.f, d1 = 0.f;
+        for (int s = 0; s < a.S; ++s) {
+            const uint16_t *b = a.lora[s] + (int64_t)slot * a.R * a.K + c;
+            const float *us = u + s * ldu;
+            for (int j = 0; j < rank; j += 8) {   // (vectors are zero past the rank)
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = ldg<uint32_t>(b + (int64_t)(j + e) * a.K);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d0 += us[j + e] * bf16_lo(w[e]);
+                    d1 += us[j + e] * bf16_hi(w[e]);
+                }
+            }
+        }
+        const float sc = a.scale[slot];
+        v0 += sc * d0;
+        v1 += sc * d1;
+    }
+    if (!NN && slot >= 0) {
         // the column's slice by selects (an index that differs between lanes
         // would load the arguments from memory, one after the other)
         int s = 0;
@@ -1128,7 +1156,8 @@ __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int
 // 12.6 us).  Work-group = one token x 512 columns, 2 per thread, so that a
 // wave's lora_b loads cover whole lines: fp32 FMAs with the token's rank vector.
 // In a wide batch every work-group first sums the splits of its token's rank
-// vector.
+// vector.  Gradient (NN, wide only): v against the slot's lora_a rows.
+template <bool NN>
 __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
     const int t = blockIdx.y;
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
@@ -1140,7 +1169,7 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
     for (int k = 0; k < kLinMaxSplits; ++k)
         if (k < a.ksp) o[k] = *reinterpret_cast<const float2 *>(pt + k * split + min(c, a.cols - 2));
     const int rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
-    if (a.wide) {
+    if (NN || a.wide) {
         __shared__ __attribute__((aligned(16))) float s_u[kLinWideRanks];
         const int LR = a.L * a.R;
         for (int q = threadIdx.x; q < a.S * a.R; q += 256) {
@@ -1160,7 +1189,7 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
             if (a.buf && blockIdx.x == 0) a.buf[((int64_t)s * a.T + t) * a.R + j] = u;
         }
         __syncthreads();
-        join_row(a, t, c, slot, rank, o, s_u, a.R);
+        join_row<NN>(a, t, c, slot, rank, o, s_u, a.R);
         return;
     }
     if (a.buf && slot < 0 && blockIdx.x == 0) {
@@ -1168,7 +1197,7 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
         for (int s = 0; s < a.S; ++s)
             for (int j = threadIdx.x; j < a.R; j += 256) a.buf[((int64_t)s * a.T + t) * a.R + j] = 0.f;
     }
-    join_row(a, t, c, slot, rank, o, a.u + (int64_t)t * a.R, (int64_t)a.T * a.R);
+    join_row<NN>(a, t, c, slot, rank, o, a.u + (int64_t)t * a.R, (int64_t)a.T * a.R);
 }
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
@@ -1290,7 +1319,7 @@ int column_tiles(LinArgs &a, int b) {
 template <int BM, int BN, int WM, int WN, int NST, bool MIXED>
 hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     a.m_tiles = (a.T + BM - 1) / BM;
-    a.n_tiles = gradient ? (a.K + BN - 1) / BN : column_tiles(a, BN);
+    a.base_tiles = a.n_tiles = gradient ? (a.K + BN - 1) / BN : column_tiles(a, BN);
     a.ksp = ksp;
     int64_t cols = a.K;
     if (!gradient) {
@@ -1309,8 +1338,11 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    if (a.join_delta && !a.order)
-        hipLaunchKernelGGL(k_lin_join_rows, dim3((unsigned)((cols + 511) / 512), (unsigned)a.T), dim3(256), 0, st, a);
+    const dim3 rows((unsigned)((cols + 511) / 512), (unsigned)a.T);
+    if (a.join_delta && gradient)
+        hipLaunchKernelGGL(k_lin_join_rows<true>, rows, dim3(256), 0, st, a);
+    else if (a.join_delta && !a.order)
+        hipLaunchKernelGGL(k_lin_join_rows<false>, rows, dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols),
                                             (unsigned)((a.T + kJoinRows - 1) / kJoinRows)), dim3(256), 0, st, a);
@@ -1482,6 +1514,23 @@ bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
 // of the slot-grouped kernels, 128 slots 54.0 against 66.6).
 bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     return !lin_few(T, K, N, S, R, L) && wide_cols(columns(N, S), S, R, L) > 0;
+}
+
+// The same for dx: v = dy B of every slot as further columns, added by the join,
+// which reads S R lora_a rows per token.  weights: dA or dB are wanted too, which
+// need the segments and the vectors in parts either way.  Against the sorted form
+// (us; MB of lora_a and sums): dx alone, rank 16, 8 slots, 6144 x 4096: 16 tokens 22.1
+// and 42.1, 256 (117 MB) 37.2 and 54.0, 512 (235 MB) 52.9 and 67.2, 1024 (470 MB)
+// 97.6 and 93.8; with weights 96 tokens 45.4 and 55.3, 256 55.9 and 62.0; rank 64,
+// 96 tokens (157 MB) 67.7 and 72.5, 256 (420 MB) 81.8 and 78.0; 4096 x 14336, 256
+// tokens (176 MB) 72.6 and 75.7; 8192 x 8192, 512 tokens (201 MB) 124 and 113; 2048
+// x 2048, 1024 tokens (100 MB) 49.6 and 46.1.  A contraction many times K keeps
+// the further columns' few tiles long: 28672 x 4096, 96 tokens, with weights 119
+// and 108.
+bool lin_wide_gradient(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights) {
+    if (T > (weights ? 512 : kLinDirectTokens) || wide_cols(K, S, R, L) == 0) return false;
+    if (weights && columns(N, S) > 4 * (int64_t)K) return false;
+    return (int64_t)T * K * (2 * S * R + 16) <= (weights ? kLinWideBytesB : kLinWideBytesA);
 }
 
 // Direct batches whose rank vectors the slot-grouped kernels find (whole

@@ -29,10 +29,11 @@ struct LinArgs {
     int32_t join_delta;       // the join adds the delta, not the tiles
     const float *u;           // fp32 rank vectors [S][T][R] of the join and of k_lin_few
     const float *scale;
-    int32_t wide;             // x A^T of every slot as S L R further columns of part (lin_wide)
+    int32_t wide;             // rank vectors of every slot, x A^T or dy B, as S L R further columns of part
+    int32_t base_tiles;       // column tiles before those
     float *buf;               // where u goes if it is wanted: k_lin_one, join of wide batches; of other
                               // batches the join only clears the rows of tokens without a slot
-    const uint16_t *la[kMaxSlices];     // k_lin_one and wide: lora_a [L][R][K]
+    const uint16_t *other[kMaxSlices];  // k_lin_one and wide: lora_a [L][R][K]; wide gradient: lora_b
     float *part;
     int64_t part_ld;          // its row: cols, and the further columns of wide batches
     int64_t cols;             // columns of out
@@ -62,12 +63,14 @@ constexpr int kLinDirectTokens = 1024;
 constexpr int64_t kLinDirectBytesA = 128 << 20;
 constexpr int64_t kLinDirectBytesB = 110 << 20;
 constexpr int64_t kLinWideBytesB = 176 << 20;
+constexpr int64_t kLinWideBytesA = 224 << 20;
 // fp32 sums of a call: splits times T columns.  At most 1020 tiles of 128 x 128
 // (launch_lin_gemm), unsplit batches bounded by lin_join_delta and lin_direct.
 constexpr int64_t kLinJoinMax = 1 << 25;
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
+bool lin_wide_gradient(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights);
 constexpr int kLinWideRanks = 1024;     // most S R of a wide batch
 hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, const Slices &sl,
                              int32_t S, int32_t L, int32_t R, const int32_t *idx,

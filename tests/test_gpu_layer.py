@@ -15,6 +15,10 @@ FILL = 7.0
 # many.
 SHAPES = [
     (1, 8, (4,), 8, 1, 0),                 # one launch
+    (1, 648, (72, 20), 16, 3, 0),          # v as further columns of dx
+    (70, 1032, (100, 360, 4), 40, 7, 4),
+    (128, 4096, (64, 1000), 64, 24, 8),
+    (1024, 392, (72,), 8, 40, 0),
     (1, 4096, (512, 128, 128), 16, 8, 0),
     (1, 72, (36, 20), 32, 3, 4),
     (1, 64, (16400,), 16, 2, 0),           # one token, many columns
@@ -93,6 +97,20 @@ def test_backward(shape, given):
     assert bool((full[:, K:] == FILL).all()), "columns past K were written"
 
 
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] < 1100], ids=str)
+def test_backward_of_x_alone(shape):
+    T, K, N, R, L, extra = shape
+    c = Layer(T, K, N, R, L, seed=T + K + 2, extra=extra)
+    dx_ref, dx_tol = c.backward()[:2]
+    full = torch.full((T, K + 8), FILL, dtype=torch.bfloat16, device="cuda")
+    ws = aa.alloc_linear_workspace(T, K, N, R, L)
+    for _ in range(2):
+        aa.lora_linear_backward(full[:, :K], None, None, c.dy, c.x, c.W, c.A, c.B, c.idx, c.rank, c.scale, ws)
+        within(full[:, :K], dx_ref, dx_tol, "dx")
+        assert bool((full[:, K:] == FILL).all()), "columns past K were written"
+        full[:, :K] = FILL
+
+
 @pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] in (17, 200, 1000, 2100)], ids=str)
 def test_backward_in_place(shape):
     """W None: dx += the adapters' part; rows without an adapter keep their bits."""
@@ -111,10 +129,11 @@ def test_backward_in_place(shape):
     assert torch.equal(dx[none], base[none])
 
 
-def test_accumulate_and_parts():
+@pytest.mark.parametrize("T,K", [(700, 136), (90, 1032)])
+def test_accumulate_and_parts(T, K):
     """Two accumulated calls add up; a call that wants one output only gives
     the bits of the call that wants all."""
-    T, K, N, R, L = 700, 136, (100, 36), 24, 5
+    N, R, L = (100, 36), 24, 5
     c = Layer(T, K, N, R, L, seed=9)
     dx = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
     dA, dB = run_backward(c, dx)
@@ -187,7 +206,7 @@ def test_no_adapter_anywhere(T):
     within(dx, ref, tol, "dx")
 
 
-@pytest.mark.parametrize("T,K,N", [(1, 136, (100, 36)), (12, 136, (100, 36)), (100, 136, (100, 36)),
+@pytest.mark.parametrize("T,K,N", [(1, 136, (100, 36)), (12, 136, (100, 36)), (100, 136, (100, 36)), (50, 1032, (100, 36)),
                                    (700, 136, (100, 36)), (1200, 2048, (260,)),
                                    (1100, 136, (3200,)), (2100, 1032, (5000, 260)),
                                    (2100, 5640, (100, 36))], ids=str)
