@@ -1396,19 +1396,13 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     // 128; 128 tiles: 132 and 97).
     if (!a.join_delta && a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
         return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
-    // Fewer tiles: K splits (about kLinSplitTiles work-groups, at least 8 K tiles
-    // each), joined by a second launch.  Tiles of 64 x 64 read each operand
-    // twice as often, which shows once all their K tiles together pass some
-    // 20000 (256 tokens, K x N: 2048 x 2048 26.1 against 27.6 us with 128 x 128,
-    // 4096 x 4096 46.3 against 49.0, 4096 x 6144 49.1 against 46.8, 14336 x 4096
-    // 86.9 against 79.5), or once they no longer run at the same time (the gradient
-    // of 1501 tokens, 1652 x 1352, 528 of them: 61.4 against 53.1).
     int64_t nk = (a.K + 63) / 64;
     if (gradient) {
         nk = 0;
         for (int s = 0; s < a.S; ++s) nk += (a.n[s] + 63) / 64;
     }
     if (!a.w) nk = 0;
+    // K splits, about kLinSplitTiles work-groups of at least 8 K tiles each
     auto splits = [&](int64_t t) {
         int64_t k = kLinSplitTiles / t;
         if (k > nk / 8) k = nk / 8;
@@ -1433,9 +1427,17 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         if (a.join_delta && t128 <= 340 && nk >= 24) k = t128 > 256 ? 3 : 2;
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, k, st);
     }
-    if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 20480))
+    // Fewer tiles: K splits, joined by a second launch.  Tiles of 64 x 64 read each operand
+    // twice as often, which shows once all their K tiles together pass some
+    // 16000 (256 tokens, K x N, with and against 128 x 128: 2048 x 2048 16.1 and
+    // 20.0 us, 4096 x 4096 41.0 and 36.9, 14336 x 4096 89.4 and 52.1; 128 tokens,
+    // 4096 x 6144 26.3 and 31.0), or once they no longer run at the same time (the
+    // gradient of 1501 tokens, 1652 x 1352, 528 of them: 61.4 and 53.1).
+    if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 16384))
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, splits(t128), st);
-    return run_tile<64, 64, 2, 2, 4, true>(a, gradient, splits(t64), st);
+    // (two stages: a work-group has few K tiles, and more stages fill for longer;
+    // 16 tokens of 14336 x 4096: 26.3 us, with four 28.2)
+    return run_tile<64, 64, 2, 2, 2, true>(a, gradient, splits(t64), st);
 }
 
 // Whether a sorted forward batch leaves the delta to the join: when the
