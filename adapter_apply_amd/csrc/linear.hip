@@ -1427,9 +1427,9 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         if (a.join_delta && t128 <= 340 && nk >= 24) k = t128 > 256 ? 3 : 2;
         return run_tile<128, 128, 2, 2, 2, true>(a, gradient, k, st);
     }
-    // Fewer tiles: K splits, joined by a second launch.  Tiles of 64 x 64 read each operand
-    // twice as often, which shows once all their K tiles together pass some
-    // 16000 (256 tokens, K x N, with and against 128 x 128: 2048 x 2048 16.1 and
+    // Fewer tiles: K splits, joined by a second launch.  Tiles of 64 x 64 read each
+    // operand twice as often, which shows once all their K tiles together pass some
+    // 16000 (256 tokens, K x N, with them and with 128 x 128: 2048 x 2048 16.1 and
     // 20.0 us, 4096 x 4096 41.0 and 36.9, 14336 x 4096 89.4 and 52.1; 128 tokens,
     // 4096 x 6144 26.3 and 31.0), or once they no longer run at the same time (the
     // gradient of 1501 tokens, 1652 x 1352, 528 of them: 61.4 and 53.1).

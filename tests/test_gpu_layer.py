@@ -277,11 +277,12 @@ def test_another_stream_and_repeats(T):
     assert all(torch.equal(p, q) for p, q in zip(dA + dB, dA2 + dB2))
 
 
-@pytest.mark.parametrize("T", [20, 600, 5000])
-def test_graph_replays(T):
+@pytest.mark.parametrize("T,K,N", [(20, 136, (100, 36)), (600, 136, (100, 36)), (5000, 136, (100, 36)),
+                                   (90, 520, (264, 136))])
+def test_graph_replays(T, K, N):
     """Two graphs on one workspace, replayed in turn with new inputs and eager
     calls between, equal the eager calls bit for bit."""
-    K, N, R, L = 136, (100, 36), 16, 5
+    R, L = 16, 5
     c = Layer(T, K, N, R, L, seed=7)
     ws = aa.alloc_linear_workspace(T, K, N, R, L)
     y = torch.empty((T, sum(N)), dtype=torch.bfloat16, device="cuda")
