@@ -247,7 +247,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         }
     };
     auto advance = [&]() { rem -= BK; po += BK; qo += qstep; };
-    if (MIXED && k0) {
+    if (MIXED && k0 && nk > 0) {
         if (NN && !vec)
             for (; (int64_t)k0 * BK >= a.n[cs]; ++cs) k0 -= (int)((a.n[cs] + BK - 1) / BK);
         rem = (NN ? a.n[cs] : a.K) - (int64_t)k0 * BK;
@@ -622,9 +622,8 @@ struct LinShrinkArgs {
     float *buf;
 };
 
-// U: steps in flight (8: K <= 4096 is one round of loads).
-template <int U>
 __global__ __launch_bounds__(kShWaves * 64) void k_lin_shrink(LinShrinkArgs a) {
+    constexpr int U = 4;                          // steps in flight
     __shared__ floatx4_t s_sum[kShWaves][64];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
@@ -1385,9 +1384,7 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     if (!gradient && lin_one(a.T, a.K, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
     if (!gradient && lin_few(a.T, a.K, a.n, a.S, a.R, a.L)) {
-        // (a round of eight steps is 4096 of K, and steps past K load too: 2048
-        // columns of K 2048, 16 tokens: 13.2 us with four steps, 16.5 with eight)
-        if (a.T <= 16) return a.K > 2048 ? run_few<1, 1, 8>(a, st) : run_few<1, 1, 4>(a, st);
+        if (a.T <= 16) return run_few<1, 1, 4>(a, st);
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
         return run_few<4, 2, 2>(a, st);
     }
@@ -1402,10 +1399,14 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         for (int s = 0; s < a.S; ++s) nk += (a.n[s] + 63) / 64;
     }
     if (!a.w) nk = 0;
-    // K splits, about kLinSplitTiles work-groups of at least 8 K tiles each
+    // K splits, about kLinSplitTiles work-groups of at least 8 K tiles each; 4 of a
+    // few tokens that are joined anyway, whose sums are small (4 tokens of 1352 x
+    // 1652 9.7 us, 11.5 with 8; 64 tokens 11.3 and 12.3, of 2048 x 2048 12.1 and
+    // 11.7; 128 tokens 14.2 and 13.4)
+    const int least = a.join_delta && a.T <= 64 ? 4 : 8;
     auto splits = [&](int64_t t) {
         int64_t k = kLinSplitTiles / t;
-        if (k > nk / 8) k = nk / 8;
+        if (k > nk / least) k = nk / least;
         if (k > kLinMaxSplits) k = kLinMaxSplits;
         return (int)(k < 1 ? 1 : k);
     };
@@ -1459,18 +1460,6 @@ bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R
     return slots * ((2 * R + 63) / 64) > K / 64 * ((int64_t)T * n <= 1 << 22 ? 0.25 : 0.4);
 }
 
-// One token of rank at most 32 takes the one launch of k_lin_one, while its
-// work-groups, each reading the slot's lora_a rows, are not too many.  Against
-// k_lin_shrink and k_lin_few, us: K 4096, 6144 columns 16.6 and 21.8 at rank 16,
-// 19.9 and 22.3 at rank 32; 16384 columns 29.7 and 31.5 at rank 8, 36.7 and 33.7
-// at rank 32; 28672 columns 52.4 and 47.5.
-bool lin_one(int32_t T, const int64_t *N, int32_t S, int32_t R) {
-    if (T != 1 || R > 32) return false;
-    int64_t n = 0;
-    for (int s = 0; s < S; ++s) n += N[s];
-    return n <= (R <= 16 ? 16384 : 8192);
-}
-
 // The further columns of a wide batch, x A^T of every slot, in whole 64-column
 // tiles; 0 when they would be more than the layer's own (or their vectors more
 // than the join holds).
@@ -1484,31 +1473,31 @@ static int64_t columns(const int64_t *N, int32_t S) {
     return n;
 }
 
-// One token of rank at most 32 takes the one launch of k_lin_one, while its
-// work-groups, each reading the slot's lora_a rows, are not too many and K is
-// not too long for one round of loads after the other.  Against the wide tiles,
-// us: K x N of 4096 x 6144 16.6 and 18.3 at rank 16; 8192 x 8192 32.7 and 31.7;
-// 4096 x 28672 52.4 and 42.8; 14336 x 4096 43.2 and 27.2.  (Against k_lin_shrink
-// and k_lin_few, rank 32, 4096 x 16384: 36.7 and 33.7.)
+// One token of rank at most 32 takes the one launch of k_lin_one while K is at
+// most two rounds of its loads and its work-groups, each reading the slot's
+// lora_a rows, are not too many.  Against the wide tiles (two launches), us: K x N
+// of 2048 x 2048 8.7 and 10.0, rank 32 10.5 and 10.8; 1024 x 16384 9.7 and 15.0;
+// 4096 x 4096 15.3 and 13.9, 4096 x 6144 16.7 and 16.7, rank 32 19.9 and 18.1, 4096
+// x 8192 17.7 and 18.6; 5120 x 5120 18.5 and 16.9; 8192 x 1024 25.3 and 12.2.
 bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R) {
-    return T == 1 && R <= 32 && K <= 8192 && columns(N, S) <= (R <= 16 ? 16384 : 8192);
+    const int64_t n = columns(N, S);
+    return T == 1 && R <= 32 && n <= 16384 && (K <= 2048 || (K <= 4096 && R <= 16 && n > 4096));
 }
 
 // Whether k_lin_few (or k_lin_one) takes a forward batch.  Its work-groups read
 // x over and over, so the tiles overtake it as tokens times W grow.  Against
-// the wide tiles (us, rank 16 to 24): 1352 x 1652, 16 tokens 11.0 and 12.6, 32
-// tokens 13.7 and 12.6; 2048 x 2048, 2 tokens 10.8 and 10.9, 8 tokens 12.0 and
-// 11.1; 4096 x 6144, 2 tokens 22.3 and 18.5, with as many further columns 22.3
-// and 25.8.  Where lora_a is too large for those, against k_lin_shrink and the
-// tiles: 4096 x 6144, 8 tokens 25.7 and 27.5, 16 tokens 29.6 and 28.9, 64 tokens
-// 39.3 and 31.5; 8192 x 8192, 2 tokens 40.7 and 40.4, 16 tokens 51.1 and 46.3;
-// 1024 x 65536, one token 55.0 and 33.4.
+// the wide tiles, us: 2048 x 1024, 4 tokens 11.3 and 9.2; with as many further
+// columns as the layer's (4096 x 6144, rank 16, 128 slots) one token 20.9 and 23.2,
+// 4 tokens 23.4 and 23.2.  Where lora_a is too large for those, against k_lin_shrink
+// and the tiles: 4096 x 6144, 8 tokens 25.7 and 27.5, 16 tokens 29.6 and 28.9, 64
+// tokens 39.3 and 31.5; 8192 x 8192, 2 tokens 40.7 and 40.4, 16 tokens 51.1 and
+// 46.3; 1024 x 65536, one token 55.0 and 33.4.
 bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     if (lin_one(T, K, N, S, R)) return true;
-    if (T > kLinFewTokens) return false;
     const int64_t n = columns(N, S), wide = wide_cols(n, S, R, L);
-    if (wide) return (T <= 16 && n * K <= 3 << 20) || (T <= 4 && 2 * wide > n && n <= 32768);
-    return n <= 32768 && T * n * K <= (T <= 16 ? 1 << 29 : 1 << 27);
+    if (T > kLinFewTokens || n > 32768) return false;
+    if (wide) return T <= 2 && 2 * wide > n;
+    return T * n * K <= (T <= 16 ? 1 << 29 : 1 << 27);
 }
 
 // Direct batches whose rank vectors come out of the tiles as further columns: a
@@ -1575,10 +1564,7 @@ hipError_t launch_lin_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, c
     int y = L < 16 ? L : 16;
     if (y > T) y = T;
     const dim3 grid((unsigned)((T + 15) / 16), (unsigned)y, (unsigned)(S * ((R + 15) / 16)));
-    // one token block leaves most of the card idle: all of K in flight; many
-    // blocks share a CU better with half the registers
-    if (T <= 16 && K > 2048) hipLaunchKernelGGL(k_lin_shrink<8>, grid, dim3(kShWaves * 64), 0, st, a);
-    else hipLaunchKernelGGL(k_lin_shrink<4>, grid, dim3(kShWaves * 64), 0, st, a);
+    hipLaunchKernelGGL(k_lin_shrink, grid, dim3(kShWaves * 64), 0, st, a);
     return hipGetLastError();
 }
 

@@ -23,6 +23,9 @@ SHAPES = [
     (1, 72, (36, 20), 32, 3, 4),
     (1, 64, (16400,), 16, 2, 0),           # one token, many columns
     (1, 640, (100,), 40, 2, 0),            # up to 64 tokens
+    (1, 4104, (68, 4), 16, 2, 4),
+    (2, 136, (40,), 8, 4, 0),              # as many further columns as the layer's
+    (5, 2120, (100, 36), 16, 3, 4),        # K splits that do not divide the K tiles
     (2, 24, (32800, 4), 8, 3, 0),          # few tokens, too many columns for one launch: tiles
     (3, 72, (36,), 24, 3, 0),
     (16, 64, (64, 64), 16, 4, 8),
