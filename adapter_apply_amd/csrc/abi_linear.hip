@@ -16,7 +16,9 @@ inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
 // Workspace of lora_linear and lora_linear_backward.  Every region grows with
 // each size argument.  The last line and the region below it belong to the
-// one-launch segment build, which needs them zero and leaves them zero.
+// one-launch segment build, which needs them zero and leaves them zero; the
+// region's place follows from the buffer's size, T and L, so in a workspace of
+// the largest sizes no layer's own regions reach another layer's.
 struct LinWs {
     SegLayout seg;
     size_t order;       // int32 [2][T]: row order of the tile GEMM and the rows' slots
@@ -24,9 +26,9 @@ struct LinWs {
     size_t hl_v;        // the same of v
     size_t v;           // fp32 [S][T][R]: v by token (wide gradients)
     size_t part;        // fp32 partial sums
-    size_t pad;         // dy with slices of whole 8-element units, when some N_s % 8
+    size_t pad;         // bf16 [T][pad_cols]: dy with slices of whole 8-element units
     size_t end;
-    bool padded;
+    bool padded;        // some N_s % 8: dy goes through pad
     int64_t pad_cols;
 };
 
@@ -74,7 +76,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         w.padded = w.padded || N[s] % 8;
         w.pad_cols += round8(N[s]);
     }
-    if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
+    o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);   // (used or not)
     w.end = o + seg_x_bytes(T, L) + 256;
     return w;
 }

@@ -1,0 +1,66 @@
+"""Sizes and rules of the layer entry points that their calls rest on, without a
+GPU: the workspace of layers that share one."""
+import random
+
+import pytest
+
+import adapter_apply_amd as aa
+
+
+def seg_exchange_bytes(T, L):
+    """The region of the one-launch segment build, zero between calls: int32
+    counts of each of its work-groups (1024 tokens, at most 16) over L + 1 keys,
+    and a 256-byte line; it ends where the workspace's last line begins."""
+    groups = min(max((T + 1023) // 1024, 1), 16)
+    return (4 * groups * (L + 1) + 255) // 256 * 256 + 256
+
+
+def size(T, K, N, R, L):
+    return aa.lora_linear_workspace_size(T, K, N, R, L)
+
+
+def data_end(T, K, N, R, L):
+    """Where a call's own regions end: the exchange region and the last line are
+    the end of its size."""
+    return size(T, K, N, R, L) - 256 - seg_exchange_bytes(T, L)
+
+
+def largest(a, b):
+    """Sizes of a workspace that both layers share: the largest of each argument."""
+    n = [0] * max(len(a[2]), len(b[2]))
+    for v in (a[2], b[2]):
+        for i, w in enumerate(v):
+            n[i] = max(n[i], w)
+    return max(a[0], b[0]), max(a[1], b[1]), tuple(n), max(a[3], b[3]), max(a[4], b[4])
+
+
+def shares(a, b):
+    both = size(*largest(a, b))
+    for p, q in ((a, b), (b, a)):
+        assert size(*p) <= both, (p, q)
+        # p leaves q's exchange region alone in a workspace of any size that is enough
+        assert data_end(*p) <= both - 256 - seg_exchange_bytes(q[0], q[4]), (p, q)
+
+
+@pytest.mark.parametrize("a,b", [
+    ((8192, 1024, (4096,), 16, 64), (4096, 1024, (4092,), 16, 64)),
+    ((7168, 64, (1024,), 8, 64), (4096, 64, (1020,), 8, 64)),
+    ((8192, 4096, (4096,), 16, 64), (7000, 4096, (4092,), 16, 64)),
+    ((6000, 64, (1024,), 8, 8), (6000, 64, (1020,), 8, 900)),
+    ((300, 64, (64, 36), 8, 8), (300, 64, (68,), 8, 8)),
+], ids=str)
+def test_layers_share_a_workspace_of_the_largest_sizes(a, b):
+    """A layer whose dy is copied (widths off 8) next to one whose is not."""
+    shares(a, b)
+
+
+def test_any_two_layers_share_a_workspace_of_the_largest_sizes():
+    rng = random.Random(7)
+
+    def layer():
+        pick = lambda hi: max(1, int(2 ** rng.uniform(0, hi)))
+        return (pick(15), 8 * pick(10), tuple(4 * pick(11) for _ in range(rng.randint(1, 8))),
+                8 * rng.randint(1, 64), pick(10))
+
+    for _ in range(4000):
+        shares(layer(), layer())
