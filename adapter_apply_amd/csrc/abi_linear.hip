@@ -2,8 +2,7 @@
 // gradient, and of the per-adapter gradient norm and clip: argument checks (all
 // before any launch), workspace carving and launches.  Declarations and
 // contracts: include/adapter_apply.h.
-#include <memory>
-#include <new>
+#include <string.h>
 
 #include "checks.hpp"
 #include "linear.hpp"
@@ -344,29 +343,35 @@ static lora_status_t check_grads(const void *const *g, const int64_t *m, int32_t
 }
 
 // Every output at an address of its own, and at a gradient's only if it is that
-// tensor's: else work-groups of two tensors would scale the same elements.
+// tensor's: else work-groups of two tensors would scale the same elements.  The
+// outputs go through a hash table on the stack, kOutBlock at a time, each block
+// against every later output and every gradient (no memory is allocated).
+constexpr int32_t kOutBlock = 2048;
 static lora_status_t check_outputs(const void *const *out, const void *const *g, const int64_t *m, int32_t n) {
-    size_t size = 16;
-    while (size < 2 * (size_t)n) size *= 2;
-    struct Entry { const void *p; int32_t i; };
-    const std::unique_ptr<Entry[]> table(new (std::nothrow) Entry[size]());
-    if (!table) return LORA_E_RUNTIME;
-    // the entry of address p, or the empty one where it belongs
-    auto find = [&](const void *p) -> Entry & {
-        size_t h = (size_t)((reinterpret_cast<uintptr_t>(p) >> 1) * 0x9E3779B97F4A7C15ull >> 20) & (size - 1);
-        while (table[h].p && table[h].p != p) h = (h + 1) & (size - 1);
-        return table[h];
-    };
-    for (int32_t i = 0; i < n; ++i) {
-        if (m[i] == 0) continue;
-        Entry &e = find(out[i]);
-        if (e.p) return LORA_E_SHAPE;
-        e = Entry{out[i], i};
-    }
-    for (int32_t i = 0; i < n; ++i) {
-        if (m[i] == 0) continue;
-        const Entry &e = find(g[i]);
-        if (e.p && e.i != i) return LORA_E_SHAPE;
+    int32_t table[2 * kOutBlock];                 // 1 + the index of an output, or 0
+    for (int32_t b = 0; b < n;) {
+        const int32_t e = n - b < kOutBlock ? n : b + kOutBlock;
+        size_t size = 16;
+        while (size < 2 * (size_t)(e - b)) size *= 2;
+        memset(table, 0, size * sizeof(table[0]));
+        // the entry of address p, or the empty one where it belongs
+        auto find = [&](const void *p) -> int32_t & {
+            size_t h = (size_t)((reinterpret_cast<uintptr_t>(p) >> 1) * 0x9E3779B97F4A7C15ull >> 20) & (size - 1);
+            while (table[h] && out[table[h] - 1] != p) h = (h + 1) & (size - 1);
+            return table[h];
+        };
+        for (int32_t i = b; i < n; ++i) {
+            if (m[i] == 0) continue;
+            int32_t &at = find(out[i]);
+            if (at) return LORA_E_SHAPE;
+            if (i < e) at = i + 1;
+        }
+        for (int32_t i = 0; i < n; ++i) {
+            if (m[i] == 0) continue;
+            const int32_t at = find(g[i]);
+            if (at && at != i + 1) return LORA_E_SHAPE;
+        }
+        b = e;
     }
     return LORA_OK;
 }

@@ -306,3 +306,48 @@ def test_clip_binding_refuses_other_outputs():
     for out in ([g[0]], [g[1], g[0]], [t.to(BF) for t in g]):
         with pytest.raises(ValueError):
             aa.lora_grad_clip(out, g, torch.zeros(L), torch.zeros(L))
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("n", [2, 2047, 2048, 2049, 5000, 9001])
+def test_equal_outputs_are_found_in_long_lists(n):
+    """One pair of equal addresses among n tensors, at both ends and in the
+    middle: two outputs, or an output and another tensor's gradient."""
+    at = [FAKE + 4096 * i for i in range(1, 2 * n + 1)]
+    m, lib = i64(*[8] * n), aa.lib()
+    for i, j in {(0, n - 1), (n // 2, n - 1), (n - 2, n - 1), (0, n // 2 or 1)}:
+        if i == j:
+            continue
+        out = (C.c_void_p * n)(*at[:n])
+        grad = (C.c_void_p * n)(*at[n:])
+        for arr, v in ((out, out[i]), (grad, out[i])):
+            keep, arr[j] = arr[j], v
+            assert lib.lora_grad_clip(out, grad, m, n, 3, FAKE, FAKE, aa.LORA_DT_F32,
+                                      None) == aa.LORA_E_SHAPE, (n, i, j)
+            arr[j] = keep
+
+
+@needs_no_gpu
+def test_clip_allocates_nothing():
+    """The check of the outputs needs no host memory: with the address space
+    held at its size it still finds the pair."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import ctypes as C, resource
+import adapter_apply_amd as aa
+n = 100000
+out = (C.c_void_p * n)(*[{FAKE} + 4096 * i for i in range(n)])
+out[n - 1] = out[1]
+m = (C.c_int64 * n)(*[8] * n)
+clip = aa.lib().lora_grad_clip
+args = (out, out, m, n, 3, {FAKE}, {FAKE}, aa.LORA_DT_F32, None)
+pages = int(open("/proc/self/statm").read().split()[0])
+resource.setrlimit(resource.RLIMIT_AS, (pages * resource.getpagesize() + 65536,) * 2)
+code = clip(*args)
+raise SystemExit(0 if code == aa.LORA_E_SHAPE else 100 + code)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
