@@ -431,7 +431,8 @@ def _aligned_ws(n: int, device):
     ws = torch.empty(max(n, 256) + 256, dtype=torch.uint8, device=device)
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + max(n, 256)]
-    lora_workspace_init(ws)
+    with torch.cuda.device(ws.device):          # its launches go to the current device
+        lora_workspace_init(ws)
     return ws
 
 

@@ -351,3 +351,30 @@ raise SystemExit(0 if code == aa.LORA_E_SHAPE else 100 + code)
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+@pytest.mark.parametrize("alloc", [
+    lambda d: aa.alloc_workspace(8, 64, 1, 16, 2, device=d),
+    lambda d: aa.alloc_moe_workspace(8, 2, 1, 16, 2, 4, device=d),
+    lambda d: aa.alloc_linear_workspace(8, 64, [32], 16, 2, device=d),
+    lambda d: aa.alloc_grad_workspace([torch.zeros(2, 8)], device=d)], ids=range(4))
+def test_workspace_is_cleared_on_its_own_device(alloc, monkeypatch):
+    """The fill runs with the workspace's device current, whatever the caller's
+    current device is, and the caller's comes back."""
+    current, cleared = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(aa, "lora_workspace_init", lambda ws, stream=None: cleared.append((current[-1], ws.device)))
+    ws = alloc("cpu")                           # (stands for a GPU that is not the current one)
+    assert cleared == [(ws.device, ws.device)] and current == [0]
+    assert ws.data_ptr() % 256 == 0
