@@ -1331,7 +1331,6 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
         a.n_tiles += a.S * ((a.L * a.R + BN - 1) / BN);
     }
     if (ksp == 1 && !a.join_delta) a.part = nullptr;
-    if (a.part && (int64_t)ksp * a.T * a.part_ld > kLinJoinMax) return hipErrorInvalidValue;   // (no rule asks for it)
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
     if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
@@ -1381,39 +1380,35 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
            tiles(T, K, N, S, true, 256) <= (1 << 22);
 }
 
-hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (!gradient && lin_one(a.T, a.K, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
-    if (!gradient && lin_few(a.T, a.K, a.n, a.S, a.R, a.L)) {
-        if (a.T <= 16) return run_few<1, 1, 4>(a, st);
-        if (a.T <= 32) return run_few<2, 2, 4>(a, st);
-        return run_few<4, 2, 2>(a, st);
-    }
+// The tiles of a batch and their K splits.  join, wide: LinArgs' join_delta and
+// wide; base: there is a base product.
+LinTilePlan lin_tile_plan(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool gradient,
+                          bool join, bool wide, bool base) {
     // 256 x 256 from 192 tiles on, most of a tile per CU (4096 tokens, 4096 x 4096, 256
     // tiles: 143 us, 163 with 128 x 128; 2048 tokens, 4096 x 6144, 192 tiles: 132 and
     // 128; 128 tiles: 132 and 97).
-    if (!a.join_delta && a.order && tiles(a.T, a.K, a.n, a.S, gradient, 256) >= 192)
-        return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
-    int64_t nk = (a.K + 63) / 64;
+    if (!join && tiles(T, K, N, S, gradient, 256) >= 192) return {256, 1};
+    int64_t nk = (K + 63) / 64;
     if (gradient) {
         nk = 0;
-        for (int s = 0; s < a.S; ++s) nk += (a.n[s] + 63) / 64;
+        for (int s = 0; s < S; ++s) nk += (N[s] + 63) / 64;
     }
-    if (!a.w) nk = 0;
+    if (!base) nk = 0;
     // K splits, about kLinSplitTiles work-groups of at least 8 K tiles each; 4 of a
     // few tokens that are joined anyway, whose sums are small (4 tokens of 1352 x
     // 1652 9.7 us, 11.5 with 8; 64 tokens 11.3 and 12.3, of 2048 x 2048 12.1 and
     // 11.7; 128 tokens 14.2 and 13.4)
-    const int least = a.join_delta && a.T <= 64 ? 4 : 8;
+    const int least = join && T <= 64 ? 4 : 8;
     auto splits = [&](int64_t t) {
         int64_t k = kLinSplitTiles / t;
         if (k > nk / least) k = nk / least;
         if (k > kLinMaxSplits) k = kLinMaxSplits;
-        return (int)(k < 1 ? 1 : k);
+        return (int32_t)(k < 1 ? 1 : k);
     };
-    int64_t t128 = tiles(a.T, a.K, a.n, a.S, gradient, 128), t64 = tiles(a.T, a.K, a.n, a.S, gradient, 64);
-    if (a.wide) {
-        t128 += (int64_t)a.S * ((a.L * a.R + 127) / 128) * ((a.T + 127) / 128);
-        t64 += (int64_t)a.S * ((a.L * a.R + 63) / 64) * ((a.T + 63) / 64);
+    int64_t t128 = tiles(T, K, N, S, gradient, 128), t64 = tiles(T, K, N, S, gradient, 64);
+    if (wide) {
+        t128 += (int64_t)S * ((L * R + 127) / 128) * ((T + 127) / 128);
+        t64 += (int64_t)S * ((L * R + 63) / 64) * ((T + 63) / 64);
     }
     // From 192 tiles of 128 x 128 on a join costs more than even work-groups give
     // (2048 tokens, 4096 x 4096: 97 us; 132 with 256 x 256, 147 with 64 x 64), but
@@ -1424,9 +1419,9 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     // two splits 54.9; 1024 tokens, 14336 x 4096, 264 tiles: 198, 172 and 156; 452
     // tiles: 117 and 126 with two).
     if (t128 >= 192) {
-        int k = t128 <= 256 && nk >= 192 ? 2 : 1;
-        if (a.join_delta && t128 <= 340 && nk >= 24) k = t128 > 256 ? 3 : 2;
-        return run_tile<128, 128, 2, 2, 2, true>(a, gradient, k, st);
+        int32_t k = t128 <= 256 && nk >= 192 ? 2 : 1;
+        if (join && t128 <= kLinEvenTiles && nk >= 24) k = t128 > 256 ? 3 : 2;
+        return {128, k};
     }
     // Fewer tiles: K splits, joined by a second launch.  Tiles of 64 x 64 read each
     // operand twice as often, which shows once all their K tiles together pass some
@@ -1435,10 +1430,32 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
     // 4096 x 6144 26.3 and 31.0), or once they no longer run at the same time (the
     // gradient of 1501 tokens, 1652 x 1352, 528 of them: 61.4 and 53.1).
     if (t128 * splits(t128) >= kLinSplitTiles / 2 && (t64 > kLinSplitTiles || t64 * nk > 16384))
-        return run_tile<128, 128, 2, 2, 2, true>(a, gradient, splits(t128), st);
+        return {128, splits(t128)};
     // (two stages: a work-group has few K tiles, and more stages fill for longer;
     // 16 tokens of 14336 x 4096: 26.3 us, with four 28.2)
-    return run_tile<64, 64, 2, 2, 2, true>(a, gradient, splits(t64), st);
+    return {64, splits(t64)};
+}
+
+// The fp32 sums of any batch stay within kLinJoinMax elements, which the
+// workspace holds: splits times the tiles' elements; unsplit, lin_join_delta
+// tests them itself, and a direct batch or a wide gradient, whose further columns
+// are no more than the layer's own, is bounded by its bytes at rank 8 and up.
+static_assert(kLinSplitTiles * 128 * 128 <= kLinJoinMax, "sums of split tiles");
+static_assert(2 * 256 * 128 * 128 <= kLinJoinMax && 3 * kLinEvenTiles * 128 * 128 <= kLinJoinMax, "sums of even tiles");
+static_assert(2 * (kLinWideBytesB / 32) <= kLinJoinMax && 2 * (kLinWideBytesA / 32) <= kLinJoinMax &&
+              kLinDirectBytesB / 32 <= kLinJoinMax, "unsplit sums");
+
+hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
+    if (!gradient && lin_one(a.T, a.K, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
+    if (!gradient && lin_few(a.T, a.K, a.n, a.S, a.R, a.L)) {
+        if (a.T <= 16) return run_few<1, 1, 4>(a, st);
+        if (a.T <= 32) return run_few<2, 2, 4>(a, st);
+        return run_few<4, 2, 2>(a, st);
+    }
+    const LinTilePlan p = lin_tile_plan(a.T, a.K, a.n, a.S, a.R, a.L, gradient, a.join_delta, a.wide, a.w != nullptr);
+    if (p.tile == 256) return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
+    if (p.tile == 128) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, p.splits, st);
+    return run_tile<64, 64, 2, 2, 2, true>(a, gradient, p.splits, st);
 }
 
 // Whether a sorted forward batch leaves the delta to the join: when the

@@ -51,6 +51,13 @@ bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R);
 bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L);
 constexpr int kLinSplitTiles = 512;     // work-groups aimed at by K splits
+constexpr int kLinEvenTiles = 340;      // most tiles of a joined batch that splits even out
+struct LinTilePlan {
+    int32_t tile;                       // 64, 128 or 256 rows and columns
+    int32_t splits;
+};
+LinTilePlan lin_tile_plan(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool gradient,
+                          bool join, bool wide, bool base);
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
 constexpr int kLinPartsFwd = 2;
@@ -64,8 +71,7 @@ constexpr int64_t kLinDirectBytesA = 128 << 20;
 constexpr int64_t kLinDirectBytesB = 110 << 20;
 constexpr int64_t kLinWideBytesB = 176 << 20;
 constexpr int64_t kLinWideBytesA = 224 << 20;
-// fp32 sums of a call: splits times T columns.  At most 1020 tiles of 128 x 128
-// (launch_lin_gemm), unsplit batches bounded by lin_join_delta and lin_direct.
+// fp32 sums of a call at most: splits times T columns (see lin_tile_plan).
 constexpr int64_t kLinJoinMax = 1 << 25;
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);

@@ -1,10 +1,11 @@
 """Sizes and rules of the layer entry points that their calls rest on, without a
-GPU: the workspace of layers that share one."""
+GPU: the workspace of layers that share one, the forms and their sums."""
 import random
 
 import pytest
 
 import adapter_apply_amd as aa
+from tests import layer_rules
 
 
 def seg_exchange_bytes(T, L):
@@ -64,3 +65,24 @@ def test_any_two_layers_share_a_workspace_of_the_largest_sizes():
 
     for _ in range(4000):
         shares(layer(), layer())
+
+
+def drawn(n, seed):
+    rng = random.Random(seed)
+    pick = lambda lo, hi: int(2 ** rng.uniform(lo, hi))
+    for _ in range(n):
+        yield (max(1, pick(0, 13.5)), 8 * pick(0, 10.8),
+               tuple(4 * pick(0, 12.8) for _ in range(rng.choice((1, 1, 2, 3, 8)))),
+               8 * rng.choice((1, 2, 2, 3, 4, 5, 8, 16, 64)), pick(0, 10))
+
+
+def test_sums_stay_within_the_workspace():
+    """The fp32 sums that any call leaves for a join: within what a workspace
+    holds, also at the most rows and columns that a rule takes."""
+    edges = [(T, K, N, R, L) for T in (1, 64, 1024, 1025, 8192) for K in (8, 1536, 4096, 16384)
+             for N in ((4,), (4096,), (14336, 14336), (32768,), (4096,) * 8) for R in (8, 128, 512) for L in (1, 64, 1024)]
+    for c in [*edges, *drawn(20000, 11)]:
+        T, K, N, R, L = c
+        for _, sums in (layer_rules.forward(*c), *(layer_rules.gradient(*c, weights=w, base=b)
+                                                   for w in (True, False) for b in (True, False))):
+            assert sums <= min(layer_rules.WS_SUMS, 8 * T * 2 * max(K, sum(N))), c
