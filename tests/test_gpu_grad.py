@@ -7,6 +7,7 @@ import adapter_apply_amd as aa
 pytestmark = pytest.mark.gpu
 
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+FILL = 7.0
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
 
@@ -140,3 +141,45 @@ def test_graph_and_stream():
             step()
         st.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, [norm, *out])), rep
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,shapes", [
+    (3, [(8192 * 700 + 5,)]),                       # 2103 chunks of one tensor
+    (4, [(64, 128), (8200,)] * 200 + [(3,), (0,)]),   # a model: launches of 96 tensors, 2404 chunks
+    (1024, [(3,), (8193,)]),                        # 3 chunks of each of 1024 slots
+    (1, [(7,)] * 2100),
+], ids=lambda v: str(v)[:30])
+def test_more_chunks_than_are_counted(L, shapes, dtype):
+    """Past 2048 chunks a launch of its own adds the partial sums; out of place,
+    then in place."""
+    grads = make(shapes, L, DT[dtype], seed=len(shapes))
+    assert L * sum(-(-t[0].numel() // 8192) for t in grads) > 2048
+    check(grads, L)
+    check(grads, L, out=grads)
+
+
+def test_norm_of_a_model_repeats_and_leaves_other_slots():
+    """The same bits from call to call and from a graph; a NaN in one slot and
+    the next call's small set (counted again on the same workspace) leave the
+    others alone."""
+    L = 4
+    grads = make([(64, 128), (8200,)] * 200, L, torch.float32, seed=3)
+    ws = aa.alloc_grad_workspace(grads)
+    norm = torch.empty((L,), device="cuda")
+    aa.lora_grad_norm(norm, grads, ws)
+    want = norm.clone()
+    small, ref = torch.empty((L,), device="cuda"), definition(grads[:3], L)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        aa.lora_grad_norm(norm, grads, ws)
+    for _ in range(3):
+        norm.fill_(FILL)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(norm, want)
+        aa.lora_grad_norm(small, grads[:3], ws)
+        assert bool(((small.double() - ref).abs() <= ref * 2.0 ** -24 * 1.001).all())
+    grads[217][2, 5] = float("nan")
+    aa.lora_grad_norm(norm, grads, ws)
+    assert bool(norm[2].isnan()) and all(bool(norm[i] == want[i]) for i in (0, 1, 3))
