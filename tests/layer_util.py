@@ -21,10 +21,11 @@ def normal(g, shape, std, dtype=torch.bfloat16):
 
 class Layer:
     """A seeded layer: tensors on the CPU, moved to `device`; x, y and dy as
-    windows of wider rows (`extra` columns)."""
+    windows of wider rows (`extra` columns).  stale: A and B hold other values
+    past each slot's rank (a slot used before for a larger adapter), not zeros."""
 
     def __init__(self, T, K, N, R, L, seed=0, extra=0, ragged=True, bias=False, runs=False,
-                 device="cuda"):
+                 device="cuda", stale=False):
         g = torch.Generator().manual_seed(1000 + seed)
         self.T, self.K, self.N, self.R, self.L, self.S = T, K, list(N), R, L, len(N)
         n = sum(N)
@@ -46,7 +47,7 @@ class Layer:
         rank = torch.randint(0, R + 1, (L,), generator=g) if ragged else torch.full((L,), R)
         if L > 1:
             rank[0], rank[1] = R, 0
-        for s in range(self.S):
+        for s in range(0 if stale else self.S):
             keep = (torch.arange(R) < rank[:, None]).to(device)
             self.A[s] *= keep[:, :, None]
             self.B[s] *= keep[:, None, :]

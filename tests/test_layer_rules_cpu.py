@@ -86,3 +86,25 @@ def test_sums_stay_within_the_workspace():
         for _, sums in (layer_rules.forward(*c), *(layer_rules.gradient(*c, weights=w, base=b)
                                                    for w in (True, False) for b in (True, False))):
             assert sums <= min(layer_rules.WS_SUMS, 8 * T * 2 * max(K, sum(N))), c
+
+
+def test_every_form_is_tested():
+    """Each form that the rules choose for a drawn shape is one that the GPU tests
+    reach (tests/test_gpu_layer.py, tests/test_gpu_layer_forms.py)."""
+    from tests.test_gpu_layer import SHAPES
+    from tests.test_gpu_layer_forms import FORMS
+    tested = set()
+    for s in FORMS + SHAPES:
+        T, K, N, R, L = s[:5]
+        tested |= {("y", *layer_rules.forward(T, K, N, R, L)[0]), ("dx", *layer_rules.gradient(T, K, N, R, L)[0])}
+        if T < 1100:
+            tested.add(("dx", *layer_rules.gradient(T, K, N, R, L, weights=False)[0]))
+        if s in SHAPES and T in (17, 200, 1000, 2100):
+            tested.add(("dx", *layer_rules.gradient(T, K, N, R, L, base=False)[0]))
+    missing = {}
+    for c in drawn(40000, 12):
+        for f in (("y", *layer_rules.forward(*c)[0]), ("dx", *layer_rules.gradient(*c)[0]),
+                  ("dx", *layer_rules.gradient(*c, weights=False)[0]), ("dx", *layer_rules.gradient(*c, base=False)[0])):
+            if f not in tested:
+                missing[f] = c
+    assert not missing, missing
