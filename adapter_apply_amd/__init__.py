@@ -606,17 +606,20 @@ def _need_stack(ts, name, shapes, dtype):
 
 
 def _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, S_cols):
-    """Checks shared by the layer and its gradient; S_cols: the [T, sum N]
-    tensor (y or dy) and its name.  Returns T, K, L, R and the widths."""
+    """Checks shared by the layer and its gradient (x None: only there); S_cols:
+    the [T, sum N] tensor (y or dy) and its name.  Returns T, K, L, R and the
+    widths."""
     torch = _torch()
     bf16 = torch.bfloat16
-    _rowmajor(x, "x")
-    _need_dtype(x, (bf16,), "x")
-    T, K = x.shape
+    if x is not None:
+        _rowmajor(x, "x")
+        _need_dtype(x, (bf16,), "x")
     if len(A) < 1 or A[0].dim() != 3 or len(A) != len(B) or any(b.dim() != 3 for b in B):
         raise ValueError("A and B must hold one [L, R, K] and one [L, N_s, R] tensor per slice "
                          f"(got {len(A)} and {len(B)} tensors)")
-    L, R, _ = A[0].shape
+    L, R, K = A[0].shape
+    T = S_cols[0].shape[0] if x is None else x.shape[0]
+    K = K if x is None else x.shape[1]
     N = [b.shape[1] for b in B]
     _need_stack(A, "A", [(L, R, K)] * len(A), bf16)
     _need_stack(B, "B", [(L, n, R) for n in N], bf16)
@@ -643,6 +646,8 @@ def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bi
     """y[:, :sum N] = x W^T + bias + scale (x A^T) B^T per slice, rounded once.
     x [T, K]; W [sum N, K]; A[s] [L, R, K]; B[s] [L, N_s, R]; bias [sum N] or
     None; all bf16.  buf [S, T, R] fp32 (optional) receives x A^T."""
+    if x is None or W is None:
+        raise ValueError("x and W are needed")
     T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
     if bias is not None:
         _need_vec(bias, sum(N), _torch().bfloat16, "bias")
@@ -658,10 +663,13 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
                          stream=None):
     """Gradient of lora_linear (W frozen).  dx [T, K] bf16 or None; dA[s]
     [L, R, K] and dB[s] [L, N_s, R] fp32, or None; dy [T, >= sum N].  W None:
-    dx += the adapters' part.  buf: x A^T as lora_linear left it, or None."""
+    dx += the adapters' part.  buf: x A^T as lora_linear left it, or None.  x
+    [T, K] may be None where it is not read: no dA, and no dB or a buf."""
     torch = _torch()
     T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
     S = len(N)
+    if x is None and (dA is not None or (dB is not None and buf is None)):
+        raise ValueError("x is needed for dA, and for dB without buf")
     if dx is not None:
         _rowmajor(dx, "dx")
         _need_dtype(dx, (torch.bfloat16,), "dx")
@@ -676,7 +684,7 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
     dev = _one_device((dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws))
     _call("lora_linear_backward", dev, stream, _ptr(dx), 0 if dx is None else dx.stride(0),
           None if dA is None else _ptr_array(dA), None if dB is None else _ptr_array(dB), _ptr(dy),
-          dy.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
+          dy.stride(0), _ptr(x), 0 if x is None else x.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
           _ptr_array(A), _ptr_array(B), (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank),
           _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
 

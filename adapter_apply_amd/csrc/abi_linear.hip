@@ -196,7 +196,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
                                    const int32_t *idx, const int32_t *slot_rank, const float *scale,
                                    const float *buf, int32_t dtype, uint32_t flags, void *ws,
                                    size_t ws_bytes, void *stream) {
-    CHECK(check_layer(T, K, ldx, N, S, L, R, lddy, dtype));
+    CHECK(check_layer(T, K, x ? ldx : K, N, S, L, R, lddy, dtype));
     if (dx) CHECK(check_k(K, lddx));
     if (dx && W) CHECK(check_k(K, ldw));
     if (!dx && !dA && !dB) return LORA_E_NULL;
@@ -215,7 +215,8 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         }
         return LORA_OK;
     }
-    if (!dy || !x || !idx || !scale) return LORA_E_NULL;
+    if (!dy || !idx || !scale) return LORA_E_NULL;
+    if (!x && (dA || (dB && !buf))) return LORA_E_NULL;
     CHECK(check_ptrs(A, S));
     CHECK(check_ptrs(B, S));
     if (!al(dx, 16) || !al(dy, 16) || !al(x, 16) || !al(W, 16) || !al(buf, 16)) return LORA_E_ALIGN;

@@ -456,6 +456,8 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
  *   dA[s][i][j][k] = sum_{t: idx[t] = i} v_s[t][j] * x[t][k]
  *   dB[s][i][n][j] = scale[i] * sum_{t: idx[t] = i} dy[t][off_s + n] * u_s[t][j]
  * dy: device bf16 [T][lddy].  dx: device bf16 [T][lddx] or NULL (not wanted).
+ * x: read for dA, and for dB when buf is NULL; else it may be NULL (ldx is then
+ * not read).
  * W NULL: dx holds the base layer's own gradient and receives the adapters'
  * part in place (rows without an adapter untouched).
  * dA, dB: host arrays of S device pointers, fp32 [L][R][K] and [L][N[s]][R],

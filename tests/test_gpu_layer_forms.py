@@ -150,3 +150,21 @@ def test_accumulate_over_token_splits(T, K, N, R, L):
             # part in the old value, and in the sum as the bound e already counts
             # more additions than that
             within(p, r + o.double(), e + 17 * U32 * o.double().abs(), "sum")
+
+
+@pytest.mark.parametrize("T,K,N", [(20, 136, (100, 36)), (96, 520, (264, 136)), (1200, 392, (100, 36))], ids=str)
+def test_backward_without_x(T, K, N):
+    """dx, and dB with a saved u, do not read x: the bits of the calls that get it."""
+    c = Layer(T, K, N, 24, 5, seed=33, stale=True)
+    ws = aa.alloc_linear_workspace(T, K, N, 24, 5)
+    buf = run_forward(c)[2]
+    for W in (c.W, None):
+        for weights in (False, True):
+            got = []
+            for x in (c.x, None):
+                dx = torch.full((T, K), 1.0, dtype=torch.bfloat16, device="cuda")
+                dB = [torch.full((5, n, 24), FILL, device="cuda") for n in N] if weights else None
+                aa.lora_linear_backward(dx, None, dB, c.dy, x, W, c.A, c.B, c.idx, c.rank, c.scale, ws,
+                                        buf=buf if weights else None)
+                got.append([dx, *(dB or [])])
+            assert all(torch.equal(p, q) for p, q in zip(*got))

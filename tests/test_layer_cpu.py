@@ -378,3 +378,31 @@ def test_workspace_is_cleared_on_its_own_device(alloc, monkeypatch):
     ws = alloc("cpu")                           # (stands for a GPU that is not the current one)
     assert cleared == [(ws.device, ws.device)] and current == [0]
     assert ws.data_ptr() % 256 == 0
+
+
+@needs_no_gpu
+def test_backward_needs_x_only_where_it_is_read():
+    """dA, and dB without a saved u: else a call without x gets as far as its
+    first launch (which fails without a GPU)."""
+    for kw in (dict(), dict(dB=None), dict(dA=None), dict(dx=None, dB=None), dict(dA=None, dx=None),
+               dict(dB=None, buf=FAKE)):
+        assert backward(x=None, ldx=0, **kw) == aa.LORA_E_NULL
+    for kw in (dict(dA=None, dB=None), dict(dA=None, buf=FAKE), dict(dA=None, dx=None, buf=FAKE),
+               dict(dA=None, dB=None, W=None)):
+        assert backward(x=None, ldx=0, **dict(dict(dx=FAKE + 0x4000000), **kw)) == aa.LORA_E_LAUNCH
+    assert backward(x=None, ldx=0, K=4092, dA=None, dB=None) == aa.LORA_E_ALIGN
+
+
+def test_backward_binding_needs_x_only_where_it_is_read():
+    for over in (dict(), dict(dB=None), dict(dA=None)):
+        with pytest.raises(ValueError, match="x is needed"):
+            call_backward(tensors(x=None, **over))
+    for over in (dict(dA=None, dB=None), dict(dA=None, buf=torch.zeros(2, T, R))):
+        with pytest.raises(ValueError, match="GPU"):      # (the next check)
+            call_backward(tensors(x=None, **over))
+    for over in (dict(dx=torch.zeros(T + 1, K, dtype=BF)), dict(W=torch.zeros(sum(N), K + 8, dtype=BF))):
+        with pytest.raises(ValueError, match="shape"):
+            call_backward(tensors(x=None, dA=None, dB=None, **over))
+    for name in ("x", "W"):
+        with pytest.raises(ValueError, match="x and W are needed"):
+            call_forward(tensors(**{name: None}))
