@@ -1491,14 +1491,19 @@ static int64_t columns(const int64_t *N, int32_t S) {
 }
 
 // One token of rank at most 32 takes the one launch of k_lin_one while K is at
-// most two rounds of its loads and its work-groups, each reading the slot's
-// lora_a rows, are not too many.  Against the wide tiles (two launches), us: K x N
-// of 2048 x 2048 8.7 and 10.0, rank 32 10.5 and 10.8; 1024 x 16384 9.7 and 15.0;
-// 4096 x 4096 15.3 and 13.9, 4096 x 6144 16.7 and 16.7, rank 32 19.9 and 18.1, 4096
-// x 8192 17.7 and 18.6; 5120 x 5120 18.5 and 16.9; 8192 x 1024 25.3 and 12.2.
+// most two rounds of its loads and its work-groups (32 columns, each reading the
+// slot's lora_a rows) fit the CUs once, or K and the rank are small.  Against the
+// wide tiles (two launches), us, medians of graph replays that repeat within 2 %:
+// K x N of 2048 x 2048 8.6 and 9.5, 1024 x 16384 9.6 and 14.9, 2048 x 16384 18.1 and
+// 20.8 (rank 32 22.0 and 21.6, 1536 x 12288 19.1 and 15.4); 4096 x 4096 15.0 and
+// 13.8, x 5120 15.9 and 15.5, x 5632 15.9 and 16.1, x 6144 15.8 and 16.8, x 8192
+// 17.7 and 18.8, x 8448 28.6 and 19.3; 3200 x 8192 13.9 and 17.1, x 8448 22.8 and
+// 17.2.  Longer K: 5120 x 5120 18.5 and 16.9; 8192 x 1024 25.3 and 12.2.
 bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R) {
     const int64_t n = columns(N, S);
-    return T == 1 && R <= 32 && n <= 16384 && (K <= 2048 || (K <= 4096 && R <= 16 && n > 4096));
+    if (T != 1 || R > 32) return false;
+    if (n > 8192) return n <= 16384 && K <= 2048 && R <= 16;
+    return K <= 2048 || (K <= 4096 && R <= 16 && n > 5120);
 }
 
 // Whether k_lin_few (or k_lin_one) takes a forward batch.  Its work-groups read

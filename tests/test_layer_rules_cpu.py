@@ -108,3 +108,11 @@ def test_every_form_is_tested():
             if f not in tested:
                 missing[f] = c
     assert not missing, missing
+
+
+@pytest.mark.parametrize("K,N,R,one", [
+    (2048, (2048,), 16, True), (4096, (4096,), 16, False), (4096, (4096, 1024, 1024), 16, True),
+    (4096, (8192,), 16, True), (4096, (8448,), 16, False), (4096, (14336,), 16, False),
+    (2048, (16384,), 16, True), (2048, (12288,), 32, False), (3200, (8192,), 16, True), (3200, (8448,), 16, False)])
+def test_one_token_takes_the_form_that_measured_faster(K, N, R, one):
+    assert (layer_rules.forward(1, K, N, R, 8)[0][0] == "one") == one
