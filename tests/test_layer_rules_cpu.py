@@ -116,3 +116,11 @@ def test_every_form_is_tested():
     (2048, (16384,), 16, True), (2048, (12288,), 32, False), (3200, (8192,), 16, True), (3200, (8448,), 16, False)])
 def test_one_token_takes_the_form_that_measured_faster(K, N, R, one):
     assert (layer_rules.forward(1, K, N, R, 8)[0][0] == "one") == one
+
+
+@pytest.mark.parametrize("T,K,N,few", [
+    (4, 4096, (4096, 1024, 1024), True), (16, 4096, (4096, 1024, 1024), False), (16, 4096, (4096,), True),
+    (2, 8192, (8192,), True), (8, 8192, (8192,), False), (16, 2048, (16384,), True),
+    (48, 1032, (2056,), True), (64, 4096, (4096, 1024, 1024), False)])
+def test_few_tokens_take_the_form_that_measured_faster(T, K, N, few):
+    assert (layer_rules.forward(T, K, N, 16, 1024)[0][0] == "few") == few
