@@ -1536,14 +1536,16 @@ bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int3
 // The same for dx: v = dy B of every slot as further columns, added by the join,
 // which reads S R lora_a rows per token.  weights: dA or dB are wanted too, which
 // need the segments and the vectors in parts either way.  Against the sorted form
-// (us; MB of lora_a and sums): dx alone, rank 16, 8 slots, 6144 x 4096: 16 tokens 22.1
-// and 42.1, 256 (117 MB) 37.2 and 54.0, 512 (235 MB) 52.9 and 67.2, 1024 (470 MB)
-// 97.6 and 93.8; with weights 96 tokens 45.4 and 55.3, 256 55.9 and 62.0; rank 64,
-// 96 tokens (157 MB) 67.7 and 72.5, 256 (420 MB) 81.8 and 78.0; 4096 x 14336, 256
-// tokens (176 MB) 72.6 and 75.7; 8192 x 8192, 512 tokens (201 MB) 124 and 113; 2048
-// x 2048, 1024 tokens (100 MB) 49.6 and 46.1.  A contraction many times K keeps
-// the further columns' few tiles long: 28672 x 4096, 96 tokens, with weights 119
-// and 108.
+// (us; MB (2^20) of lora_a and sums): dx alone, rank 16, 8 slots, 6144 x 4096: 16
+// tokens 22.1 and 42.1, 512 (224 MB) 56.0 and 69.9, 640 (280 MB) 70.1 and 76.6, 896
+// (392 MB) 83.6 and 94.6, 1024 (448 MB) 106 and 100; 8192 x 8192, 512 tokens (192
+// MB) 110 and 104, 640 (240 MB) 122 and 140, 768 (288 MB) 141 and 140, 1024 (384 MB)
+// 214 and 154; 4096 x 4096, 768 tokens (144 MB) 52.1 and 62.6, 1024 (192 MB) 73.8 and
+// 65.6; 4096 x 14336, 512 tokens (336 MB) 95.7 and 91.0: no one number of bytes parts
+// them, and past 256 MB what is lost grows larger than what is won.  With weights 96
+// tokens 45.4 and 55.3, 256 55.9 and 62.0; rank 64, 96 tokens (150 MB) 67.7 and 72.5,
+// 256 (400 MB) 81.8 and 78.0.  A contraction many times K keeps the further columns'
+// few tiles long: 28672 x 4096, 96 tokens, with weights 119 and 108.
 bool lin_wide_gradient(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights) {
     if (T > (weights ? 512 : kLinDirectTokens) || wide_cols(K, S, R, L) == 0) return false;
     if (weights && columns(N, S) > 4 * (int64_t)K) return false;

@@ -70,7 +70,7 @@ constexpr int kLinDirectTokens = 1024;
 constexpr int64_t kLinDirectBytesA = 128 << 20;
 constexpr int64_t kLinDirectBytesB = 110 << 20;
 constexpr int64_t kLinWideBytesB = 176 << 20;
-constexpr int64_t kLinWideBytesA = 224 << 20;
+constexpr int64_t kLinWideBytesA = 256 << 20;
 // fp32 sums of a call at most: splits times T columns (see lin_tile_plan).
 constexpr int64_t kLinJoinMax = 1 << 25;
 bool lin_join_delta(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L);

@@ -124,3 +124,10 @@ def test_one_token_takes_the_form_that_measured_faster(K, N, R, one):
     (48, 1032, (2056,), True), (64, 4096, (4096, 1024, 1024), False)])
 def test_few_tokens_take_the_form_that_measured_faster(T, K, N, few):
     assert (layer_rules.forward(T, K, N, 16, 1024)[0][0] == "few") == few
+
+
+@pytest.mark.parametrize("T,K,N,wide", [
+    (512, 4096, (4096, 1024, 1024), True), (1024, 4096, (4096, 1024, 1024), False), (640, 8192, (8192,), True),
+    (1024, 8192, (8192,), False), (768, 4096, (4096,), True), (512, 14336, (4096,), False)])
+def test_dx_alone_takes_the_form_that_measured_faster(T, K, N, wide):
+    assert (layer_rules.gradient(T, K, N, 16, 8, weights=False)[0][0] == "wide") == wide
