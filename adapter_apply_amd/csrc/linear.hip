@@ -1507,15 +1507,14 @@ bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R) {
 }
 
 // Whether k_lin_few (or k_lin_one) takes a forward batch.  Its work-groups read
-// x over and over, so the tiles overtake it as tokens times W grow, sooner where
-// a work-group takes several rounds of K.  Against the wide tiles, us: 2048 x 1024,
+// x over and over, so the tiles overtake it as tokens times W grow.  Against the wide tiles, us: 2048 x 1024,
 // 4 tokens 11.3 and 9.2; with as many further columns as the layer's (4096 x 6144,
 // rank 16, 128 slots) one token 20.9 and 23.2, 4 tokens 23.4 and 23.2.  Where lora_a
 // is too large for those, against k_lin_shrink and the tiles (rank 16, medians that
 // repeat within 2 %): 4096 x 6144, 4 tokens 23.5 and 24.4, 8 tokens 25.7 and 25.4,
 // 16 tokens 29.1 and 26.8, 64 tokens 39.3 and 31.5; 4096 x 4096, 16 tokens 22.6 and
 // 24.8; 8192 x 8192, 2 tokens 38.1 and 38.3, 4 tokens 40.6 and 39.9, 8 tokens 46.3
-// and 41.3; 2048 x 16384, 16 tokens 27.7 and 30.4.  Past 16 tokens: 1032 x 2056, 48
+// and 41.3; 2048 x 8192, 16 tokens 19.1 and 21.2.  Past 16 tokens: 1032 x 2056, 48
 // tokens 13.2 and 14.4; 1032 x 8200, 17 tokens 15.2 and 16.6, 48 tokens 20.2 and
 // 20.0; 2048 x 2048, 20 tokens 16.9 and 15.4.
 bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
@@ -1523,7 +1522,7 @@ bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     const int64_t n = columns(N, S), wide = wide_cols(n, S, R, L);
     if (T > kLinFewTokens || n > 32768) return false;
     if (wide) return T <= 2 && 2 * wide > n;
-    return T * n * K <= (T > 16 ? 1 << 27 : K > 2048 ? 1 << 28 : 1 << 29);
+    return T * n * K <= (T > 16 ? 1 << 27 : 1 << 28);
 }
 
 // Direct batches whose rank vectors come out of the tiles as further columns: a

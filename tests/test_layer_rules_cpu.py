@@ -120,7 +120,7 @@ def test_one_token_takes_the_form_that_measured_faster(K, N, R, one):
 
 @pytest.mark.parametrize("T,K,N,few", [
     (4, 4096, (4096, 1024, 1024), True), (16, 4096, (4096, 1024, 1024), False), (16, 4096, (4096,), True),
-    (2, 8192, (8192,), True), (8, 8192, (8192,), False), (16, 2048, (16384,), True),
+    (2, 8192, (8192,), True), (8, 8192, (8192,), False), (16, 2048, (8192,), True),
     (48, 1032, (2056,), True), (64, 4096, (4096, 1024, 1024), False)])
 def test_few_tokens_take_the_form_that_measured_faster(T, K, N, few):
     assert (layer_rules.forward(T, K, N, 16, 1024)[0][0] == "few") == few
