@@ -1217,7 +1217,11 @@ struct LinReduceArgs {
 // the tokens without a slot in token order; and each row's slot (or -1) after
 // it.  A work-group writes 256 positions of the slots' runs and places its 256
 // tokens without a slot, whose number before it is counted from idx (a bitmap
-// of the slots in use in LDS).
+// of the slots in use in LDS), or past kOrderScan tokens from the slots' runs,
+// since the counting grows with the square of the tokens (all of k_lin_vectors,
+// rank 8, us: 4096 tokens, 8 slots 5.7 and by the runs 4.9, 1024 slots 5.3 and 7.9;
+// 8192 tokens 8.0 and 5.6; 2^20 tokens 1180 and 37, of 1024 slots 1190 and 203).
+constexpr int kOrderScan = 4096;
 __device__ __forceinline__ void row_order(const LinReduceArgs &a) {
     constexpr int NW = kRedThreads / 64;
     __shared__ unsigned s_act[kMaxSlots / 32];
@@ -1234,8 +1238,23 @@ __device__ __forceinline__ void row_order(const LinReduceArgs &a) {
     __syncthreads();
     auto none = [&](int s) { return s < 0 || s >= a.L || !(s_act[s >> 5] >> (s & 31) & 1); };
     int before = 0;
+    if (base <= kOrderScan) {
 #pragma unroll 8
-    for (int i = tid; i < base; i += kRedThreads) before += none(a.idx[i]);
+        for (int i = tid; i < base; i += kRedThreads) before += none(a.idx[i]);
+    } else {
+        // all tokens before the block but the slots' own (a run ascends)
+        before = tid == 0 ? base : 0;
+        for (int s = tid; s < a.L; s += kRedThreads) {
+            const int start = a.seg.slot_start[s];
+            int lo = start, hi = a.seg.slot_start[s + 1];
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (a.seg.perm[mid] < base) lo = mid + 1;
+                else hi = mid;
+            }
+            before -= lo - start;
+        }
+    }
     for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
     const bool mine = t < a.T && none(a.idx[t]);
     const unsigned long long b = __ballot(mine);

@@ -168,3 +168,18 @@ def test_backward_without_x(T, K, N):
                                         buf=buf if weights else None)
                 got.append([dx, *(dB or [])])
             assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+@pytest.mark.parametrize("T,L", [(4097, 1), (4700, 300), (8191, 7), (70000, 1024), (33000, 40)])
+def test_tokens_without_a_slot_in_long_batches(T, L):
+    """Their places behind the slots' rows, counted from the slots' runs: every
+    row of y and dx is there once."""
+    c = Layer(T, 16, (12,), 8, L, seed=T, stale=True, runs=L == 7)
+    y_ref, y_tol, b_ref, b_tol = c.forward()
+    assert 0 < sum(len(m) for _, _, m in c.members()) < T
+    full, y, buf = run_forward(c)
+    within(y, y_ref, y_tol, "y")
+    within(buf, b_ref, b_tol, "buf")
+    dx = torch.full((T, 16), FILL, dtype=torch.bfloat16, device="cuda")
+    run_backward(c, dx)
+    within(dx, *c.backward()[:2], "dx")
