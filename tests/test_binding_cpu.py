@@ -168,3 +168,22 @@ def test_bench_refuses_more_than_one_gpu():
     assert r.returncode == 2
     assert "exactly one GPU" in r.stderr
     assert r.stdout == ""
+
+
+def test_counter_summaries_outlive_edits_of_the_layer_kernels(monkeypatch, tmp_path):
+    """The committed counters belong to the sources of the kernels that the bench
+    runs: an edit of another operator's source keeps them, one of theirs does not."""
+    import shutil
+    import bench
+    csrc = tmp_path / "adapter_apply_amd" / "csrc"
+    shutil.copytree(os.path.join(bench.ROOT, "adapter_apply_amd", "csrc"), csrc)
+    want = bench.kernel_hash()
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.kernel_hash() == want
+    for f in bench.LAYER_SOURCES:
+        (csrc / f).write_text((csrc / f).read_text() + "int more;\n")
+    assert bench.kernel_hash() == want
+    (csrc / "relay.hip").write_text((csrc / "relay.hip").read_text() + "// a comment\n")
+    assert bench.kernel_hash() == want
+    (csrc / "relay.hip").write_text((csrc / "relay.hip").read_text() + "int more;\n")
+    assert bench.kernel_hash() != want
