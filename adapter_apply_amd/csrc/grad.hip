@@ -2,8 +2,8 @@
 // [L][m]; slot i's norm runs over every tensor's row i.
 //   norm[i] = sqrt(sum g^2);  out = round(g * min(1, max_norm[i] / (norm[i] + 1e-6)))
 // Work-group = (tensor, chunk of kChunk elements of one slot's row).  Both
-// passes stream their bytes once and are bound by HBM: 320 tensors, 453 MB, 84 us
-// (5.4 TB/s) for the norm's and 162 us (5.6 TB/s) for the clip's.  Squares are summed in
+// passes stream their bytes once and are bound by HBM: 320 tensors, 453 MB, 83 us
+// (5.4 TB/s) for the norm's and 160 us (5.7 TB/s) for the clip's.  Squares are summed in
 // 64 bits (no overflow or underflow of a square, and no error that grows with
 // the number of elements; the fp64 rate is far above what the bytes need), in
 // a fixed order: partial sums [L][items], added by the slot's last work-group.

@@ -47,10 +47,10 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // and a block of several goes through a temporary and a select, in the K
 // tiles (MIXED) or after them.
 //
-// Bound by the matrix rate: 8192 tokens, 4096 x 28672, rank 64, 16 slots 1.58 to
-// 1.71 ms; its base product alone 1.47 ms, 1.31 PFLOP/s (1.4 us per K tile of 256 x
-// 256, 1.0 at the dense peak of a 2.1 GHz clock).  Small batches are bound by L2:
-// 256 tokens, 4096 x 6144 read 200 MB of operand tiles in 24 us.
+// Bound by the matrix rate: 8192 tokens, 4096 x 28672, rank 64, 16 slots 1.71 ms
+// (median of 24; 1.64 to 2.16); its base product alone 1.48 ms, 1.30 PFLOP/s (1.4 us
+// per K tile of 256 x 256, 1.0 at the dense peak of a 2.1 GHz clock).  Small batches
+// are bound by L2: 256 tokens, 4096 x 6144 request 280 MB there in 25 us.
 template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED>
 __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
     constexpr int NW = WM * WN, BK = 64, KK = 2;
@@ -609,9 +609,9 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
 // 16 ranks of a slice), 8 waves each taking every eighth 64-column step of K
 // straight from global memory into 16x16x32 MFMA fragments; the waves' sums
 // are added in order.  Work-groups of y past the block's slots end at once;
-// y = 0 clears buf for the tokens without a slot.  Latency: one slot's loads and
-// sums take 7.6 us (one token, K 4096, rank 16); past some tokens the lora_a
-// reads per block of 16 (777 tokens, 1352, rank 24, 5 slots: 10.7 us).
+// y = 0 clears buf for the tokens without a slot.  Latency: 9.4 us for 4 tokens of K
+// 4096, rank 16; past some tokens the lora_a reads per block of 16 (500 tokens, K
+// 2056, rank 8, 520 slots: 8.5 us).
 constexpr int kShWaves = 8;
 struct LinShrinkArgs {
     const uint16_t *x;
@@ -721,7 +721,7 @@ __device__ __forceinline__ void add_delta(floatx4_t &r, const LinArgs &a, const 
 // from global memory into 16x16x32 MFMA fragments -- W is read once, 64 bytes
 // of 16 rows per load, with U steps in flight.  The waves' sums are added in
 // order through LDS; then each thread adds the delta of one token and 4
-// columns.  4096 x 6144: 14 us for one token, 3.6 TB/s of W.
+// columns.  4096 x 6144: 14.9 us for 4 tokens, 3.4 TB/s of W.
 constexpr int kFewWaves = 8;
 template <int TB, int CT, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void k_lin_few(LinArgs a) {
@@ -1201,8 +1201,8 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
 // own, scales, splits into bf16 parts, and clears buf for tokens without a
-// slot.  Latency bound: 12.8 us for 8192 tokens of 2 x 64 ranks with the row order,
-// 5.3 for 1024 of 128.
+// slot.  Latency bound: 9.7 us for 8192 tokens of 2 x 64 ranks with the row order,
+// 5.6 for 1024 of 128.
 constexpr int kRedThreads = 256;
 struct LinReduceArgs {
     LinVectors job[2];
@@ -1400,7 +1400,9 @@ bool lin_grid_fits(int32_t T, int32_t K, const int64_t *N, int32_t S) {
 }
 
 // The tiles of a batch and their K splits.  join, wide: LinArgs' join_delta and
-// wide; base: there is a base product.
+// wide; base: there is a base product.  (Times at this rule and the next ones: us of
+// whole calls in graph replays.  They repeat within 2 %, so figures nearer than
+// that are ties.)
 LinTilePlan lin_tile_plan(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool gradient,
                           bool join, bool wide, bool base) {
     // 256 x 256 from 192 tiles on, most of a tile per CU (4096 tokens, 4096 x 4096, 256
@@ -1415,8 +1417,8 @@ LinTilePlan lin_tile_plan(int32_t T, int32_t K, const int64_t *N, int32_t S, int
     if (!base) nk = 0;
     // K splits, about kLinSplitTiles work-groups of at least 8 K tiles each; 4 of a
     // few tokens that are joined anyway, whose sums are small (4 tokens of 1352 x
-    // 1652 9.7 us, 11.5 with 8; 64 tokens 11.3 and 12.3, of 2048 x 2048 12.1 and
-    // 11.7; 128 tokens 14.2 and 13.4)
+    // 1652 9.5 us, 11.5 with 8; 64 tokens 11.7 and 12.5, of 512 x 4096 10.6 and 11.0,
+    // of 2048 x 2048 12.3 and 11.8; 128 tokens 14.7 and 13.6)
     const int least = join && T <= 64 ? 4 : 8;
     auto splits = [&](int64_t t) {
         int64_t k = kLinSplitTiles / t;
@@ -1555,7 +1557,7 @@ bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int3
 // which reads S R lora_a rows per token.  weights: dA or dB are wanted too, which
 // need the segments and the vectors in parts either way.  Against the sorted form
 // (us; MB (2^20) of lora_a and sums): dx alone, rank 16, 8 slots, 6144 x 4096: 16
-// tokens 22.1 and 42.1, 512 (224 MB) 56.0 and 69.9, 640 (280 MB) 70.1 and 76.6, 896
+// tokens 20.3 and 40.9, 512 (224 MB) 56.0 and 69.9, 640 (280 MB) 70.1 and 76.6, 896
 // (392 MB) 83.6 and 94.6, 1024 (448 MB) 106 and 100; 8192 x 8192, 512 tokens (192
 // MB) 110 and 104, 640 (240 MB) 122 and 140, 768 (288 MB) 141 and 140, 1024 (384 MB)
 // 214 and 154; 4096 x 4096, 768 tokens (144 MB) 52.1 and 62.6, 1024 (192 MB) 73.8 and

@@ -63,8 +63,9 @@ __global__ __launch_bounds__(kPadThreads) void k_lin_pad(PadArgs a) {
 
 // v: work-group = (tile of at most 64 tokens of one slot, slice, RB ranks,
 // split of the slice's columns), 4 waves of 16 tokens.  A stage is 64 columns
-// of dy's rows and 64 rows of lora_b, three in flight.  Bound by dy's bytes: 8192
-// tokens of 28672 columns, 470 MB in 103 us.
+// of dy's rows and 64 rows of lora_b, three in flight.  Bound by bytes: 8192 tokens
+// of 28672 columns, dy's 470 MB and what lora_b's tiles read again, 680 MB past L2
+// in 102 us.
 struct DuArgs {
     const uint16_t *dy;
     int64_t lddy;
@@ -160,8 +161,8 @@ __global__ __launch_bounds__(256) void k_lin_du(DuArgs a) {
 // through transposed reads; the rank vectors' three bf16 parts, which hold the
 // whole fp32 value, add into the same accumulators).  Slots without tokens
 // write zeros.  Bound by its bytes: 8192 tokens, 4096 -> 28672, rank 64, 16 slots,
-// some 750 MB in 164 us (250 with two stages of 64 tokens); 4096 tokens, 14336 ->
-// 4096, rank 32, 170 MB in 35 us.
+// 700 MB past L2 in 170 us (median of 24, 164 to 203; 250 with two stages of 64
+// tokens); 4096 tokens, 14336 -> 4096, rank 32, 170 MB in 36 us.
 constexpr int kWgCols = 128;
 constexpr int kWgTokens = 1024;       // token indexes staged at a time
 constexpr int kWgStep = 32;           // tokens per stage
