@@ -614,19 +614,18 @@ def _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, S_cols):
     if x is not None:
         _rowmajor(x, "x")
         _need_dtype(x, (bf16,), "x")
+    t, name = S_cols
+    _rowmajor(t, name)
+    _need_dtype(t, (bf16,), name)
     if len(A) < 1 or A[0].dim() != 3 or len(A) != len(B) or any(b.dim() != 3 for b in B):
         raise ValueError("A and B must hold one [L, R, K] and one [L, N_s, R] tensor per slice "
                          f"(got {len(A)} and {len(B)} tensors)")
     L, R, K = A[0].shape
-    T = S_cols[0].shape[0] if x is None else x.shape[0]
-    K = K if x is None else x.shape[1]
+    T, K = (t.shape[0], K) if x is None else x.shape
     N = [b.shape[1] for b in B]
     _need_stack(A, "A", [(L, R, K)] * len(A), bf16)
     _need_stack(B, "B", [(L, n, R) for n in N], bf16)
     n = sum(N)
-    t, name = S_cols
-    _rowmajor(t, name)
-    _need_dtype(t, (bf16,), name)
     if t.shape[0] != T or t.shape[1] < n:
         raise ValueError(f"{name} has shape {list(t.shape)}; expected [{T}, >= {n}]")
     if W is not None:

@@ -439,6 +439,8 @@ lora_status_t lora_linear_workspace_size(int32_t T, int32_t K, const int64_t *N,
  * bias: device bf16 [sum N] or NULL; y: device bf16 [T][ldy], overwritten (its
  * columns past sum N untouched).  All sums in fp32, one rounding; u enters the
  * second product as a sum of two bf16 values (within 2^-16 of the fp32 value).
+ * The same call gives the same bits; the order of the sums follows from the
+ * sizes, so a token of another batch size may round differently.
  * buf: NULL, or device fp32 [S][T][R] that receives u (zero for tokens without
  * an adapter and for j >= slot_rank[i]) for lora_linear_backward.
  * flags: LORA_FLAG_SEGMENTS_READY.

@@ -406,3 +406,10 @@ def test_backward_binding_needs_x_only_where_it_is_read():
     for name in ("x", "W"):
         with pytest.raises(ValueError, match="x and W are needed"):
             call_forward(tensors(**{name: None}))
+
+
+@pytest.mark.parametrize("dy", [torch.zeros((), dtype=BF), torch.zeros(T, dtype=BF), torch.zeros(T, sum(N))],
+                         ids=["no dims", "one dim", "fp32"])
+def test_backward_binding_refuses_dy_without_x(dy):
+    with pytest.raises(ValueError, match="dy"):
+        call_backward(tensors(x=None, dA=None, dB=None, y=dy))
