@@ -560,8 +560,8 @@ def lora_linear_workspace_size(T: int, K: int, N: Sequence[int], R: int, L: int)
 
 def alloc_linear_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, device="cuda"):
     """A zero-filled workspace of lora_linear and lora_linear_backward for at
-    most T tokens; N lists the slices' widths.  Layers that share it need the
-    largest value of each argument (N slice by slice)."""
+    most T tokens; N lists the slices' widths.  Layers may share one as large as
+    the largest of their own."""
     return _aligned_ws(lora_linear_workspace_size(T, K, N, R, L), device)
 
 

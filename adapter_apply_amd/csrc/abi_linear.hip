@@ -13,11 +13,12 @@ namespace {
 
 inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
-// Workspace of lora_linear and lora_linear_backward.  Every region grows with
-// each size argument.  The last line and the region below it belong to the
-// one-launch segment build, which needs them zero and leaves them zero; the
-// region's place follows from the buffer's size, T and L, so in a workspace of
-// the largest sizes no layer's own regions reach another layer's.
+// Workspace of lora_linear and lora_linear_backward.  Behind the call's own
+// regions stands room for the largest exchange region that a one-launch segment
+// build of any T and L takes below the last line: those bytes need to be zero and
+// are left zero, and no layer that shares the workspace writes there, whatever
+// its sizes (the region ends where the buffer does, so it is not at one place of
+// the layout).
 struct LinWs {
     SegLayout seg;
     size_t order;       // int32 [2][T]: row order of the tile GEMM and the rows' slots
@@ -26,6 +27,7 @@ struct LinWs {
     size_t v;           // fp32 [S][T][R]: v by token (wide gradients)
     size_t part;        // fp32 partial sums
     size_t pad;         // bf16 [T][pad_cols]: dy with slices of whole 8-element units
+    size_t data;        // end of the call's own regions
     size_t end;
     bool padded;        // some N_s % 8: dy goes through pad
     int64_t pad_cols;
@@ -75,8 +77,9 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         w.padded = w.padded || N[s] % 8;
         w.pad_cols += round8(N[s]);
     }
-    o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);   // (used or not)
-    w.end = o + seg_x_bytes(T, L) + 256;
+    if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
+    w.data = o;
+    w.end = o + seg_x_bytes(kSegOneMaxWg * kSegThreads, kMaxSlots) + 256;
     return w;
 }
 
@@ -93,7 +96,7 @@ lora_status_t check_layer(int32_t T, int32_t K, int64_t ldx, const int64_t *N, i
 
 SegPtrs lin_seg(void *ws, size_t ws_bytes, const LinWs &w, int32_t T, int32_t L) {
     SegPtrs seg = seg_ptrs(ws, w.seg);
-    attach_seg_x(seg, ws, ws_bytes, T, L, 0, w.end - seg_x_bytes(T, L) - 256);
+    attach_seg_x(seg, ws, ws_bytes, T, L, 0, w.data);
     return seg;
 }
 

@@ -422,10 +422,9 @@ lora_status_t moe_lora_apply(int32_t kind, void *y, int64_t ldy, int32_t reduce_
 
 /* Workspace bytes of lora_linear and lora_linear_backward for these sizes.
  * Rules of `ws` as above (256-byte aligned, zero-filled once by
- * lora_workspace_init, calls ordered on one stream, sized at the largest value
- * of each argument when shared by several layers: T, K, R, L, S and each
- * N[s]; a maximum of the layers' own sizes is not enough), but it is not shared
- * with the calls above, lora_build_segments excepted. */
+ * lora_workspace_init, calls ordered on one stream), except that layers which
+ * share one need no more than the largest of their own sizes, and that it is not
+ * shared with the calls above, lora_build_segments excepted. */
 lora_status_t lora_linear_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
                                          int32_t L, size_t *bytes);
 

@@ -183,3 +183,24 @@ def test_tokens_without_a_slot_in_long_batches(T, L):
     dx = torch.full((T, 16), FILL, dtype=torch.bfloat16, device="cuda")
     run_backward(c, dx)
     within(dx, *c.backward()[:2], "dx")
+
+
+@pytest.mark.parametrize("p,q", [((4096, 64, (1020,), 8, 64), (7168, 64, (1024,), 8, 64)),
+                                 ((5000, 72, (36,), 8, 3), (6000, 64, (64, 32), 16, 900)),
+                                 ((1300, 136, (100, 36), 24, 5), (40, 4096, (4096,), 16, 8))], ids=str)
+def test_layers_share_the_larger_workspace(p, q):
+    """Forward and gradient of two layers in turn, the workspace as large as the
+    larger one's: the bits of calls with workspaces of their own."""
+    cs = [Layer(*s, seed=51 + i) for i, s in enumerate((p, q))]
+    ws = max((aa.alloc_linear_workspace(*s) for s in (p, q)), key=lambda t: t.numel())
+
+    def run(c, ws):
+        y, buf = run_forward(c, ws=ws)[1:]
+        dx = torch.empty((c.T, c.K), dtype=torch.bfloat16, device="cuda")
+        return [y, buf, dx, *sum(run_backward(c, dx, ws=ws), [])]
+
+    want = [run(c, None) for c in cs]
+    for _ in range(2):
+        for c, w in zip(cs, want):
+            assert all(torch.equal(a, b) for a, b in zip(run(c, ws), w))
+    aa.lora_workspace_check(ws)

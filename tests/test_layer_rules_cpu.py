@@ -21,26 +21,16 @@ def size(T, K, N, R, L):
 
 
 def data_end(T, K, N, R, L):
-    """Where a call's own regions end: the exchange region and the last line are
-    the end of its size."""
-    return size(T, K, N, R, L) - 256 - seg_exchange_bytes(T, L)
-
-
-def largest(a, b):
-    """Sizes of a workspace that both layers share: the largest of each argument."""
-    n = [0] * max(len(a[2]), len(b[2]))
-    for v in (a[2], b[2]):
-        for i, w in enumerate(v):
-            n[i] = max(n[i], w)
-    return max(a[0], b[0]), max(a[1], b[1]), tuple(n), max(a[3], b[3]), max(a[4], b[4])
+    """Where a call's own regions end: room for the largest exchange region and
+    the last line are the end of its size."""
+    return size(T, K, N, R, L) - 256 - seg_exchange_bytes(1 << 20, 1024)
 
 
 def shares(a, b):
-    both = size(*largest(a, b))
-    for p, q in ((a, b), (b, a)):
-        assert size(*p) <= both, (p, q)
-        # p leaves q's exchange region alone in a workspace of any size that is enough
-        assert data_end(*p) <= both - 256 - seg_exchange_bytes(q[0], q[4]), (p, q)
+    """a and b on a workspace as large as the larger one's size (and larger)."""
+    for ws in (max(size(*a), size(*b)), max(size(*a), size(*b)) + 4096):
+        for p, q in ((a, b), (b, a)):
+            assert data_end(*p) <= ws - 256 - seg_exchange_bytes(q[0], q[4]), (p, q)
 
 
 @pytest.mark.parametrize("a,b", [
@@ -49,13 +39,32 @@ def shares(a, b):
     ((8192, 4096, (4096,), 16, 64), (7000, 4096, (4092,), 16, 64)),
     ((6000, 64, (1024,), 8, 8), (6000, 64, (1020,), 8, 900)),
     ((300, 64, (64, 36), 8, 8), (300, 64, (68,), 8, 8)),
+    ((16, 16384, (14336,), 128, 8), (16384, 8, (8,), 8, 1024)),
 ], ids=str)
-def test_layers_share_a_workspace_of_the_largest_sizes(a, b):
-    """A layer whose dy is copied (widths off 8) next to one whose is not."""
+def test_layers_share_the_larger_workspace(a, b):
+    """A layer whose dy is copied (widths off 8) next to one whose is not, or with
+    more tokens or slots."""
     shares(a, b)
 
 
-def test_any_two_layers_share_a_workspace_of_the_largest_sizes():
+def test_every_size_holds_the_largest_exchange_region():
+    """Also that of a call whose own regions take next to nothing, and no more
+    than that: one slot more costs no exchange counts."""
+    small = size(1, 8, (4,), 8, 1)
+    assert 0 < data_end(1, 8, (4,), 8, 1) < 16384, small
+    for T in (1, 5000):
+        grows = size(T, 8, (4,), 8, 1024) - size(T, 8, (4,), 8, 1023)
+        assert 0 <= grows <= 256 + 4 * ((T + 1023) // 1024) + 2 * 256 + 2 * 16, grows
+
+
+def test_segments_of_a_layer_fit_its_workspace():
+    """What lora_build_segments writes lies before the layer's other regions."""
+    for T, L in ((1, 1), (700, 1024), (8192, 64), (70000, 1024)):
+        lay = aa.lora_segment_layout(T, L)
+        assert max(v for k, v in lay.items() if not k.startswith("tile_")) < data_end(T, 8, (4,), 8, L)
+
+
+def test_any_two_layers_share_the_larger_workspace():
     rng = random.Random(7)
 
     def layer():
