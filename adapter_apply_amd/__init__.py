@@ -51,6 +51,9 @@ LORA_FLAG_PARTIAL = 4
 LORA_FLAG_RELAY_GIVE_UP = 8   # test hook: the RELAY path's waits give up at once
 LORA_FLAG_ACCUMULATE = 16     # lora_linear_backward: dA, dB +=
 
+LORA_MX_FP4 = 0
+LORA_MX_INT8 = 1
+
 # Every symbol the header declares, with its ctypes signature.
 _vp = C.c_void_p
 _i32 = C.c_int32
@@ -97,6 +100,14 @@ SIGNATURES = {
     "lora_linear_backward": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp,
                                     _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                     _i32, _u32, _vp, _sz, _vp]),
+    "lora_mx_quantize": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
+    "lora_mx_dequantize": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
+    "lora_linear_mx_workspace_size": (_i32, [_i32, _i32, _vp, _i32, _i32, _i32, C.POINTER(_sz)]),
+    "lora_linear_mx": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                              _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _u32, _vp, _sz, _vp]),
+    "lora_linear_mx_backward": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                                       _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32,
+                                       _vp, _vp, _vp, _vp, _i32, _u32, _vp, _sz, _vp]),
     "lora_grad_workspace_size": (_i32, [_vp, _i32, _i32, C.POINTER(_sz)]),
     "lora_grad_norm": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _sz, _vp]),
     "lora_grad_clip": (_i32, [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp]),
@@ -657,15 +668,9 @@ def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bi
           _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
 
 
-def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
-                         B: Sequence, idx, slot_rank, scale, ws, buf=None, flags: int = 0,
-                         stream=None):
-    """Gradient of lora_linear (W frozen).  dx [T, K] bf16 or None; dA[s]
-    [L, R, K] and dB[s] [L, N_s, R] fp32, or None; dy [T, >= sum N].  W None:
-    dx += the adapters' part.  buf: x A^T as lora_linear left it, or None.  x
-    [T, K] may be None where it is not read: no dA, and no dB or a buf."""
+def _check_backward(dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws, T, K, L, R, N, *more):
+    """Checks of the gradients' outputs; returns the device and the slices."""
     torch = _torch()
-    T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
     S = len(N)
     if x is None and (dA is not None or (dB is not None and buf is None)):
         raise ValueError("x is needed for dA, and for dB without buf")
@@ -680,12 +685,131 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
     outs = [t.data_ptr() for t in (dx, *(dA or ()), *(dB or ())) if t is not None and t.numel()]
     if len(set(outs)) != len(outs):
         raise ValueError("dx, dA and dB must be different tensors")
-    dev = _one_device((dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws))
+    return _one_device((dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws, *more)), S
+
+
+def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
+                         B: Sequence, idx, slot_rank, scale, ws, buf=None, flags: int = 0,
+                         stream=None):
+    """Gradient of lora_linear (W frozen).  dx [T, K] bf16 or None; dA[s]
+    [L, R, K] and dB[s] [L, N_s, R] fp32, or None; dy [T, >= sum N].  W None:
+    dx += the adapters' part.  buf: x A^T as lora_linear left it, or None.  x
+    [T, K] may be None where it is not read: no dA, and no dB or a buf."""
+    T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
+    dev, S = _check_backward(dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws, T, K, L, R, N)
     _call("lora_linear_backward", dev, stream, _ptr(dx), 0 if dx is None else dx.stride(0),
           None if dA is None else _ptr_array(dA), None if dB is None else _ptr_array(dB), _ptr(dy),
           dy.stride(0), _ptr(x), 0 if x is None else x.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
           _ptr_array(A), _ptr_array(B), (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank),
           _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
+
+
+# ---------------------------------------------------------------------------
+# microscaled storage, and the layer with its projection or activations in it
+# ---------------------------------------------------------------------------
+
+def _mx_shapes(M, K, fmt):
+    """Shapes of the codes and scales of an [M, K] matrix."""
+    if fmt not in (LORA_MX_FP4, LORA_MX_INT8):
+        raise ValueError(f"fmt must be LORA_MX_FP4 or LORA_MX_INT8 (got {fmt})")
+    n = (K + 31) // 32
+    return (M, n * (16 if fmt == LORA_MX_FP4 else 32)), (M, (n + 3) // 4 * 4)
+
+
+def _need_mx(codes, scales, M, K, fmt, name):
+    u8 = _torch().uint8
+    cs, ss = _mx_shapes(M, K, fmt)
+    for t, shape, what in ((codes, cs, name), (scales, ss, f"{name}'s scales")):
+        if t.dtype is not u8 or t.shape != shape or t.stride(1) != 1:
+            raise ValueError(f"{what} must be a uint8 {list(shape)} tensor with unit column stride (got {t.dtype} "
+                             f"{list(t.shape)})")
+
+
+def alloc_mx(M: int, K: int, fmt: int, device="cuda"):
+    """Codes and scales (uint8) of an [M, K] matrix, not initialised."""
+    torch = _torch()
+    cs, ss = _mx_shapes(M, K, fmt)
+    return (torch.empty(cs, dtype=torch.uint8, device=device),
+            torch.empty(ss, dtype=torch.uint8, device=device))
+
+
+def _mx_call(name, x, codes, scales, fmt, stream, outs_first):
+    _rowmajor(x, "x")
+    _need_dtype(x, _float_types(), "x")
+    M, K = x.shape
+    _need_mx(codes, scales, M, K, fmt, "codes")
+    dev = _one_device((x, codes, scales))
+    mx = (_ptr(codes), codes.stride(0), _ptr(scales), scales.stride(0))
+    xs = (_ptr(x), x.stride(0))
+    _call(name, dev, stream, *(mx + xs if outs_first else xs + mx), M, K, fmt, _dtype_code(x))
+
+
+def lora_mx_quantize(codes, scales, x, fmt: int, stream=None):
+    """codes, scales (shapes of alloc_mx) = x [M, K], bf16 or fp32, in blocks of
+    32 that share a power of two: fmt LORA_MX_FP4 (e2m1) or LORA_MX_INT8."""
+    _mx_call("lora_mx_quantize", x, codes, scales, fmt, stream, True)
+
+
+def lora_mx_dequantize(x, codes, scales, fmt: int, stream=None):
+    """x [M, K], bf16 or fp32 = the values that codes and scales stand for."""
+    _mx_call("lora_mx_dequantize", x, codes, scales, fmt, stream, False)
+
+
+def lora_linear_mx_workspace_size(T: int, K: int, N: Sequence[int], R: int, L: int) -> int:
+    n = _sz(0)
+    _check(lib().lora_linear_mx_workspace_size(T, K, (_i64 * len(N))(*N), len(N), R, L, C.byref(n)),
+           "lora_linear_mx_workspace_size")
+    return int(n.value)
+
+
+def alloc_linear_mx_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, device="cuda"):
+    """alloc_linear_workspace for lora_linear_mx and lora_linear_mx_backward."""
+    return _aligned_ws(lora_linear_mx_workspace_size(T, K, N, R, L), device)
+
+
+def lora_linear_mx(y, x, W, W_scales, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bias=None,
+                   buf=None, flags: int = 0, stream=None):
+    """lora_linear with W [sum N, K] in 4 bits: LORA_MX_FP4 codes and scales."""
+    if x is None or W is None or W_scales is None:
+        raise ValueError("x, W and W_scales are needed")
+    T, K, L, R, N = _check_layer(x, None, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
+    _need_mx(W, W_scales, sum(N), K, LORA_MX_FP4, "W")
+    if bias is not None:
+        _need_vec(bias, sum(N), _torch().bfloat16, "bias")
+    dev = _one_device((y, x, W, W_scales, *A, *B, idx, slot_rank, scale, buf, bias, ws))
+    S = len(N)
+    _call("lora_linear_mx", dev, stream, _ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
+          W.stride(0), _ptr(W_scales), W_scales.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B),
+          (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags,
+          _ptr(ws), ws.nbytes)
+
+
+def lora_linear_mx_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
+                            B: Sequence, idx, slot_rank, scale, ws, buf=None, x_scales=None,
+                            W_scales=None, flags: int = 0, stream=None):
+    """lora_linear_backward with W_scales: W are LORA_MX_FP4 codes; with
+    x_scales: x are LORA_MX_INT8 codes (dB then needs buf)."""
+    if W is None and W_scales is not None:
+        raise ValueError("W_scales without W")
+    if x is None and x_scales is not None:
+        raise ValueError("x_scales without x")
+    if x_scales is not None and dB is not None and buf is None:
+        raise ValueError("dB from an 8-bit x needs buf")
+    T, K, L, R, N = _check_layer(x if x_scales is None else None, W if W_scales is None else None, A, B, idx,
+                                 slot_rank, scale, buf, ws, (dy, "dy"))
+    if W_scales is not None:
+        _need_mx(W, W_scales, sum(N), K, LORA_MX_FP4, "W")
+    if x_scales is not None:
+        _need_mx(x, x_scales, T, K, LORA_MX_INT8, "x")
+    dev, S = _check_backward(dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws, T, K, L, R, N,
+                             x_scales, W_scales)
+    _call("lora_linear_mx_backward", dev, stream, _ptr(dx), 0 if dx is None else dx.stride(0),
+          None if dA is None else _ptr_array(dA), None if dB is None else _ptr_array(dB), _ptr(dy),
+          dy.stride(0), _ptr(x), 0 if x is None else x.stride(0), _ptr(x_scales),
+          0 if x_scales is None else x_scales.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
+          _ptr(W_scales), 0 if W_scales is None else W_scales.stride(0), _ptr_array(A), _ptr_array(B),
+          (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags,
+          _ptr(ws), ws.nbytes)
 
 
 # ---------------------------------------------------------------------------

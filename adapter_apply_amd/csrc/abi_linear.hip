@@ -6,6 +6,7 @@
 
 #include "checks.hpp"
 #include "linear.hpp"
+#include "mx.hpp"
 
 using namespace aa;
 
@@ -27,13 +28,15 @@ struct LinWs {
     size_t v;           // fp32 [S][T][R]: v by token (wide gradients)
     size_t part;        // fp32 partial sums
     size_t pad;         // bf16 [T][pad_cols]: dy with slices of whole 8-element units
+    size_t w16;         // bf16 [sum N][K]: the projection restored from 4 bits
+    size_t x16;         // bf16 [T][K]: x restored from 8 bits
     size_t data;        // end of the call's own regions
     size_t end;
     bool padded;        // some N_s % 8: dy goes through pad
     int64_t pad_cols;
 };
 
-LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool mx = false) {
     LinWs w{};
     w.seg = seg_layout(T, L);
     size_t o = w.seg.end;
@@ -78,9 +81,43 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         w.pad_cols += round8(N[s]);
     }
     if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
+    if (mx) {
+        size_t n = 0;
+        for (int s = 0; s < S; ++s) n += (size_t)N[s];
+        w.w16 = o; o = align256(o + sizeof(uint16_t) * n * K);
+        w.x16 = o; o = align256(o + sizeof(uint16_t) * (size_t)T * K);
+    }
     w.data = o;
     w.end = o + seg_x_bytes(kSegOneMaxWg * kSegThreads, kMaxSlots) + 256;
     return w;
+}
+
+// A matrix: bf16 (scales null), or microscaled codes and scales, ld and lds in bytes.
+struct Mat {
+    const void *p;
+    int64_t ld;
+    const uint8_t *scales;
+    int64_t lds;
+};
+// Codes and scales of rows of K values.
+lora_status_t check_mx(const void *codes, int64_t ldc, const void *scales, int64_t lds, int32_t K, int32_t format) {
+    const int64_t b = mx_blocks(K);
+    if (ldc < b * (format == LORA_MX_FP4 ? 16 : 32) || lds < (b + 3) / 4 * 4) return LORA_E_SHAPE;
+    if (ldc % 16 || lds % 4 || !al(codes, 16) || !al(scales, 4)) return LORA_E_ALIGN;
+    return LORA_OK;
+}
+lora_status_t check_mat(const Mat &m, int32_t K, int32_t format) {
+    return m.scales ? check_mx(m.p, m.ld, m.scales, m.lds, K, format) : check_k(K, m.ld);
+}
+// m restored to bf16 at out.
+hipError_t restore(Mat &m, int64_t rows, int32_t K, int32_t format, void *out, hipStream_t st) {
+    MxArgs a{};
+    a.x = out; a.ldx = K;
+    a.codes = static_cast<uint8_t *>(const_cast<void *>(m.p)); a.ldc = m.ld;
+    a.scales = const_cast<uint8_t *>(m.scales); a.lds = m.lds;
+    a.M = rows; a.K = K;
+    m = Mat{out, K, nullptr, 0};
+    return launch_mx(a, false, format, LORA_DT_BF16, st);
 }
 
 lora_status_t check_layer(int32_t T, int32_t K, int64_t ldx, const int64_t *N, int32_t S, int32_t L,
@@ -109,35 +146,20 @@ lora_status_t sorted_shrink(const void *x, int64_t ldx, int32_t T, int32_t K, co
     return launched(launch_pre_shrink(x, ldx, T, K, sl, S, L, R, slot_rank, seg, nullptr, st, GroupMap(), part, nsp));
 }
 
-}  // namespace
-
-extern "C" {
-
-lora_status_t lora_linear_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
-                                         int32_t L, size_t *bytes) {
-    if (!bytes || !N) return LORA_E_NULL;
-    int64_t total = 0;
-    CHECK(check_sizes(T, S, L, R, LORA_DT_BF16));
-    if (K < 1) return LORA_E_SHAPE;
-    CHECK(check_n(N, S, INT64_MAX / 8 * 4, 0, &total));
-    if (!lin_grid_fits(T, K, N, S)) return LORA_E_SHAPE;
-    *bytes = lin_ws(T, K, N, S, R, L).end;
-    return LORA_OK;
-}
-
-lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K,
-                          const void *W, int64_t ldw, const void *bias, const void *const *A,
-                          const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
-                          const int32_t *idx, const int32_t *slot_rank, const float *scale, float *buf,
-                          int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
+// lora_linear and, mx, lora_linear_mx.
+lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K, Mat W, bool mx,
+                      const void *bias, const void *const *A, const void *const *B, const int64_t *N, int32_t S,
+                      int32_t L, int32_t R, const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                      float *buf, int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
     CHECK(check_layer(T, K, ldx, N, S, L, R, ldy, dtype));
-    CHECK(check_k(K, ldw));
+    if (mx && !W.scales) return LORA_E_NULL;
+    CHECK(check_mat(W, K, LORA_MX_FP4));
     if (T == 0) return LORA_OK;
-    if (!y || !x || !W || !idx || !scale) return LORA_E_NULL;
+    if (!y || !x || !W.p || !idx || !scale) return LORA_E_NULL;
     CHECK(check_ptrs(A, S));
     CHECK(check_ptrs(B, S));
-    if (!al(y, 16) || !al(x, 16) || !al(W, 16) || !al(buf, 16) || !al(bias, 2)) return LORA_E_ALIGN;
-    const LinWs wl = lin_ws(T, K, N, S, R, L);
+    if (!al(y, 16) || !al(x, 16) || !al(W.p, 16) || !al(buf, 16) || !al(bias, 2)) return LORA_E_ALIGN;
+    const LinWs wl = lin_ws(T, K, N, S, R, L, mx);
     CHECK(check_ws(ws, ws_bytes, wl.end));
 
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -173,9 +195,10 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
         const LinVectors v{part, nsp, nullptr, join ? nullptr : hl, kLinPartsFwd, join ? u : buf};
         CHECK(launched(launch_lin_vectors(&v, 1, T, S, L, R, idx, slot_rank, scale, seg, order, st)));
     }
+    if (mx) CHECK(launched(restore(W, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
     LinArgs a{};
     a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
-    a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
+    a.w = static_cast<const uint16_t *>(W.p); a.ldw = W.ld;
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
     a.part = reinterpret_cast<float *>(wp + wl.part);
@@ -192,22 +215,22 @@ lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int3
     return launched(launch_lin_gemm(a, false, st));
 }
 
-lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, float *const *dB,
-                                   const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T,
-                                   int32_t K, const void *W, int64_t ldw, const void *const *A,
-                                   const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
-                                   const int32_t *idx, const int32_t *slot_rank, const float *scale,
-                                   const float *buf, int32_t dtype, uint32_t flags, void *ws,
-                                   size_t ws_bytes, void *stream) {
-    CHECK(check_layer(T, K, x ? ldx : K, N, S, L, R, lddy, dtype));
+// lora_linear_backward and, mx, lora_linear_mx_backward.
+lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *dB, const void *dy, int64_t lddy,
+                       Mat X, int32_t T, int32_t K, Mat Wm, bool mx, const void *const *A, const void *const *B,
+                       const int64_t *N, int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                       const int32_t *slot_rank, const float *scale, const float *buf, int32_t dtype,
+                       uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
+    CHECK(check_layer(T, K, X.p && !X.scales ? X.ld : K, N, S, L, R, lddy, dtype));
+    if (X.p && X.scales) CHECK(check_mat(X, K, LORA_MX_INT8));
     if (dx) CHECK(check_k(K, lddx));
-    if (dx && W) CHECK(check_k(K, ldw));
+    if (dx && Wm.p) CHECK(check_mat(Wm, K, LORA_MX_FP4));
     if (!dx && !dA && !dB) return LORA_E_NULL;
     for (int s = 0; s < S; ++s) {
         if ((dA && !dA[s]) || (dB && !dB[s])) return LORA_E_NULL;
         if ((dA && !al(dA[s], 16)) || (dB && !al(dB[s], 16))) return LORA_E_ALIGN;
     }
-    const LinWs wl = lin_ws(T, K, N, S, R, L);
+    const LinWs wl = lin_ws(T, K, N, S, R, L, mx);
     if (!wl.padded && lddy % 8) return LORA_E_ALIGN;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (T == 0) {
@@ -219,10 +242,11 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         return LORA_OK;
     }
     if (!dy || !idx || !scale) return LORA_E_NULL;
-    if (!x && (dA || (dB && !buf))) return LORA_E_NULL;
+    if (!X.p && (dA || (dB && !buf))) return LORA_E_NULL;
+    if (X.scales && dB && !buf) return LORA_E_NULL;
     CHECK(check_ptrs(A, S));
     CHECK(check_ptrs(B, S));
-    if (!al(dx, 16) || !al(dy, 16) || !al(x, 16) || !al(W, 16) || !al(buf, 16)) return LORA_E_ALIGN;
+    if (!al(dx, 16) || !al(dy, 16) || !al(X.p, 16) || !al(Wm.p, 16) || !al(buf, 16)) return LORA_E_ALIGN;
     CHECK(check_ws(ws, ws_bytes, wl.end));
     const void *outs[2 * kMaxSlices + 1];
     int n_out = 0;
@@ -237,6 +261,10 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
 
     char *wp = static_cast<char *>(ws);
     const Slices sl = make_slices(A, B, N, S, 0);
+    if (X.p && X.scales && dA) CHECK(launched(restore(X, T, K, LORA_MX_INT8, wp + wl.x16, st)));
+    if (dx && Wm.p && Wm.scales) CHECK(launched(restore(Wm, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
+    const void *x = X.p, *W = dx ? Wm.p : nullptr;
+    const int64_t ldx = X.ld, ldw = Wm.ld;
     const SegPtrs seg = lin_seg(ws, ws_bytes, wl, T, L);
     uint16_t *hl_u = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
     uint16_t *hl_v = reinterpret_cast<uint16_t *>(wp + wl.hl_v);
@@ -331,6 +359,110 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
         CHECK(launched(launch_lin_gemm(a, true, st)));
     }
     return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status_t lora_linear_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
+                                         int32_t L, size_t *bytes) {
+    if (!bytes || !N) return LORA_E_NULL;
+    int64_t total = 0;
+    CHECK(check_sizes(T, S, L, R, LORA_DT_BF16));
+    if (K < 1) return LORA_E_SHAPE;
+    CHECK(check_n(N, S, INT64_MAX / 8 * 4, 0, &total));
+    if (!lin_grid_fits(T, K, N, S)) return LORA_E_SHAPE;
+    *bytes = lin_ws(T, K, N, S, R, L).end;
+    return LORA_OK;
+}
+
+lora_status_t lora_linear(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K,
+                          const void *W, int64_t ldw, const void *bias, const void *const *A,
+                          const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
+                          const int32_t *idx, const int32_t *slot_rank, const float *scale, float *buf,
+                          int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
+    return forward(y, ldy, x, ldx, T, K, Mat{W, ldw, nullptr, 0}, false, bias, A, B, N, S, L, R, idx, slot_rank,
+                   scale, buf, dtype, flags, ws, ws_bytes, stream);
+}
+
+lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, float *const *dB,
+                                   const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T,
+                                   int32_t K, const void *W, int64_t ldw, const void *const *A,
+                                   const void *const *B, const int64_t *N, int32_t S, int32_t L, int32_t R,
+                                   const int32_t *idx, const int32_t *slot_rank, const float *scale,
+                                   const float *buf, int32_t dtype, uint32_t flags, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    return backward(dx, lddx, dA, dB, dy, lddy, Mat{x, ldx, nullptr, 0}, T, K, Mat{W, ldw, nullptr, 0}, false, A, B,
+                    N, S, L, R, idx, slot_rank, scale, buf, dtype, flags, ws, ws_bytes, stream);
+}
+
+lora_status_t lora_linear_mx_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
+                                            int32_t L, size_t *bytes) {
+    CHECK(lora_linear_workspace_size(T, K, N, S, R, L, bytes));
+    *bytes = lin_ws(T, K, N, S, R, L, true).end;
+    return LORA_OK;
+}
+
+lora_status_t lora_linear_mx(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K,
+                             const void *W, int64_t ldw, const void *W_scales, int64_t ldws,
+                             const void *bias, const void *const *A, const void *const *B,
+                             const int64_t *N, int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                             const int32_t *slot_rank, const float *scale, float *buf, int32_t dtype,
+                             uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
+    return forward(y, ldy, x, ldx, T, K, Mat{W, ldw, static_cast<const uint8_t *>(W_scales), ldws}, true, bias, A, B,
+                   N, S, L, R, idx, slot_rank, scale, buf, dtype, flags, ws, ws_bytes, stream);
+}
+
+lora_status_t lora_linear_mx_backward(void *dx, int64_t lddx, float *const *dA, float *const *dB,
+                                      const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                      const void *x_scales, int64_t ldxs, int32_t T, int32_t K,
+                                      const void *W, int64_t ldw, const void *W_scales, int64_t ldws,
+                                      const void *const *A, const void *const *B, const int64_t *N,
+                                      int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                                      const int32_t *slot_rank, const float *scale, const float *buf,
+                                      int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes,
+                                      void *stream) {
+    return backward(dx, lddx, dA, dB, dy, lddy, Mat{x, ldx, static_cast<const uint8_t *>(x_scales), ldxs}, T, K,
+                    Mat{W, ldw, static_cast<const uint8_t *>(W_scales), ldws}, true, A, B, N, S, L, R, idx,
+                    slot_rank, scale, buf, dtype, flags, ws, ws_bytes, stream);
+}
+
+static lora_status_t check_mx_call(const void *x, int64_t ldx, const void *codes, int64_t ldc, const void *scales,
+                                   int64_t lds, int64_t M, int32_t K, int32_t format, int32_t dtype) {
+    if (dtype != LORA_DT_F32 && dtype != LORA_DT_BF16) return LORA_E_DTYPE;
+    if (format != LORA_MX_FP4 && format != LORA_MX_INT8) return LORA_E_DTYPE;
+    if (M < 0 || K < 1 || ldx < K) return LORA_E_SHAPE;
+    if (M > 0 && (mx_blocks(K) + 3) / 4 > ((1 << 30) - 1) / M) return LORA_E_SHAPE;
+    if (K % 8 || ldx % (dtype == LORA_DT_BF16 ? 8 : 4)) return LORA_E_ALIGN;
+    CHECK(check_mx(codes, ldc, scales, lds, K, format));
+    if (M == 0) return LORA_OK;
+    if (!x || !codes || !scales) return LORA_E_NULL;
+    return al(x, 16) ? LORA_OK : LORA_E_ALIGN;
+}
+
+lora_status_t lora_mx_quantize(void *codes, int64_t ldc, void *scales, int64_t lds, const void *x,
+                               int64_t ldx, int64_t M, int32_t K, int32_t format, int32_t dtype,
+                               void *stream) {
+    CHECK(check_mx_call(x, ldx, codes, ldc, scales, lds, M, K, format, dtype));
+    if (M == 0) return LORA_OK;
+    MxArgs a{};
+    a.x = x; a.ldx = ldx; a.M = M; a.K = K;
+    a.codes = static_cast<uint8_t *>(codes); a.ldc = ldc;
+    a.scales = static_cast<uint8_t *>(scales); a.lds = lds;
+    return launched(launch_mx(a, true, format, dtype, static_cast<hipStream_t>(stream)));
+}
+
+lora_status_t lora_mx_dequantize(void *x, int64_t ldx, const void *codes, int64_t ldc,
+                                 const void *scales, int64_t lds, int64_t M, int32_t K,
+                                 int32_t format, int32_t dtype, void *stream) {
+    CHECK(check_mx_call(x, ldx, codes, ldc, scales, lds, M, K, format, dtype));
+    if (M == 0) return LORA_OK;
+    MxArgs a{};
+    a.x = x; a.ldx = ldx; a.M = M; a.K = K;
+    a.codes = static_cast<uint8_t *>(const_cast<void *>(codes)); a.ldc = ldc;
+    a.scales = static_cast<uint8_t *>(const_cast<void *>(scales)); a.lds = lds;
+    return launched(launch_mx(a, false, format, dtype, static_cast<hipStream_t>(stream)));
 }
 
 static lora_status_t check_grads(const void *const *g, const int64_t *m, int32_t n, int32_t L, int32_t dtype) {

@@ -479,6 +479,81 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
                                    size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled storage (the OCP MX formats MXFP4 and MXINT8): the frozen
+ * projection of a layer in 4 bits, and activations kept in 8 bits between the
+ * forward and the backward call.
+ *
+ * A row of K values is KB = ceil(K / 32) blocks of 32, the last one filled up
+ * with zeros; a block has one scale byte e and stands for 2^(e - 127) times its
+ * elements (e = 255: every value is NaN).
+ *   codes  device bytes [M][ldc]: 16 KB of a row used (LORA_MX_FP4: e2m1 codes, two
+ *          a byte, the lower nibble first; bit 3 the sign, magnitudes 0, 0.5, 1, 1.5,
+ *          2, 3, 4, 6) or 32 KB (LORA_MX_INT8: two's complement / 64); 16-byte aligned,
+ *          ldc % 16 == 0.
+ *   scales device bytes [M][lds]: KB bytes of a row rounded up to whole 4 used; 4-byte
+ *          aligned, lds % 4 == 0.
+ * bf16 holds every value exactly (fp32 too), overflows to infinity excepted.
+ * ------------------------------------------------------------------------ */
+#define LORA_MX_FP4  0
+#define LORA_MX_INT8 1
+
+/*
+ * codes, scales = x [M][ldx], K values a row, of dtype LORA_DT_BF16 or LORA_DT_F32
+ * (16-byte aligned rows: ldx % 8 == 0 for bf16, % 4 for fp32; K % 8 == 0).  A block's
+ * scale is the power of two of its largest magnitude, over 4 for FP4 (its largest
+ * power), at least 2^-127; elements are rounded to nearest, ties to the even code, and
+ * those past the largest (6, 127 / 64) become it.  A block that holds an infinity or
+ * NaN gets scale 255.  The codes past K of a row's last block and the scales past KB up
+ * to whole 4 are written as zeros.  M >= 0, and M * ceil(K / 128) < 2^30.  No output
+ * overlaps x or another output.
+ */
+lora_status_t lora_mx_quantize(void *codes, int64_t ldc, void *scales, int64_t lds, const void *x,
+                               int64_t ldx, int64_t M, int32_t K, int32_t format, int32_t dtype,
+                               void *stream);
+
+/* x [M][ldx] = the values that codes and scales stand for. */
+lora_status_t lora_mx_dequantize(void *x, int64_t ldx, const void *codes, int64_t ldc,
+                                 const void *scales, int64_t lds, int64_t M, int32_t K,
+                                 int32_t format, int32_t dtype, void *stream);
+
+/* Workspace bytes of lora_linear_mx and lora_linear_mx_backward for these sizes; rules
+ * of `ws` as for lora_linear, whose calls may share it. */
+lora_status_t lora_linear_mx_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
+                                            int32_t L, size_t *bytes);
+
+/*
+ * lora_linear with the projection in 4 bits: W are LORA_MX_FP4 codes [sum N][ldw
+ * bytes] and W_scales [sum N][ldws], blocks along K.  Everything else as lora_linear
+ * called with the restored values in bf16: x, A, B, bias and y are bf16, products of
+ * restored values are exact, and the order of the sums follows from the sizes.
+ */
+lora_status_t lora_linear_mx(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t T, int32_t K,
+                             const void *W, int64_t ldw, const void *W_scales, int64_t ldws,
+                             const void *bias, const void *const *A, const void *const *B,
+                             const int64_t *N, int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                             const int32_t *slot_rank, const float *scale, float *buf, int32_t dtype,
+                             uint32_t flags, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * lora_linear_backward with W, x or both microscaled.
+ * W_scales: W are LORA_MX_FP4 codes (ldw in bytes) as for lora_linear_mx; NULL: W is
+ * bf16 (or NULL), as for lora_linear_backward.
+ * x_scales [T][ldxs]: x are LORA_MX_INT8 codes [T][ldx bytes], the checkpoint of the
+ * forward call's x, and dA is the gradient with its restored values; NULL: x is bf16.
+ * With x_scales dB needs buf (LORA_E_NULL without), the forward call's u of the
+ * unrounded x.  Everything else as lora_linear_backward.
+ */
+lora_status_t lora_linear_mx_backward(void *dx, int64_t lddx, float *const *dA, float *const *dB,
+                                      const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                      const void *x_scales, int64_t ldxs, int32_t T, int32_t K,
+                                      const void *W, int64_t ldw, const void *W_scales, int64_t ldws,
+                                      const void *const *A, const void *const *B, const int64_t *N,
+                                      int32_t S, int32_t L, int32_t R, const int32_t *idx,
+                                      const int32_t *slot_rank, const float *scale, const float *buf,
+                                      int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes,
+                                      void *stream);
+
+/* ------------------------------------------------------------------------
  * Gradient norm and clip, per adapter slot over all of a model's stacked
  * tensors (each adapter is a model of its own; L == 1 is the ordinary global
  * norm).
