@@ -195,10 +195,11 @@ lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t 
         const LinVectors v{part, nsp, nullptr, join ? nullptr : hl, kLinPartsFwd, join ? u : buf};
         CHECK(launched(launch_lin_vectors(&v, 1, T, S, L, R, idx, slot_rank, scale, seg, order, st)));
     }
-    if (mx) CHECK(launched(restore(W, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
+    if (mx && lin_few(T, K, N, S, R, L)) CHECK(launched(restore(W, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
     LinArgs a{};
     a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
     a.w = static_cast<const uint16_t *>(W.p); a.ldw = W.ld;
+    a.ws = W.scales; a.ldws = W.lds;
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(y); a.ldo = ldy;
     a.part = reinterpret_cast<float *>(wp + wl.part);
@@ -262,7 +263,6 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
     char *wp = static_cast<char *>(ws);
     const Slices sl = make_slices(A, B, N, S, 0);
     if (X.p && X.scales && dA) CHECK(launched(restore(X, T, K, LORA_MX_INT8, wp + wl.x16, st)));
-    if (dx && Wm.p && Wm.scales) CHECK(launched(restore(Wm, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
     const void *x = X.p, *W = dx ? Wm.p : nullptr;
     const int64_t ldx = X.ld, ldw = Wm.ld;
     const SegPtrs seg = lin_seg(ws, ws_bytes, wl, T, L);
@@ -309,6 +309,7 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
     LinArgs a{};
     a.p = p; a.ldp = ldp;
     a.w = static_cast<const uint16_t *>(W); a.ldw = ldw;
+    a.ws = W ? Wm.scales : nullptr; a.ldws = Wm.lds;
     a.out = static_cast<uint16_t *>(dx); a.ldo = lddx;
     a.part = part;
     a.idx = idx; a.slot_rank = slot_rank; a.scale = scale;

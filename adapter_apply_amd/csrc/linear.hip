@@ -10,6 +10,7 @@
 // [high | low] against lora rows repeated, so that the product is within 2^-16
 // of the fp32 buffer's, well below the bf16 rounding of the output.
 #include "linear.hpp"
+#include "mx.hpp"
 
 namespace aa {
 
@@ -51,8 +52,36 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // (median of 24; 1.64 to 2.16); its base product alone 1.48 ms, 1.30 PFLOP/s (1.4 us
 // per K tile of 256 x 256, 1.0 at the dense peak of a 2.1 GHz clock).  Small batches
 // are bound by L2: 256 tokens, 4096 x 6144 request 280 MB there in 25 us.
-template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED>
-__global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
+//
+// kQCodes: the projection's Q rows are 4-bit codes.  A thread loads its share of a tile
+// one tile ahead of the DMA into registers and writes it to the stage as bf16, in
+// the DMA's layout, when the stage is free; everything past the stage is the same.
+template <int BM, int BN, int NST>
+struct TileLds {
+    __attribute__((aligned(16))) char stage[NST * (BM + BN) * 128];
+    int tok[BM], slot[BM], list[BM + 1], r8[BM + 1], whole[BM / 16], n, nt, any;
+    unsigned bits[32];
+};
+// Work-group i runs on XCD i % 8: each XCD takes a contiguous run of tiles,
+// ordered so that 8 token tiles share a column tile before the next.
+struct TileAt { int mt, nt; };
+__device__ __forceinline__ TileAt tile_at(const LinArgs &a) {
+    const int total = a.m_tiles * a.n_tiles;
+    const int xcd = blockIdx.x % kXcds, q = total / kXcds, rem = total % kXcds;
+    int id = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
+    const int gm = 8, band = gm * a.n_tiles;
+    const int g = id / band, r = id - g * band;
+    const int rows = min(gm, a.m_tiles - g * gm);
+    const int nt = r / rows;
+    return {g * gm + r - nt * rows, nt};
+}
+// Q operands: bf16 rows of the projection and, past its column tiles, of the
+// adapters; its codes only; the adapters' only (the last two apart, so that one's
+// registers do not crowd the other's loop: in one body the 128 x 128 tiles spill).
+enum { kQRows, kQCodes, kQVectors };
+
+template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED, int Q>
+__device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> &sh, int mt, int nt) {
     constexpr int NW = WM * WN, BK = 64, KK = 2;
     constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
     constexpr int PB = BM * BK * 2, QB = BN * BK * 2;
@@ -61,34 +90,24 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     constexpr int CPR = NN ? BN / 8 : UP;         // 16-byte units per Q row
     static_assert(PI >= 1 && QI >= 1 && NW % 2 == 0, "whole DMA instructions per wave");
     static_assert(BM * BN * 2 <= NST * (PB + QB), "the output tile fits the stages");
-    __shared__ __attribute__((aligned(16))) char s_stage[NST * (PB + QB)];
-    __shared__ int s_tok[BM], s_slot[BM], s_list[BM + 1], s_r8[BM + 1], s_whole[BM / 16], s_n, s_nt, s_any;
-    __shared__ unsigned s_bits[32];
+    char *const s_stage = sh.stage;
+    auto &s_tok = sh.tok, &s_slot = sh.slot;
+    auto &s_list = sh.list, &s_r8 = sh.r8;
+    auto &s_whole = sh.whole;
+    int &s_n = sh.n, &s_nt = sh.nt, &s_any = sh.any;
+    auto &s_bits = sh.bits;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / WN, wn = w % WN;
 
-    // Work-group i runs on XCD i % 8: each XCD takes a contiguous run of
-    // tiles, ordered so that 8 token tiles share a column tile before the next.
-    int mt, nt;
-    {
-        const int total = a.m_tiles * a.n_tiles;
-        const int xcd = blockIdx.x % kXcds, q = total / kXcds, rem = total % kXcds;
-        int id = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
-        const int gm = 8, band = gm * a.n_tiles;
-        const int g = id / band, r = id - g * band;
-        const int rows = min(gm, a.m_tiles - g * gm);
-        nt = r / rows;
-        mt = g * gm + r - nt * rows;
-    }
     // forward: the tile's slice, whose rows of W start at qb; past those in a wide
     // batch (vec), every slot's lora_a rows of a slice, in the gradient its lora_b
     // columns, whose contraction is the slice's alone
     int sc = 0;
     const uint16_t *qb = a.w;
     int64_t ldq = a.ldw, c0 = (int64_t)nt * BN, cend = a.K, obase = 0;   // columns: first, end, slice's first in out
-    const bool vec = MIXED && nt >= a.base_tiles;
+    const bool vec = Q == kQVectors || (Q == kQRows && MIXED && nt >= a.base_tiles);
     if (vec) {
         const int per = (a.L * a.R + BN - 1) / BN;
         nt -= a.base_tiles;
@@ -234,6 +253,84 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
     const void *zero = g_zero16;
     const uint32_t lds0 = lds_addr(s_stage) + w * 1024;
 
+    // kQCodes: a thread's NQ pieces of a tile, HB code bytes each (a block of 32 or half
+    // of one), as rows and blocks such that the 8 lanes of one LDS write hit
+    // different banks; pieces past the contraction's end read zeros (code 0, scale 0).
+    constexpr int NT = NW * 64, HB = 2 * BN >= NT ? 16 : 8, NQ = BN * 32 / (NT * HB), NL = 2 * NQ;
+    struct Pieces { uint4 c[NQ]; uint32_t s[NQ]; };
+    const uint8_t *qcode[NQ], *qscale[NQ];
+    int qrow_of[NQ], qunit[NQ];                   // the piece's row and first 16-byte unit in the stage
+    int q_cs = NN ? sc : 0;
+    int64_t q_rem = 0, q_at = 0;                  // steps left, first row (NN) or K tile
+    constexpr bool codes = Q == kQCodes;
+    static_assert(!codes || NL <= QI, "a base tile issues no more loads than a rank-vector tile");
+    if (codes) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int b = i * NT + tid;
+            int row, blk, half = 0;
+            if (NN && BN == 256) {
+                blk = (b & 3) | ((b >> 3) & 1) << 2;
+                row = ((b >> 2) & 1) | b >> 4 << 1;
+            } else if (HB == 16) {
+                constexpr int BPR = NN ? BN / 32 : 2;
+                blk = b % BPR;
+                row = b / BPR;
+            } else {
+                half = b & 1;
+                blk = (b >> 1) & 1;
+                row = b >> 2;
+            }
+            qrow_of[i] = row;
+            qunit[i] = blk * 4 + half * 2;
+            int64_t n = row;
+            if (!NN) n = a.off[sc] + min(c0 + row, cend - 1);
+            else blk = (c0 >> 5) + blk < (a.K + 31) >> 5 ? (int)(c0 >> 5) + blk : 0;
+            qcode[i] = reinterpret_cast<const uint8_t *>(a.w) + n * a.ldw + blk * 16 + half * 8;
+            qscale[i] = a.ws + n * a.ldws + blk;
+        }
+    }
+    auto load_q = [&](Pieces &r, int i) __attribute__((always_inline)) {
+        const bool in = (NN ? qrow_of[i] : qunit[i] * 8) < q_rem;
+        const void *c = in ? (const void *)(qcode[i] + q_at * (NN ? a.ldw : 32)) : (const void *)g_zero16;
+        const uint8_t *s = in ? qscale[i] + q_at * (NN ? a.ldws : 2) : reinterpret_cast<const uint8_t *>(g_zero16);
+        if (HB == 16) {
+            r.c[i] = *static_cast<const uint4 *>(c);
+        } else {
+            const uint2 h = *static_cast<const uint2 *>(c);
+            r.c[i] = make_uint4(h.x, h.y, 0, 0);
+        }
+        r.s[i] = *s;
+    };
+    auto begin_q = [&]() {                        // the next tile's slice
+        if (NN && q_rem <= 0 && q_cs + 1 < a.S) q_rem = a.n[++q_cs];
+    };
+    auto end_q = [&]() {
+        if (NN) q_at += q_rem < BK ? (q_rem > 0 ? q_rem : 0) : BK;
+        else ++q_at;
+        q_rem -= BK;
+    };
+    auto load_qs = [&](Pieces &r) __attribute__((always_inline)) {
+        begin_q();
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) load_q(r, i);
+        end_q();
+    };
+    // unit u of piece i
+    auto store_q = [&](const Pieces &r, int stage, int i, int u) __attribute__((always_inline)) {
+        const uint32_t c[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
+        const int row = qrow_of[i];
+        *reinterpret_cast<uint4 *>(s_stage + stage * (PB + QB) + PB + row * (CPR * 16) +
+                                   (((qunit[i] + u) ^ qswz(row)) << 4)) = mx_fp4_bf16(c[u], r.s[i] << 23);
+    };
+    auto store_qs = [&](const Pieces &r, int stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int u = 0; u < HB / 4; ++u) store_q(r, stage, i, u);
+    };
+    Pieces qr;
+
     // The next base K tile: steps left in its row (forward) or slice, and the
     // offsets into the P and Q rows.
     int cs = NN ? sc : 0;
@@ -254,6 +351,11 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         po = (NN ? a.poff[cs] : 0) + (int64_t)k0 * BK;
         qo = NN ? ((vec ? 0 : a.off[cs]) + (int64_t)k0 * BK) * ldq : (int64_t)k0 * BK;
     }
+    if (codes) {
+        q_cs = cs;
+        q_rem = rem;
+        q_at = NN ? a.off[cs] + (a.n[cs] - rem) : (a.K - rem) / BK;
+    }
     auto issue = [&](int v, int stage) {
         // recomputed here each time: hoisted lane values would crowd the
         // registers of the fast loop
@@ -265,13 +367,19 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
         const uint32_t pl = lds0 + stage * (PB + QB), ql = pl + PB;
         if (v < nk) {
             next_slice();
+            if (codes && v >= NST) {              // (the first NST tiles are written by the prologue)
+                store_qs(qr, stage);
+                load_qs(qr);
+            }
 #pragma unroll
             for (int i = 0; i < PI; ++i)
                 dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + po) : zero);
+            if (!codes) {
 #pragma unroll
-            for (int i = 0; i < QI; ++i)
-                dma16(ql + i * NW * 1024,
-                      (NN ? qrow(i) : qlc(i) * 8) < rem ? (const void *)(qptr[i] + qo) : zero);
+                for (int i = 0; i < QI; ++i)
+                    dma16(ql + i * NW * 1024,
+                          (NN ? qrow(i) : qlc(i) * 8) < rem ? (const void *)(qptr[i] + qo) : zero);
+            }
             advance();
             return;
         }
@@ -343,17 +451,34 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
 #pragma unroll
         for (int i = j * QI / n; i < (j + 1) * QI / n; ++i) dma16(pl + PB + i * NW * 1024, qptr[i] + qo);
     };
-    if (nk >= NST && rem >= NST * BK) {
+    // all but the NST - 1 youngest tiles' loads; a base tile of codes has fewer
+    auto wait_tile = [&](bool more) __attribute__((always_inline)) {
+        if (!more) wait_barrier<0>();
+        else if (codes) wait_barrier<(NST - 1) * (PI + NL)>();
+        else wait_barrier<(NST - 1) * (PI + QI)>();
+    };
+    if (codes) {
+        Pieces first[NST];
+        for (int i = 0; i < NST; ++i)
+            if (i < nv) issue(i, i);
+#pragma unroll
+        for (int i = 0; i < NST; ++i) load_qs(first[i]);
+        load_qs(qr);
+#pragma unroll
+        for (int i = 0; i < NST; ++i)
+            if (i < nk) store_qs(first[i], i);
+        wait_barrier<0>();
+    } else if (nk >= NST && rem >= NST * BK) {
         for (int i = 0; i < NST; ++i) {
             loads(lds0 + i * (PB + QB), 0, 1);
             advance();
         }
+        wait_tile(true);
     } else {
         for (int i = 0; i < NST; ++i)
             if (i < nv) issue(i, i);
+        wait_tile(nv >= NST);
     }
-    if (nv >= NST) wait_barrier<(NST - 1) * (PI + QI)>();
-    else wait_barrier<0>();
     for (int v = 0; v < nv; ++v) {
         // Fast tiles: tile v's DMA slot takes a whole base tile, v + NST.
         next_slice();
@@ -382,7 +507,53 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
             constexpr int M3 = M * 3 / 4;                 // MFMAs beside the second half's reads
 #pragma unroll
             for (int i = 0; i < RD; ++i) read1(0, stage_ptr(v), 0, i);
-            do {
+            // beside the MFMAs once a stage is free: the codes in registers to the
+            // stage, the next tile's codes, P's DMA
+            constexpr int SU = HB / 4, CI = NQ * SU + NQ + PI;
+            auto refill1 = [&](uint32_t pl, int stage, int i) __attribute__((always_inline)) {
+                if (i < NQ * SU) {
+                    store_q(qr, stage, i / SU, i % SU);
+                } else if (i < NQ * SU + NQ) {
+                    if (i == NQ * SU) begin_q();
+                    load_q(qr, i - NQ * SU);
+                    if (i == NQ * SU + NQ - 1) end_q();
+                } else {
+                    const int p = i - NQ * SU - NQ;
+                    dma16(pl + p * NW * 1024, pptr[p] + po);
+                }
+            };
+            if (codes) do {
+                const char *st = stage_ptr(v);
+                const int stage = v % NST;
+                const uint32_t pl = lds0 + stage * (PB + QB);
+#pragma unroll
+                for (int n = 0; n < M; ++n) {
+                    if (n < M1) {
+#pragma unroll
+                        for (int i = n * RD / M1; i < (n + 1) * RD / M1; ++i) read1(1, st, 1, i);
+                    } else {
+                        if (n == M1) meet_reads();
+#pragma unroll
+                        for (int i = (n - M1) * CI / M2; i < (n - M1 + 1) * CI / M2; ++i) refill1(pl, stage, i);
+                    }
+                    mfma1(0, n);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                advance();
+                ++v;
+                wait_tile(true);
+                const char *nx = stage_ptr(v);
+#pragma unroll
+                for (int n = 0; n < M; ++n) {
+                    if (n < M3) {
+#pragma unroll
+                        for (int i = n * RD / M3; i < (n + 1) * RD / M3; ++i) read1(0, nx, 0, i);
+                    }
+                    mfma1(1, n);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } while (v + NST < nk && rem >= BK);
+            else do {
                 const char *st = stage_ptr(v);
                 const uint32_t pl = lds0 + (v % NST) * (PB + QB);
                 // first half: the stage's second fragment set, after which the
@@ -458,8 +629,7 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
             }
         }
         // tile v + 1 has landed
-        if (v + NST < nv) wait_barrier<(NST - 1) * (PI + QI)>();
-        else wait_barrier<0>();
+        wait_tile(v + NST < nv);
     }
 
     // 16-token blocks that hold several slots: each slot's part from global
@@ -602,6 +772,15 @@ __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(Lin
                     __builtin_bit_cast(unsigned long, v[i]),
                     reinterpret_cast<unsigned long *>(a.out + (int64_t)tok[i] * a.ldo + obase + c0 + cl));
     }
+}
+
+template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED, bool MX>
+__global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
+    __shared__ TileLds<BM, BN, NST> sh;
+    const TileAt at = tile_at(a);
+    if (!MX) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQRows>(a, sh, at.mt, at.nt);
+    else if (MIXED && at.nt >= a.base_tiles) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQVectors>(a, sh, at.mt, at.nt);
+    else lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQCodes>(a, sh, at.mt, at.nt);
 }
 
 // Rank vectors of a small batch: u[t][j] = sum_k x[t][k] A[i][j][k] with no
@@ -1334,8 +1513,8 @@ int column_tiles(LinArgs &a, int b) {
     return c;
 }
 
-template <int BM, int BN, int WM, int WN, int NST, bool MIXED>
-hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
+template <int BM, int BN, int WM, int WN, int NST, bool MIXED, bool MX>
+hipError_t run_tile_of(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     a.m_tiles = (a.T + BM - 1) / BM;
     a.base_tiles = a.n_tiles = gradient ? (a.K + BN - 1) / BN : column_tiles(a, BN);
     a.ksp = ksp;
@@ -1351,8 +1530,8 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     }
     if (ksp == 1 && !a.join_delta) a.part = nullptr;
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
-    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED>), grid, block, 0, st, a);
+    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED, MX>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED, MX>), grid, block, 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     const dim3 rows((unsigned)((cols + 511) / 512), (unsigned)a.T);
@@ -1364,6 +1543,12 @@ hipError_t run_tile(LinArgs a, bool gradient, int ksp, hipStream_t st) {
         hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols),
                                             (unsigned)((a.T + kJoinRows - 1) / kJoinRows)), dim3(256), 0, st, a);
     return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int NST, bool MIXED>
+hipError_t run_tile(const LinArgs &a, bool gradient, int ksp, hipStream_t st) {
+    return a.ws ? run_tile_of<BM, BN, WM, WN, NST, MIXED, true>(a, gradient, ksp, st)
+                : run_tile_of<BM, BN, WM, WN, NST, MIXED, false>(a, gradient, ksp, st);
 }
 
 template <int CT, int NRB, int U>

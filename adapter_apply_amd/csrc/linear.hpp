@@ -13,7 +13,9 @@ struct LinArgs {
     const uint16_t *p;        // x [T][ldp], or dy (whole 8-element units per slice)
     int64_t ldp;
     const uint16_t *w;        // the projection [sum N][ldw]; null: no base product
-    int64_t ldw;
+    int64_t ldw;              // elements, of a microscaled projection bytes
+    const uint8_t *ws;        // its scales (w are LORA_MX_FP4 codes), or null
+    int64_t ldws;
     const uint16_t *bias;     // [sum N] or null (forward)
     uint16_t *out;
     int64_t ldo;
