@@ -20,6 +20,17 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kXcds = 8;
 
+// f(B), .., f(E - 1), each with its index as a constant (loops of this many steps are
+// past what the compiler unrolls).
+template <int I> struct Index { static constexpr int value = I; };
+template <int B, int E, typename F>
+__device__ __forceinline__ void each(const F &f) {
+    if constexpr (B < E) {
+        f(Index<B>());
+        each<B + 1, E>(f);
+    }
+}
+
 __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_cast(bf16x8_t, u); }
 
 // Tile GEMM.  Work-group = BM tokens x BN output columns, WM x WN waves.  A
@@ -53,9 +64,12 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // per K tile of 256 x 256, 1.0 at the dense peak of a 2.1 GHz clock).  Small batches
 // are bound by L2: 256 tokens, 4096 x 6144 request 280 MB there in 25 us.
 //
-// kQCodes: the projection's Q rows are 4-bit codes.  A thread loads its share of a tile
-// one tile ahead of the DMA into registers and writes it to the stage as bf16, in
-// the DMA's layout, when the stage is free; everything past the stage is the same.
+// kQCodes: the projection's Q rows are 4-bit codes.  Forward: the stage holds the codes
+// and their scales, and a wave converts its fragments between the MFMAs (a pair of
+// values an instruction).  Gradient, whose transposed reads take 16-bit values and
+// whose scales run along the contraction: a thread loads its share of a tile one tile
+// ahead of the DMA into registers and writes it to the stage as bf16, in the DMA's
+// layout, when the stage is free; everything past the stage is the same.
 template <int BM, int BN, int NST>
 struct TileLds {
     __attribute__((aligned(16))) char stage[NST * (BM + BN) * 128];
@@ -253,29 +267,51 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     const void *zero = g_zero16;
     const uint32_t lds0 = lds_addr(s_stage) + w * 1024;
 
-    // kQCodes: a thread's NQ pieces of a tile, HB code bytes each (a block of 32 or half
+    constexpr bool codes = Q == kQCodes, staged = codes && NN, direct = codes && !NN;
+    // direct: QC instructions of codes (32 bytes a row) and one of 4 blocks' scales a
+    // row, of which two tiles in turn take two each.  Fewer rows than a work-group's
+    // instructions cover are loaded twice, to the same place.
+    constexpr int QC = BN / 32 / NW > 0 ? BN / 32 / NW : 1, SB = BN * 32;      // scales behind the codes
+    static_assert(!direct || QC + 1 <= QI, "a base tile issues no more loads than a rank-vector tile");
+    const uint8_t *cptr[QC], *sptr = nullptr;
+    if (direct) {
+        auto row = [&](int r) { return a.off[sc] + min(c0 + r, cend - 1); };
+#pragma unroll
+        for (int i = 0; i < QC; ++i)
+            cptr[i] = reinterpret_cast<const uint8_t *>(a.w) + row((i * NW + w) % (BN / 32) * 32 + lane / 2) * a.ldw +
+                      (lane & 1) * 16;
+        sptr = a.ws + row((w * 64 + lane) % BN) * a.ldws;
+    }
+    int ktile = 0;                                // direct: the next base tile to load
+    auto code1 = [&](uint32_t ql0, int i, const void *from) __attribute__((always_inline)) {
+        dma16(ql0 + (i * NW + w) % (BN / 32) * 1024, from);
+    };
+    auto scales1 = [&](uint32_t ql0) __attribute__((always_inline)) {
+        dma4(ql0 + SB + (w * 64) % BN * 4, sptr + (ktile >> 1) * 4);
+    };
+    const uint32_t stage0 = lds_addr(s_stage);
+
+    // staged: a thread's NQ pieces of a tile, HB code bytes each (a block of 32 or half
     // of one), as rows and blocks such that the 8 lanes of one LDS write hit
     // different banks; pieces past the contraction's end read zeros (code 0, scale 0).
     constexpr int NT = NW * 64, HB = 2 * BN >= NT ? 16 : 8, NQ = BN * 32 / (NT * HB), NL = 2 * NQ;
     struct Pieces { uint4 c[NQ]; uint32_t s[NQ]; };
     const uint8_t *qcode[NQ], *qscale[NQ];
     int qrow_of[NQ], qunit[NQ];                   // the piece's row and first 16-byte unit in the stage
-    int q_cs = NN ? sc : 0;
-    int64_t q_rem = 0, q_at = 0;                  // steps left, first row (NN) or K tile
-    constexpr bool codes = Q == kQCodes;
-    static_assert(!codes || NL <= QI, "a base tile issues no more loads than a rank-vector tile");
-    if (codes) {
+    int q_cs = sc;
+    int64_t q_rem = 0, q_at = 0;                  // rows left in the slice, first row
+    static_assert(!staged || NL <= QI, "a base tile issues no more loads than a rank-vector tile");
+    if (staged) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             const int b = i * NT + tid;
             int row, blk, half = 0;
-            if (NN && BN == 256) {
+            if (BN == 256) {
                 blk = (b & 3) | ((b >> 3) & 1) << 2;
                 row = ((b >> 2) & 1) | b >> 4 << 1;
             } else if (HB == 16) {
-                constexpr int BPR = NN ? BN / 32 : 2;
-                blk = b % BPR;
-                row = b / BPR;
+                blk = b % (BN / 32);
+                row = b / (BN / 32);
             } else {
                 half = b & 1;
                 blk = (b >> 1) & 1;
@@ -283,17 +319,15 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
             }
             qrow_of[i] = row;
             qunit[i] = blk * 4 + half * 2;
-            int64_t n = row;
-            if (!NN) n = a.off[sc] + min(c0 + row, cend - 1);
-            else blk = (c0 >> 5) + blk < (a.K + 31) >> 5 ? (int)(c0 >> 5) + blk : 0;
-            qcode[i] = reinterpret_cast<const uint8_t *>(a.w) + n * a.ldw + blk * 16 + half * 8;
-            qscale[i] = a.ws + n * a.ldws + blk;
+            blk = (c0 >> 5) + blk < (a.K + 31) >> 5 ? (int)(c0 >> 5) + blk : 0;
+            qcode[i] = reinterpret_cast<const uint8_t *>(a.w) + row * a.ldw + blk * 16 + half * 8;
+            qscale[i] = a.ws + row * a.ldws + blk;
         }
     }
     auto load_q = [&](Pieces &r, int i) __attribute__((always_inline)) {
-        const bool in = (NN ? qrow_of[i] : qunit[i] * 8) < q_rem;
-        const void *c = in ? (const void *)(qcode[i] + q_at * (NN ? a.ldw : 32)) : (const void *)g_zero16;
-        const uint8_t *s = in ? qscale[i] + q_at * (NN ? a.ldws : 2) : reinterpret_cast<const uint8_t *>(g_zero16);
+        const bool in = qrow_of[i] < q_rem;
+        const void *c = in ? (const void *)(qcode[i] + q_at * a.ldw) : (const void *)g_zero16;
+        const uint8_t *s = in ? qscale[i] + q_at * a.ldws : reinterpret_cast<const uint8_t *>(g_zero16);
         if (HB == 16) {
             r.c[i] = *static_cast<const uint4 *>(c);
         } else {
@@ -303,11 +337,10 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
         r.s[i] = *s;
     };
     auto begin_q = [&]() {                        // the next tile's slice
-        if (NN && q_rem <= 0 && q_cs + 1 < a.S) q_rem = a.n[++q_cs];
+        if (q_rem <= 0 && q_cs + 1 < a.S) q_rem = a.n[++q_cs];
     };
     auto end_q = [&]() {
-        if (NN) q_at += q_rem < BK ? (q_rem > 0 ? q_rem : 0) : BK;
-        else ++q_at;
+        q_at += q_rem < BK ? (q_rem > 0 ? q_rem : 0) : BK;
         q_rem -= BK;
     };
     auto load_qs = [&](Pieces &r) __attribute__((always_inline)) {
@@ -343,7 +376,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
             qo = a.off[cs] * a.ldw;
         }
     };
-    auto advance = [&]() { rem -= BK; po += BK; qo += qstep; };
+    auto advance = [&]() { rem -= BK; po += BK; qo += qstep; ++ktile; };
     if (MIXED && k0 && nk > 0) {
         if (NN && !vec)
             for (; (int64_t)k0 * BK >= a.n[cs]; ++cs) k0 -= (int)((a.n[cs] + BK - 1) / BK);
@@ -351,11 +384,12 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
         po = (NN ? a.poff[cs] : 0) + (int64_t)k0 * BK;
         qo = NN ? ((vec ? 0 : a.off[cs]) + (int64_t)k0 * BK) * ldq : (int64_t)k0 * BK;
     }
-    if (codes) {
+    if (staged) {
         q_cs = cs;
         q_rem = rem;
-        q_at = NN ? a.off[cs] + (a.n[cs] - rem) : (a.K - rem) / BK;
+        q_at = a.off[cs] + (a.n[cs] - rem);
     }
+    if (direct) ktile = k0;
     auto issue = [&](int v, int stage) {
         // recomputed here each time: hoisted lane values would crowd the
         // registers of the fast loop
@@ -367,13 +401,20 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
         const uint32_t pl = lds0 + stage * (PB + QB), ql = pl + PB;
         if (v < nk) {
             next_slice();
-            if (codes && v >= NST) {              // (the first NST tiles are written by the prologue)
+            if (staged && v >= NST) {             // (the first NST tiles are written by the prologue)
                 store_qs(qr, stage);
                 load_qs(qr);
             }
 #pragma unroll
             for (int i = 0; i < PI; ++i)
                 dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + po) : zero);
+            if (direct) {
+                const uint32_t ql0 = stage0 + stage * (PB + QB) + PB;
+#pragma unroll
+                for (int i = 0; i < QC; ++i)
+                    code1(ql0, i, (lane & 1) * 32 < rem ? (const void *)(cptr[i] + ktile * 32) : zero);
+                scales1(ql0);
+            }
             if (!codes) {
 #pragma unroll
                 for (int i = 0; i < QI; ++i)
@@ -426,9 +467,19 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
         for (int j = 0; j < MB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     const int g = lane >> 4, l16 = lane & 15;
+    // The 8 contraction steps of a lane's fragment kk: direct, the two halves of the 16
+    // whose codes it reads at once.
+    auto unit = [&](int kk) { return direct ? 2 * g + kk : kk * 4 + g; };
     auto pfrag = [&](const char *st, int mb, int kk) {
         const int row = (wm * MB + mb) * 16 + l16;
-        return frag(*reinterpret_cast<const uint4 *>(st + row * (BK * 2) + (((kk * 4 + g) ^ pswz(row)) << 4)));
+        return frag(*reinterpret_cast<const uint4 *>(st + row * (BK * 2) + ((unit(kk) ^ pswz(row)) << 4)));
+    };
+    auto qcodes = [&](const char *st, int nb) {
+        return *reinterpret_cast<const uint2 *>(st + PB + ((wn * NB + nb) * 16 + l16) * 32 + g * 8);
+    };
+    auto qscale1 = [&](const char *st, int nb, int kt) {
+        return (uint32_t)*reinterpret_cast<const uint8_t *>(st + PB + SB + ((wn * NB + nb) * 16 + l16) * 4 + (kt & 1) * 2 +
+                                                            (g >> 1));
     };
     auto qfrag = [&](const char *st, int nb, int kk) {
         if (NN) {
@@ -439,7 +490,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
             return frag(make_uint4(x0.x, x0.y, x1.x, x1.y));
         }
         const int row = (wn * NB + nb) * 16 + l16;
-        return frag(*reinterpret_cast<const uint4 *>(st + PB + row * (BK * 2) + (((kk * 4 + g) ^ pswz(row)) << 4)));
+        return frag(*reinterpret_cast<const uint4 *>(st + PB + row * (BK * 2) + ((unit(kk) ^ pswz(row)) << 4)));
     };
     auto stage_ptr = [&](int v) { return s_stage + (v % NST) * (PB + QB); };
     auto meet_reads = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
@@ -454,10 +505,10 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     // all but the NST - 1 youngest tiles' loads; a base tile of codes has fewer
     auto wait_tile = [&](bool more) __attribute__((always_inline)) {
         if (!more) wait_barrier<0>();
-        else if (codes) wait_barrier<(NST - 1) * (PI + NL)>();
+        else if (codes) wait_barrier<(NST - 1) * (PI + (NN ? NL : QC + 1))>();
         else wait_barrier<(NST - 1) * (PI + QI)>();
     };
-    if (codes) {
+    if (staged) {
         Pieces first[NST];
         for (int i = 0; i < NST; ++i)
             if (i < nv) issue(i, i);
@@ -468,7 +519,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
         for (int i = 0; i < NST; ++i)
             if (i < nk) store_qs(first[i], i);
         wait_barrier<0>();
-    } else if (nk >= NST && rem >= NST * BK) {
+    } else if (!codes && nk >= NST && rem >= NST * BK) {
         for (int i = 0; i < NST; ++i) {
             loads(lds0 + i * (PB + QB), 0, 1);
             advance();
@@ -505,8 +556,10 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
             constexpr int M1 = M / 4;                     // MFMAs beside the first half's reads
             constexpr int M2 = M - M1;                    // and its DMA
             constexpr int M3 = M * 3 / 4;                 // MFMAs beside the second half's reads
+            if (!direct) {
 #pragma unroll
-            for (int i = 0; i < RD; ++i) read1(0, stage_ptr(v), 0, i);
+                for (int i = 0; i < RD; ++i) read1(0, stage_ptr(v), 0, i);
+            }
             // beside the MFMAs once a stage is free: the codes in registers to the
             // stage, the next tile's codes, P's DMA
             constexpr int SU = HB / 4, CI = NQ * SU + NQ + PI;
@@ -522,7 +575,123 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                     dma16(pl + p * NW * 1024, pptr[p] + po);
                 }
             };
-            if (codes) do {
+            // direct: a tile's codes of both sets and their scales
+            uint2 qc[NB];
+            uint32_t qs[NB];
+            constexpr int RC = 2 * NB + MB;
+            // one instruction of fragment i / 4's conversion
+            uint32_t fu[2][NB][4];
+            auto convert1 = [&](int set, int i) __attribute__((always_inline)) {
+                const uint32_t c = set ? qc[i / 4].y : qc[i / 4].x;
+                const float sc = __uint_as_float(qs[i / 4]);
+                bf16x2_t r;
+                if (i % 4 == 0) r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 0);
+                else if (i % 4 == 1) r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 1);
+                else if (i % 4 == 2) r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 2);
+                else r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 3);
+                fu[set][i / 4][i % 4] = __builtin_bit_cast(uint32_t, r);
+                if (i % 4 == 3)
+                    fq[set][i / 4] = frag(make_uint4(fu[set][i / 4][0], fu[set][i / 4][1], fu[set][i / 4][2], fu[set][i / 4][3]));
+            };
+            // the scale of a fragment to a float's exponent, then the first set's conversions
+            auto scale1 = [&](int i) __attribute__((always_inline)) {
+                if (i % 5 == 0) qs[i / 5] <<= 23;
+                else convert1(0, i / 5 * 4 + i % 5 - 1);
+            };
+            if (direct) {
+                // Loop-carried addresses (opaque: else the compiler keeps two sets and
+                // advances one at the loop's end, a clump), LDS addresses of a lane's
+                // first row.
+                const uint16_t *pp[PI];
+                const uint8_t *cp[QC];
+#pragma unroll
+                for (int i = 0; i < PI; ++i) pp[i] = pptr[i] + po;
+#pragma unroll
+                for (int i = 0; i < QC; ++i) cp[i] = cptr[i] + ktile * 32;
+                const int c_row = PB + (wn * NB * 16 + l16) * 32 + g * 8, s_row = PB + SB + (wn * NB * 16 + l16) * 4 + (g >> 1);
+                const int p_row = (wm * MB * 16 + l16) * (BK * 2);
+                int fast = min(nk - NST - v, (int)(rem / BK));
+                auto read_p = [&](int set, int st, int i) __attribute__((always_inline)) {
+                    fp[set][i] = frag(*reinterpret_cast<const uint4 *>(
+                        s_stage + (st + p_row + ((unit(set) ^ pswz(l16)) << 4)) + i * 16 * BK * 2));
+                };
+                // item i of a tile's first reads: codes and scales in turn, P fragments
+                auto read_first = [&](int st, int sst, int i) __attribute__((always_inline)) {
+                    if (i >= 2 * NB) read_p(0, st, i - 2 * NB);
+                    else if (i % 2) qs[i / 2] = (uint8_t)*(s_stage + (sst + s_row) + i / 2 * 64);
+                    else qc[i / 2] = *reinterpret_cast<const uint2 *>(s_stage + (st + c_row) + i / 2 * 512);
+                };
+                // item i of the DMA that a free stage takes
+                constexpr int LC = PI + QC + 1;
+                auto dma1 = [&](uint32_t at, int i) __attribute__((always_inline)) {
+                    if (i < PI) dma16(at + w * 1024 + i * NW * 1024, pp[i]);
+                    else if (i < PI + QC) code1(at + PB, i - PI, cp[i - PI]);
+                    else scales1(at + PB);
+                };
+                auto next1 = [&](int i) __attribute__((always_inline)) {
+                    if (i < PI) {
+                        pp[i] += BK;
+                        asm volatile("" : "+v"(pp[i]));
+                    } else if (i < PI + QC) {
+                        cp[i - PI] += 32;
+                        asm volatile("" : "+v"(cp[i - PI]));
+                    }
+                };
+                auto at_of = [&](int v) { return (v % NST) * (PB + QB); };
+                // Slots between the MFMAs of a half: about three instructions each.
+                constexpr bool WIDE = M >= 64;
+                constexpr int MR = WIDE ? M * 3 / 8 : M / 2, MC = WIDE ? MR : M / 2;
+#pragma unroll
+                for (int i = 0; i < RC; ++i) read_first(at_of(v), at_of(v) + ((k0 + v) & 1) * 2, i);
+#pragma unroll
+                for (int i = 0; i < 5 * NB; ++i) scale1(i);
+                do {
+                    const int st = at_of(v);
+                    const uint32_t at = stage0 + st;
+                    // first half: P's second fragments, the codes' from registers, and once
+                    // the stage is free its DMA
+                    each<0, M>([&](auto slot) __attribute__((always_inline)) {
+                        constexpr int n = decltype(slot)::value;
+                        if constexpr (n < M1)
+                            each<n * MB / M1, (n + 1) * MB / M1>(
+                                [&](auto i) __attribute__((always_inline)) { read_p(1, st, i.value); });
+                        if constexpr (n == M1) meet_reads();
+                        if constexpr (WIDE) {
+                            constexpr int D = (n - M1 - 1) / 4;       // DMA in every fourth slot, its next address two on
+                            if constexpr (n > M1 && (n - M1 - 1) % 4 == 0 && D < LC) dma1(at, D);
+                            if constexpr (n > M1 && (n - M1 - 1) % 4 == 2 && D < LC) next1(D);
+                            if constexpr (n < M1 ? n % 2 == 1 : n % 2 == 0) convert1(1, n / 2);
+                        } else {
+                            if constexpr (n >= M1)
+                                each<(n - M1) * LC / M2, (n - M1 + 1) * LC / M2>([&](auto i) __attribute__((always_inline)) {
+                                    dma1(at, i.value);
+                                    next1(i.value);
+                                });
+                            each<n * 4 * NB / M, (n + 1) * 4 * NB / M>(
+                                [&](auto i) __attribute__((always_inline)) { convert1(1, i.value); });
+                        }
+                        mfma1(0, n);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                    advance();
+                    ++v;
+                    wait_tile(true);
+                    // second half: the next tile's codes, scales and first P fragments, its
+                    // first conversions
+                    const int nx = at_of(v), nxs = nx + ((k0 + v) & 1) * 2;
+                    each<0, M>([&](auto slot) __attribute__((always_inline)) {
+                        constexpr int n = decltype(slot)::value;
+                        if constexpr (n < MR)
+                            each<n * RC / MR, (n + 1) * RC / MR>(
+                                [&](auto i) __attribute__((always_inline)) { read_first(nx, nxs, i.value); });
+                        if constexpr (n >= MC)
+                            each<(n - MC) * 5 * NB / (M - MC), (n - MC + 1) * 5 * NB / (M - MC)>(
+                                [&](auto i) __attribute__((always_inline)) { scale1(i.value); });
+                        mfma1(1, n);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                } while (--fast > 0);
+            } else if (staged) do {
                 const char *st = stage_ptr(v);
                 const int stage = v % NST;
                 const uint32_t pl = lds0 + stage * (PB + QB);
@@ -596,7 +765,17 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) q[kk][i] = qfrag(st, i, kk);
+            for (int i = 0; i < NB; ++i) {
+                if (direct && base) {
+                    // (scales past the row's blocks may be anything)
+                    const int kt = k0 + v;
+                    const uint32_t s = kt * BK + (g >> 1) * kMxBlock < a.K ? qscale1(st, i, kt) : 0u;
+                    const uint2 c = qcodes(st, i);
+                    q[kk][i] = frag(mx_fp4_bf16(kk ? c.y : c.x, s << 23));
+                } else {
+                    q[kk][i] = qfrag(st, i, kk);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < MB; ++j) p[kk][j] = pfrag(st, j, kk);
         }
