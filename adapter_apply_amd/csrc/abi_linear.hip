@@ -29,12 +29,19 @@ struct LinWs {
     size_t part;        // fp32 partial sums
     size_t pad;         // bf16 [T][pad_cols]: dy with slices of whole 8-element units
     size_t w16;         // bf16 [sum N][K]: the projection restored from 4 bits
-    size_t x16;         // bf16 [T][K]: x restored from 8 bits
     size_t data;        // end of the call's own regions
     size_t end;
     bool padded;        // some N_s % 8: dy goes through pad
     int64_t pad_cols;
 };
+
+constexpr size_t kMxCountBytes = 4096;
+
+// Whether a gradient through a 4-bit projection that is not wide takes the 256 x 256
+// tiles, which read it restored.
+bool lin_restores(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
+    return T > 0 && lin_tile_plan(T, K, N, S, R, L, true, false, false, true).tile == 256;
+}
 
 LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool mx = false) {
     LinWs w{};
@@ -74,6 +81,14 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
     size_t sums = kLinMaxSplits * (size_t)T * 2 * cols;     // (wide batches: up to as many columns more)
     if (sums > (size_t)kLinJoinMax) sums = (size_t)kLinJoinMax;
     if (4 * sums > part) part = 4 * sums;
+    if (mx && T > 0) {
+        // a few tokens' sums (fewer tokens of a larger batch's workspace among them)
+        size_t n = 0;
+        for (int s = 0; s < S; ++s) n += (size_t)N[s];
+        const size_t t = T < kMxFewTokens ? T : kMxFewTokens;
+        const size_t few = 4 * (kLinMaxSplits * t > kMxOneSplits ? kLinMaxSplits * t : kMxOneSplits) * (n + S * R);
+        if (n <= (size_t)kMxFewCols && few > part) part = few;
+    }
     o = align256(o + part);
     w.pad = o;
     for (int s = 0; s < S; ++s) {
@@ -81,11 +96,10 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         w.pad_cols += round8(N[s]);
     }
     if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
-    if (mx) {
+    if (mx && lin_restores(T, K, N, S, R, L)) {
         size_t n = 0;
         for (int s = 0; s < S; ++s) n += (size_t)N[s];
         w.w16 = o; o = align256(o + sizeof(uint16_t) * n * K);
-        w.x16 = o; o = align256(o + sizeof(uint16_t) * (size_t)T * K);
     }
     w.data = o;
     w.end = o + seg_x_bytes(kSegOneMaxWg * kSegThreads, kMaxSlots) + 256;
@@ -167,16 +181,18 @@ lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t 
     const Slices sl = make_slices(A, B, N, S, 0);
     uint16_t *hl = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
     int32_t *order = nullptr;
-    const bool direct = lin_direct(T, K, N, S, R, L);
+    // (a few tokens on 4 bits take their own kernels or the wide tiles, never lin_few)
+    const bool few = mx && mx_few(T, N, S, R, L);
+    const bool direct = few || lin_direct(T, K, N, S, R, L);
     const bool join = direct || lin_join_delta(T, K, N, S, R, L);
-    const bool wide = direct && lin_wide(T, K, N, S, R, L);
+    const bool wide = few || (direct && lin_wide(T, K, N, S, R, L));
     float *u = buf, *u_out = nullptr;
     // fp32 rank vectors by token, in buf if it is wanted
     if (join && !u) u = reinterpret_cast<float *>(wp + wl.hl_u);
-    if (lin_one(T, K, N, S, R) || wide) {
+    if (wide || (!mx && lin_one(T, K, N, S, R))) {
         u_out = buf;
     } else if (direct) {
-        if (!lin_few(T, K, N, S, R, L) && lin_grouped(T, K, R, L)) {
+        if ((mx || !lin_few(T, K, N, S, R, L)) && lin_grouped(T, K, R, L)) {
             float *part = reinterpret_cast<float *>(wp + wl.part);
             CHECK(launched(launch_grp_shrink(x, ldx, T, K, sl, S, L, R, idx, slot_rank, part, nullptr, nullptr, st)));
             CHECK(launched(launch_grp_reduce(T, S, L, R, idx, slot_rank, part, grp_kchunks(K), u, nullptr, st)));
@@ -195,7 +211,6 @@ lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t 
         const LinVectors v{part, nsp, nullptr, join ? nullptr : hl, kLinPartsFwd, join ? u : buf};
         CHECK(launched(launch_lin_vectors(&v, 1, T, S, L, R, idx, slot_rank, scale, seg, order, st)));
     }
-    if (mx && lin_few(T, K, N, S, R, L)) CHECK(launched(restore(W, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
     LinArgs a{};
     a.p = static_cast<const uint16_t *>(x); a.ldp = ldx;
     a.w = static_cast<const uint16_t *>(W.p); a.ldw = W.ld;
@@ -213,7 +228,11 @@ lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t 
         a.n[s] = N[s];
         a.off[s] = sl.off[s];
     }
-    return launched(launch_lin_gemm(a, false, st));
+    if (!few) return launched(launch_lin_gemm(a, false, st));
+    // (counts among the exchange region's bytes, which are zero between calls)
+    static_assert(sizeof(int32_t) * kMxCounts <= kMxCountBytes, "counts");
+    char *counts = wp + err_word_offset(ws_bytes) - kMxCountBytes;
+    return launched(launch_mx_few(a, reinterpret_cast<int32_t *>(counts), st));
 }
 
 // lora_linear_backward and, mx, lora_linear_mx_backward.
@@ -262,15 +281,25 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
 
     char *wp = static_cast<char *>(ws);
     const Slices sl = make_slices(A, B, N, S, 0);
-    if (X.p && X.scales && dA) CHECK(launched(restore(X, T, K, LORA_MX_INT8, wp + wl.x16, st)));
     const void *x = X.p, *W = dx ? Wm.p : nullptr;
-    const int64_t ldx = X.ld, ldw = Wm.ld;
+    const int64_t ldx = X.ld;
+    int64_t ldw = Wm.ld;
     const SegPtrs seg = lin_seg(ws, ws_bytes, wl, T, L);
     uint16_t *hl_u = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
     uint16_t *hl_v = reinterpret_cast<uint16_t *>(wp + wl.hl_v);
     float *part = reinterpret_cast<float *>(wp + wl.part);
     int32_t *order = reinterpret_cast<int32_t *>(wp + wl.order);
     const bool wide = dx && W && lin_wide_gradient(T, K, N, S, R, L, dA || dB);
+    // The largest gradient tiles read a restored projection: their transposed reads of
+    // codes cost more than restoring them once (us for dx: 2048 tokens, 4096 x 14336 256
+    // and 283, 4096 tokens, 6144 x 4096 216 and 246, 8192 tokens, 28672 x 4096 1700 and
+    // 2013; with 128 x 128 tiles the other way: 512 tokens, 6144 x 4096 70 and 58, 1024
+    // tokens, 28672 x 4096 351 and 301).
+    if (W && Wm.scales && !wide && lin_restores(T, K, N, S, R, L)) {
+        CHECK(launched(restore(Wm, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
+        W = Wm.p;
+        ldw = Wm.ld;
+    }
     if (!(flags & LORA_FLAG_SEGMENTS_READY) && (dA || dB || !wide))
         CHECK(launched(launch_segments(idx, slot_rank, T, L, R, seg, st)));
 
@@ -341,6 +370,7 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
         wa.accumulate = (flags & LORA_FLAG_ACCUMULATE) != 0;
         wb = wa;
         wa.p = static_cast<const uint16_t *>(x); wa.ldp = ldx; wa.hl = hl_v;
+        wa.xs = X.scales; wa.ldxs = X.lds;
         wb.p = p; wb.ldp = ldp; wb.hl = hl_u;
         for (int s = 0; s < S; ++s) {
             wa.out[s] = dA ? dA[s] : nullptr;

@@ -1528,12 +1528,11 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
     const int rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
     if (NN || a.wide) {
         __shared__ __attribute__((aligned(16))) float s_u[kLinWideRanks];
-        const int LR = a.L * a.R;
         for (int q = threadIdx.x; q < a.S * a.R; q += 256) {
             const int s = q / a.R, j = q - s * a.R;
             float u = 0.f;
             if (j < rank) {
-                const float *p = pt + a.cols + s * LR + slot * a.R + j;
+                const float *p = pt + a.cols + s * a.u_slice + slot * a.u_slot + j;
                 float w[kLinMaxSplits];
 #pragma unroll
                 for (int k = 0; k < kLinMaxSplits; ++k)
@@ -1705,19 +1704,19 @@ hipError_t run_tile_of(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     a.cols = a.part_ld = cols;
     if (a.wide) {
         a.part_ld += (int64_t)a.S * a.L * a.R;
+        a.u_slice = a.L * a.R;
+        a.u_slot = a.R;
         a.n_tiles += a.S * ((a.L * a.R + BN - 1) / BN);
     }
     if (ksp == 1 && !a.join_delta) a.part = nullptr;
     const dim3 grid((unsigned)(a.m_tiles * a.n_tiles), (unsigned)ksp), block(WM * WN * 64);
-    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED, MX>), grid, block, 0, st, a);
+    if (gradient) hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, true, MIXED, MX && MIXED>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_lin_tile<BM, BN, WM, WN, NST, false, MIXED, MX>), grid, block, 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    const dim3 rows((unsigned)((cols + 511) / 512), (unsigned)a.T);
+    if (a.join_delta && !gradient && !a.order) return launch_lin_join_rows(a, st);
     if (a.join_delta && gradient)
-        hipLaunchKernelGGL(k_lin_join_rows<true>, rows, dim3(256), 0, st, a);
-    else if (a.join_delta && !a.order)
-        hipLaunchKernelGGL(k_lin_join_rows<false>, rows, dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_lin_join_rows<true>, dim3((unsigned)((cols + 511) / 512), (unsigned)a.T), dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols),
                                             (unsigned)((a.T + kJoinRows - 1) / kJoinRows)), dim3(256), 0, st, a);
@@ -1830,15 +1829,24 @@ static_assert(2 * 256 * 128 * 128 <= kLinJoinMax && 3 * kLinEvenTiles * 128 * 12
 static_assert(2 * (kLinWideBytesB / 32) <= kLinJoinMax && 2 * (kLinWideBytesA / 32) <= kLinJoinMax &&
               kLinDirectBytesB / 32 <= kLinJoinMax, "unsplit sums");
 
+hipError_t launch_lin_join_rows(const LinArgs &a, hipStream_t st) {
+    const dim3 rows((unsigned)((a.cols + 511) / 512), (unsigned)a.T);
+    hipLaunchKernelGGL(k_lin_join_rows<false>, rows, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
-    if (!gradient && lin_one(a.T, a.K, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
-    if (!gradient && lin_few(a.T, a.K, a.n, a.S, a.R, a.L)) {
+    // (4-bit batches that lin_few would take: mx_few, or the tiles)
+    if (!gradient && !a.ws && lin_one(a.T, a.K, a.n, a.S, a.R)) return a.R <= 16 ? run_one<2, 1, 2>(a, st) : run_one<2, 2, 2>(a, st);
+    if (!gradient && !a.ws && lin_few(a.T, a.K, a.n, a.S, a.R, a.L)) {
         if (a.T <= 16) return run_few<1, 1, 4>(a, st);
         if (a.T <= 32) return run_few<2, 2, 4>(a, st);
         return run_few<4, 2, 2>(a, st);
     }
     const LinTilePlan p = lin_tile_plan(a.T, a.K, a.n, a.S, a.R, a.L, gradient, a.join_delta, a.wide, a.w != nullptr);
-    if (p.tile == 256) return run_tile<256, 256, 2, 2, 2, false>(a, gradient, 1, st);
+    // (a gradient's 4-bit projection is restored for these)
+    if (p.tile == 256) return gradient ? run_tile_of<256, 256, 2, 2, 2, false, false>(a, true, 1, st)
+                                       : run_tile<256, 256, 2, 2, 2, false>(a, false, 1, st);
     if (p.tile == 128) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, p.splits, st);
     return run_tile<64, 64, 2, 2, 2, true>(a, gradient, p.splits, st);
 }

@@ -33,6 +33,8 @@ struct LinArgs {
     const float *scale;
     int32_t wide;             // rank vectors of every slot, x A^T or dy B, as S L R further columns of part
     int32_t base_tiles;       // column tiles before those
+    int32_t u_slice, u_slot;  // wide: where a token's ranks are in its row past cols: slice s of
+                              // slot i starts at s u_slice + i u_slot
     float *buf;               // where u goes if it is wanted: k_lin_one, join of wide batches; of other
                               // batches the join only clears the rows of tokens without a slot
     const uint16_t *other[kMaxSlices];  // k_lin_one and wide: lora_a [L][R][K]; wide gradient: lora_b
@@ -47,6 +49,15 @@ struct LinArgs {
 };
 
 hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st);
+// The sums of a direct batch's splits (a.part, a.ksp), bias and delta, to a.out.
+hipError_t launch_lin_join_rows(const LinArgs &a, hipStream_t st);
+// A few tokens on a 4-bit projection (mx_few.hip).
+constexpr int64_t kMxFewCols = 65536;   // most columns of a token
+constexpr int kMxFewTokens = 32;        // most tokens
+bool mx_few(int32_t T, const int64_t *N, int32_t S, int32_t R, int32_t L);
+constexpr int kMxOneSplits = 16;        // most K splits of one token
+constexpr int kMxCounts = kMxFewCols / 128 + kMaxSlices;   // counts, zero between calls
+hipError_t launch_mx_few(LinArgs a, int32_t *count, hipStream_t st);
 constexpr int kLinFewTokens = 64;       // most tokens of k_lin_few
 constexpr int kLinMaxSplits = 8;
 bool lin_one(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R);
@@ -120,6 +131,8 @@ hipError_t launch_lin_du(const uint16_t *dy, int64_t lddy, const int64_t *poff, 
 struct LinWgArgs {
     const uint16_t *p;
     int64_t ldp;
+    const uint8_t *xs;         // p are LORA_MX_INT8 codes (ldp in bytes) with these scales, or null
+    int64_t ldxs;
     const uint16_t *hl;        // bf16 [S][T][3R]
     float *out[kMaxSlices];
     int64_t m[kMaxSlices];

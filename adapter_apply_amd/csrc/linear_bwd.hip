@@ -7,6 +7,7 @@
 // reach the MFMA through transposed LDS reads.  All sums are fp32, in a fixed
 // order (no atomics); splits are summed in order by a kernel of their own.
 #include "linear.hpp"
+#include "mx.hpp"
 
 namespace aa {
 
@@ -175,6 +176,42 @@ struct WgLds {
     int tok[kWgTokens];
 };
 
+// The sums of a work-group's tile to its gradient, or to its split's place.
+template <int RB, bool TRANSPOSED>
+__device__ __forceinline__ void wg_store(const LinWgArgs &a, int s, int slot, int64_t m0, int r0,
+                                         const floatx4_t (&acc)[2][RB / 16]) {
+    constexpr int NB = RB / 16;
+    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t M = a.m[s];
+    float *out = a.nsp > 1 ? a.part + (int64_t)blockIdx.z * a.part_stride + a.part_off[s] : a.out[s];
+    const bool add = a.accumulate && a.nsp == 1;
+    const int rank = a.slot_rank ? a.slot_rank[slot] : a.R;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            // TRANSPOSED: lane holds rank l16, columns 4 g..; else column l16, ranks 4 g..
+            const int64_t m = m0 + w * 32 + i * 16 + (TRANSPOSED ? 4 * g : l16);
+            const int r = r0 + j * 16 + (TRANSPOSED ? l16 : 4 * g);
+            if (m >= M || r >= a.R) continue;
+            const int64_t o = TRANSPOSED ? ((int64_t)slot * a.R + r) * M + m : ((int64_t)slot * M + m) * a.R + r;
+            floatx4_t *dst = reinterpret_cast<floatx4_t *>(out + o);
+            floatx4_t v = acc[i][j];
+            // ranks past the slot's own are zero, whatever the rows hold (an
+            // infinity times the zero rank vector is NaN)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (r + (TRANSPOSED ? 0 : q) >= rank) v[q] = 0.f;
+            if (add) {
+                const floatx4_t old = *dst;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += old[q];
+            }
+            *dst = v;
+        }
+}
+
 template <int RB, bool TRANSPOSED>
 __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgLds<RB> &sh) {
     constexpr int NP = kLinPartsBwd;
@@ -270,44 +307,132 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
         }
     }
 
-    float *out = a.nsp > 1 ? a.part + (int64_t)blockIdx.z * a.part_stride + a.part_off[s] : a.out[s];
-    const bool add = a.accumulate && a.nsp == 1;
-    const int rank = a.slot_rank ? a.slot_rank[slot] : a.R;
+    wg_store<RB, TRANSPOSED>(a, s, slot, m0, r0, acc);
+}
+
+// dA from 8-bit activations: the same tile and fragments, with x restored to bf16 on the
+// way to LDS.  A thread has its share of a stage in registers (16 codes of a token, of
+// one block, and the rank vectors' units), kWg8Depth stages ahead; all its loads are
+// the compiler's, which then waits for a stage's own only.
+constexpr int kWg8Depth = 2;
+template <int RB>
+__device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, WgLds<RB> &sh) {
+    constexpr int NP = kLinPartsBwd, TK = kWgStep;
+    constexpr int PB = TK * kWgCols * 2, QB = TK * RB * 2;
+    constexpr int CPP = kWgCols / 8, CPQ = RB / 8, NB = RB / 16;
+    constexpr int QU = NP * QB / 16, QL = (QU + 255) / 256;     // 16-byte units of a stage's rank vectors, loads a thread
+    int s = 0;
+    const int mt_all = bx / nrb, r0 = (bx - mt_all * nrb) * RB;
+    while (s + 1 < a.S && mt_all >= a.tile_start[s + 1]) ++s;
+    const int64_t m0 = (int64_t)(mt_all - a.tile_start[s]) * kWgCols, M = a.m[s];
+    const int slot = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int b = a.seg.slot_start[slot], e = a.seg.slot_start[slot + 1];
+    {
+        const int per = ((e - b + a.nsp - 1) / a.nsp + TK - 1) / TK * TK;
+        b = min(b + (int)blockIdx.z * per, e);
+        e = min(b + per, e);
+    }
+    const int hlr = NP * a.R;
+    const uint16_t *hl = a.hl + (int64_t)s * a.T * hlr;
+    const int prow = tid >> 3, pcol = (tid & 7) * 16;
+    const bool pin = m0 + pcol < M;
+    const uint8_t *xc = reinterpret_cast<const uint8_t *>(a.p) + (pin ? m0 + pcol : 0);
+    const uint8_t *xs = a.xs + (pin ? m0 + pcol : 0) / kMxBlock;
+
+    floatx4_t acc[2][NB];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            // TRANSPOSED: lane holds rank l16, columns 4 g..; else column l16, ranks 4 g..
-            const int64_t m = m0 + w * 32 + i * 16 + (TRANSPOSED ? 4 * g : l16);
-            const int r = r0 + j * 16 + (TRANSPOSED ? l16 : 4 * g);
-            if (m >= M || r >= a.R) continue;
-            const int64_t o = TRANSPOSED ? ((int64_t)slot * a.R + r) * M + m : ((int64_t)slot * M + m) * a.R + r;
-            floatx4_t *dst = reinterpret_cast<floatx4_t *>(out + o);
-            floatx4_t v = acc[i][j];
-            // ranks past the slot's own are zero, whatever the rows hold (an
-            // infinity times the zero rank vector is NaN)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (r + (TRANSPOSED ? 0 : q) >= rank) v[q] = 0.f;
-            if (add) {
-                const floatx4_t old = *dst;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += old[q];
+        for (int j = 0; j < NB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    struct Stage {
+        uint4 x, q[QL];
+        uint32_t scale;
+    };
+    for (int cb = b; cb < e; cb += kWgTokens) {
+        const int cnt = min(kWgTokens, e - cb), nst = (cnt + TK - 1) / TK;
+        __syncthreads();
+        for (int i = tid; i < cnt; i += 256) sh.tok[i] = a.seg.perm[cb + i];
+        __syncthreads();
+        auto load = [&](Stage &t, int v) __attribute__((always_inline)) {
+            {
+                const int64_t tok = sh.tok[min(v * TK + prow, cnt - 1)];
+                t.x = ldg<uint4>(xc + tok * a.ldp);
+                t.scale = xs[tok * a.ldxs];
             }
-            *dst = v;
-        }
+#pragma unroll
+            for (int i = 0; i < QL; ++i) {
+                const int u = i * 256 + tid, part = u / (QB / 16), row = u % (QB / 16) / CPQ, tk = v * TK + row;
+                const int j = r0 + u % CPQ * 8;
+                const bool in = u < QU && tk < cnt && j < a.R;
+                t.q[i] = ldg<uint4>(hl + (int64_t)sh.tok[in ? tk : 0] * hlr + (in ? part * a.R + j : 0));
+                if (!in) t.q[i] = make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto store = [&](const Stage &t, int v) __attribute__((always_inline)) {
+            char *st = sh.stage[v & 1];
+            // (a token past the count is a copy of the last, whose rank vector is zero:
+            // its values must be finite)
+            const bool in = pin && v * TK + prow < cnt;
+            const float unit = in ? mx_int8_unit(t.scale) : 0.f;
+            char *p = st + prow * (CPP * 16) + ((((tid & 7) * 2) ^ tr_swz<CPP>(prow)) << 4);
+            *reinterpret_cast<uint4 *>(p) = mx_int8_bf16(make_uint2(t.x.x, t.x.y), unit);
+            *reinterpret_cast<uint4 *>(p + 16) = mx_int8_bf16(make_uint2(t.x.z, t.x.w), unit);
+#pragma unroll
+            for (int i = 0; i < QL; ++i) {
+                const int u = i * 256 + tid, part = u / (QB / 16), row = u % (QB / 16) / CPQ;
+                if (u < QU)
+                    *reinterpret_cast<uint4 *>(st + PB + part * QB + row * (CPQ * 16) +
+                                               ((u % CPQ ^ tr_swz<CPQ>(row)) << 4)) = t.q[i];
+            }
+        };
+        Stage ring[kWg8Depth];
+#pragma unroll
+        for (int d = 0; d < kWg8Depth; ++d)
+            if (d < nst) load(ring[d], d);
+        for (int v0 = 0; v0 < nst; v0 += kWg8Depth)
+#pragma unroll
+            for (int d = 0; d < kWg8Depth; ++d) {
+                const int v = v0 + d;
+                if (v >= nst) break;
+                store(ring[d], v);
+                lds_barrier();
+                if (v + kWg8Depth < nst) load(ring[d], v + kWg8Depth);
+                const char *st = sh.stage[v & 1];
+#pragma unroll
+                for (int kk = 0; kk < TK / 32; ++kk) {
+                    bf16x8_t p[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) p[i] = tr_frag<CPP>(st, w * 32 + i * 16, kk, lane);
+#pragma unroll
+                    for (int h = 0; h < NP; ++h)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            const bf16x8_t q = tr_frag<CPQ>(st + PB + h * QB, j * 16, kk, lane);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[i], q, acc[i][j], 0, 0, 0);
+                        }
+                }
+            }
+    }
+    wg_store<RB, true>(a, s, slot, m0, r0, acc);
 }
 
 struct WgJobs {
     LinWgArgs a, b;      // dA (transposed), dB
     int32_t na, nrb;     // work-groups of a along x
 };
-template <int RB>
+template <int RB, bool X8>
 __global__ __launch_bounds__(256) void k_lin_wg(WgJobs j) {
     __shared__ WgLds<RB> sh;
     const int bx = blockIdx.x;
     if (bx < j.na) {
-        if ((int)blockIdx.z < j.a.nsp) wg_tile<RB, true>(j.a, j.nrb, bx, sh);
+        if ((int)blockIdx.z >= j.a.nsp) return;
+        if (X8) wg_tile8<RB>(j.a, j.nrb, bx, sh);
+        else wg_tile<RB, true>(j.a, j.nrb, bx, sh);
     } else if ((int)blockIdx.z < j.b.nsp) {
         wg_tile<RB, false>(j.b, j.nrb, bx - j.na, sh);
     }
@@ -329,6 +454,15 @@ __global__ __launch_bounds__(256) void k_lin_wsum(WgJobs j) {
         for (int e = 0; e < 4; ++e) v[e] += o[e];
     }
     *dst = v;
+}
+
+template <bool X8>
+void run_wg(int rb, dim3 grid, const WgJobs &j, hipStream_t st) {
+    switch (rb) {
+        case 16: hipLaunchKernelGGL((k_lin_wg<16, X8>), grid, dim3(256), 0, st, j); break;
+        case 32: hipLaunchKernelGGL((k_lin_wg<32, X8>), grid, dim3(256), 0, st, j); break;
+        default: hipLaunchKernelGGL((k_lin_wg<64, X8>), grid, dim3(256), 0, st, j); break;
+    }
 }
 
 int du_rb(int32_t R) { return R <= 32 ? 32 : R <= 64 ? 64 : 128; }
@@ -438,11 +572,8 @@ hipError_t launch_lin_wg(const LinWgArgs *dA, const LinWgArgs *dB, hipStream_t s
     j.na = nx;
     if (dB) fill(*dB, j.b);
     const dim3 grid((unsigned)nx, (unsigned)any.L, (unsigned)nsp);
-    switch (rb) {
-        case 16: hipLaunchKernelGGL(k_lin_wg<16>, grid, dim3(256), 0, st, j); break;
-        case 32: hipLaunchKernelGGL(k_lin_wg<32>, grid, dim3(256), 0, st, j); break;
-        default: hipLaunchKernelGGL(k_lin_wg<64>, grid, dim3(256), 0, st, j); break;
-    }
+    if (dA && dA->xs) run_wg<true>(rb, grid, j, st);
+    else run_wg<false>(rb, grid, j, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || nsp == 1) return e;
     const int64_t units = (int64_t)any.L * any.R * widest / 4;
