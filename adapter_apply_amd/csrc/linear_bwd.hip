@@ -367,8 +367,9 @@ __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, Wg
                 const int u = i * 256 + tid, part = u / (QB / 16), row = u % (QB / 16) / CPQ, tk = v * TK + row;
                 const int j = r0 + u % CPQ * 8;
                 const bool in = u < QU && tk < cnt && j < a.R;
-                t.q[i] = ldg<uint4>(hl + (int64_t)sh.tok[in ? tk : 0] * hlr + (in ? part * a.R + j : 0));
-                if (!in) t.q[i] = make_uint4(0, 0, 0, 0);
+                const uint16_t *q = hl + (int64_t)sh.tok[in ? tk : 0] * hlr + part * a.R + j;
+                // (a choice of values would wait for the load here)
+                t.q[i] = *(in ? reinterpret_cast<const uint4 *>(q) : reinterpret_cast<const uint4 *>(g_zero16));
             }
         };
         auto store = [&](const Stage &t, int v) __attribute__((always_inline)) {

@@ -59,7 +59,6 @@ __device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT> &sh) {
     for (int i = 0; i < CT; ++i)
 #pragma unroll
         for (int j = 0; j < TB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    const uint4 z = make_uint4(0, 0, 0, 0);
 
     // A chunk: the wave's U steps of codes (neighbouring ones, whole lines of 128 bytes a
     // row) and a share of all its x, in registers.
@@ -81,8 +80,9 @@ __device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT> &sh) {
         for (int i = 0; i < XU; ++i) {
             const int q = i * kMfWaves * 64 + tid, row = q >> 4 & (TB * 16 - 1), st = q / (TB * 256);
             const int k = (s0 + st) * kMfStep + (q & 15) * 8;
-            c.x[i] = ldg<uint4>(a.p + (int64_t)min(row, a.T - 1) * a.ldp + min(k, a.K - 8));
-            if (k >= a.K) c.x[i] = z;
+            const uint16_t *x = a.p + (int64_t)min(row, a.T - 1) * a.ldp + k;
+            // (a choice of values would wait for the load here)
+            c.x[i] = *(k < a.K ? reinterpret_cast<const uint4 *>(x) : reinterpret_cast<const uint4 *>(g_zero16));
         }
     };
     auto store_x = [&](const Chunk &c, int buf) __attribute__((always_inline)) {
