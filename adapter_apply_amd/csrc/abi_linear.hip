@@ -86,7 +86,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         size_t n = 0;
         for (int s = 0; s < S; ++s) n += (size_t)N[s];
         const size_t t = T < kMxFewTokens ? T : kMxFewTokens;
-        const size_t few = 4 * (kLinMaxSplits * t > kMxOneSplits ? kLinMaxSplits * t : kMxOneSplits) * (n + S * R);
+        const size_t few = 4 * kMxFewSplits * t * (n + S * R);
         if (n <= (size_t)kMxFewCols && few > part) part = few;
     }
     o = align256(o + part);

@@ -1458,13 +1458,18 @@ __global__ __launch_bounds__(256, 3) void k_lin_join(LinArgs a) {
 
 // Two columns c, c + 1 of one token: the sum of the splits o, bias, delta (the
 // rank vector from u), rounded once.
-template <bool NN>
+struct JoinB {                // a thread's two lora_b rows (forward), and their first 16 ranks
+    const uint16_t *p;
+    int s;
+    uint4 b0[2], b1[2];
+};
+template <bool NN, int MK>
 __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int slot, int rank,
-                                         const float2 (&o)[kLinMaxSplits], const float *u, int64_t ldu) {
+                                         const float2 (&o)[MK], const JoinB &jb, const float *u, int64_t ldu) {
     if (c >= a.cols) return;
     float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-    for (int k = 0; k < kLinMaxSplits; ++k)
+    for (int k = 0; k < MK; ++k)
         if (k < a.ksp) {
             v0 += o[k].x;
             v1 += o[k].y;
@@ -1494,22 +1499,11 @@ __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int
         v1 += sc * d1;
     }
     if (!NN && slot >= 0) {
-        // the column's slice by selects (an index that differs between lanes
-        // would load the arguments from memory, one after the other)
-        int s = 0;
-        int64_t off = 0, n = a.n[0];
-        const uint16_t *b = a.lora[0];
-#pragma unroll
-        for (int i = 1; i < kMaxSlices; ++i)
-            if (i < a.S && c >= a.off[i]) { s = i; off = a.off[i]; n = a.n[i]; b = a.lora[i]; }
-        b += ((int64_t)slot * n + c - off) * a.R;
         float d0 = 0.f, d1 = 0.f;
-#pragma unroll 2
-        for (int j = 0; j < rank; j += 8) {
-            const uint4 b0 = ldg<uint4>(b + j), b1 = ldg<uint4>(b + a.R + j);
-            const float *up = u + s * ldu + j;
-            const floatx4_t u0 = *reinterpret_cast<const floatx4_t *>(up);
-            const floatx4_t u1 = *reinterpret_cast<const floatx4_t *>(up + 4);
+        const float *us = u + jb.s * ldu;
+        auto add8 = [&](const uint4 &b0, const uint4 &b1, int j) __attribute__((always_inline)) {
+            const floatx4_t u0 = *reinterpret_cast<const floatx4_t *>(us + j);
+            const floatx4_t u1 = *reinterpret_cast<const floatx4_t *>(us + j + 4);
             const float uv[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
             const uint32_t w0[4] = {b0.x, b0.y, b0.z, b0.w}, w1[4] = {b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -1519,7 +1513,12 @@ __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int
                 d1 += uv[2 * q] * bf16_lo(w1[q]);
                 d1 += uv[2 * q + 1] * bf16_hi(w1[q]);
             }
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (i * 8 < rank) add8(jb.b0[i], jb.b1[i], i * 8);
+#pragma unroll 2
+        for (int j = 16; j < rank; j += 8) add8(ldg<uint4>(jb.p + j), ldg<uint4>(jb.p + a.R + j), j);
         const float sc = a.scale[slot];
         v0 += sc * d0;
         v1 += sc * d1;
@@ -1533,17 +1532,36 @@ __device__ __forceinline__ void join_row(const LinArgs &a, int t, int64_t c, int
 // wave's lora_b loads cover whole lines: fp32 FMAs with the token's rank vector.
 // In a wide batch every work-group first sums the splits of its token's rank
 // vector.  Gradient (NN, wide only): v against the slot's lora_a rows.
-template <bool NN>
+template <bool NN, int MK>
 __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
     const int t = blockIdx.y;
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
     const int slot = slot_of_token(a.idx, a.slot_rank, a.L, t);
     const float *pt = a.part + (int64_t)t * a.part_ld;
     const int64_t split = (int64_t)a.T * a.part_ld;
-    float2 o[kLinMaxSplits];
+    float2 o[MK];
 #pragma unroll
-    for (int k = 0; k < kLinMaxSplits; ++k)
+    for (int k = 0; k < MK; ++k)
         if (k < a.ksp) o[k] = *reinterpret_cast<const float2 *>(pt + k * split + min(c, a.cols - 2));
+    JoinB jb;
+    if (!NN && slot >= 0) {
+        // the column's slice by selects (an index that differs between lanes
+        // would load the arguments from memory, one after the other); the rows' loads run
+        // beside those of the rank vector's sums
+        const int64_t cc = min(c, a.cols - 2);
+        int64_t off = 0, n = a.n[0];
+        jb.s = 0;
+        jb.p = a.lora[0];
+#pragma unroll
+        for (int i = 1; i < kMaxSlices; ++i)
+            if (i < a.S && cc >= a.off[i]) { jb.s = i; off = a.off[i]; n = a.n[i]; jb.p = a.lora[i]; }
+        jb.p += ((int64_t)slot * n + cc - off) * a.R;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            jb.b0[i] = ldg<uint4>(jb.p + min(i * 8, a.R - 8));
+            jb.b1[i] = ldg<uint4>(jb.p + a.R + min(i * 8, a.R - 8));
+        }
+    }
     const int rank = slot < 0 ? 0 : a.slot_rank ? min(a.slot_rank[slot], a.R) : a.R;
     if (NN || a.wide) {
         __shared__ __attribute__((aligned(16))) float s_u[kLinWideRanks];
@@ -1552,19 +1570,19 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
             float u = 0.f;
             if (j < rank) {
                 const float *p = pt + a.cols + s * a.u_slice + slot * a.u_slot + j;
-                float w[kLinMaxSplits];
+                float w[MK];
 #pragma unroll
-                for (int k = 0; k < kLinMaxSplits; ++k)
+                for (int k = 0; k < MK; ++k)
                     if (k < a.ksp) w[k] = p[k * split];
 #pragma unroll
-                for (int k = 0; k < kLinMaxSplits; ++k)
+                for (int k = 0; k < MK; ++k)
                     if (k < a.ksp) u += w[k];
             }
             s_u[q] = u;
             if (a.buf && blockIdx.x == 0) a.buf[((int64_t)s * a.T + t) * a.R + j] = u;
         }
         __syncthreads();
-        join_row<NN>(a, t, c, slot, rank, o, s_u, a.R);
+        join_row<NN>(a, t, c, slot, rank, o, jb, s_u, a.R);
         return;
     }
     if (a.buf && slot < 0 && blockIdx.x == 0) {
@@ -1572,7 +1590,7 @@ __global__ __launch_bounds__(256) void k_lin_join_rows(LinArgs a) {
         for (int s = 0; s < a.S; ++s)
             for (int j = threadIdx.x; j < a.R; j += 256) a.buf[((int64_t)s * a.T + t) * a.R + j] = 0.f;
     }
-    join_row<NN>(a, t, c, slot, rank, o, a.u + (int64_t)t * a.R, (int64_t)a.T * a.R);
+    join_row<NN>(a, t, c, slot, rank, o, jb, a.u + (int64_t)t * a.R, (int64_t)a.T * a.R);
 }
 // Rank vectors from partial sums (by slot-sorted position) or from a caller's
 // buffer (by token): sums the splits in order, zeroes ranks past the slot's
@@ -1735,7 +1753,7 @@ hipError_t run_tile_of(LinArgs a, bool gradient, int ksp, hipStream_t st) {
     if (e != hipSuccess || !a.part) return e;
     if (a.join_delta && !gradient && !a.order) return launch_lin_join_rows(a, st);
     if (a.join_delta && gradient)
-        hipLaunchKernelGGL(k_lin_join_rows<true>, dim3((unsigned)((cols + 511) / 512), (unsigned)a.T), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_lin_join_rows<true, kLinMaxSplits>), dim3((unsigned)((cols + 511) / 512), (unsigned)a.T), dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL(k_lin_join, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols),
                                             (unsigned)((a.T + kJoinRows - 1) / kJoinRows)), dim3(256), 0, st, a);
@@ -1850,7 +1868,8 @@ static_assert(2 * (kLinWideBytesB / 32) <= kLinJoinMax && 2 * (kLinWideBytesA / 
 
 hipError_t launch_lin_join_rows(const LinArgs &a, hipStream_t st) {
     const dim3 rows((unsigned)((a.cols + 511) / 512), (unsigned)a.T);
-    hipLaunchKernelGGL(k_lin_join_rows<false>, rows, dim3(256), 0, st, a);
+    if (a.ksp <= kLinMaxSplits) hipLaunchKernelGGL((k_lin_join_rows<false, kLinMaxSplits>), rows, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_lin_join_rows<false, kMxFewSplits>), rows, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

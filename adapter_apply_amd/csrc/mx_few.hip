@@ -413,12 +413,12 @@ __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_one(OneArgs f) {
         if (!s_last) return;
         if (tid == 0) __hip_atomic_store(f.count + blockIdx.x, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (col || urow) {
-            float v[kMxOneSplits], sum = 0.f;
+            float v[kMxFewSplits], sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kMxOneSplits; ++k)
+            for (int k = 0; k < kMxFewSplits; ++k)
                 if (k < a.ksp) v[k] = __hip_atomic_load(a.part + k * a.part_ld + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-            for (int k = 0; k < kMxOneSplits; ++k)
+            for (int k = 0; k < kMxFewSplits; ++k)
                 if (k < a.ksp) sum += v[k];
             if (col) y = sum;
             else u = sum;
@@ -451,13 +451,13 @@ hipError_t run(FewArgs f, hipStream_t st) {
 
 // K splits of a few tokens: about 512 work-groups of four K steps or more
 // (a round of a work-group's loads).
-static int32_t mx_few_splits(int32_t K, const int64_t *N, int32_t S, int32_t most) {
+static int32_t mx_few_splits(int32_t K, const int64_t *N, int32_t S) {
     int64_t c = 0;
     for (int s = 0; s < S; ++s) c += (N[s] + 127) / 128;
     const int64_t steps = (K + kMfStep - 1) / kMfStep;
     int64_t k = 512 / c;
     if (k > (steps + 3) / 4) k = (steps + 3) / 4;
-    if (k > most) k = most;
+    if (k > kMxFewSplits) k = kMxFewSplits;
     if (k < 1) k = 1;
     const int64_t per = (steps + k - 1) / k;      // (whole steps: fewer splits may do)
     return (int32_t)((steps + per - 1) / per);
@@ -492,7 +492,7 @@ static hipError_t launch_one(LinArgs a, int32_t *count, hipStream_t st) {
     }
     for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
     const int steps = (a.K + kMfStep - 1) / kMfStep;
-    a.ksp = mx_few_splits(a.K, a.n, a.S, kMxOneSplits);
+    a.ksp = mx_few_splits(a.K, a.n, a.S);
     f.l = a;
     f.per = (steps + a.ksp - 1) / a.ksp;
     f.count = count;
@@ -508,7 +508,7 @@ hipError_t launch_mx_few(LinArgs a, int32_t *count, hipStream_t st) {
     a.part_ld = a.cols + (int64_t)a.S * a.R;
     if (mx_one(a)) return launch_one(a, count, st);
     FewArgs f{};
-    a.ksp = mx_few_splits(a.K, a.n, a.S, kLinMaxSplits);
+    a.ksp = mx_few_splits(a.K, a.n, a.S);
     a.wide = 1;
     a.u_slice = a.R;
     a.u_slot = 0;
