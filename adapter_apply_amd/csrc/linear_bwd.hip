@@ -391,8 +391,7 @@ __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, Wg
         };
         Stage ring[kWg8Depth];
 #pragma unroll
-        for (int d = 0; d < kWg8Depth; ++d)
-            if (d < nst) load(ring[d], d);
+        for (int d = 0; d < kWg8Depth; ++d) load(ring[d], d);
         for (int v0 = 0; v0 < nst; v0 += kWg8Depth)
 #pragma unroll
             for (int d = 0; d < kWg8Depth; ++d) {
@@ -400,7 +399,9 @@ __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, Wg
                 if (v >= nst) break;
                 store(ring[d], v);
                 lds_barrier();
-                if (v + kWg8Depth < nst) load(ring[d], v + kWg8Depth);
+                // (past the count too: under a condition the compiler would wait for every
+                // load at each use)
+                load(ring[d], v + kWg8Depth);
                 const char *st = sh.stage[v & 1];
 #pragma unroll
                 for (int kk = 0; kk < TK / 32; ++kk) {

@@ -19,7 +19,6 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // the blocks of 16 ranks and K.
 constexpr int kMfWaves = 8;
 constexpr int kMfStep = 128;                      // K steps of a lane group's 4 blocks
-constexpr int kMfChunk = 4;                       // such steps of x in LDS together
 struct FewArgs {
     LinArgs l;
     int32_t per;              // K steps of kMfStep per split
@@ -29,16 +28,16 @@ struct FewArgs {
     int32_t rank_groups;
 };
 
-template <int TB, int CT>
+template <int TB, int CT, int CH, bool MULTI>
 struct FewLds {
-    uint4 x[2][kMfChunk][TB * 16][16];            // [chunk][step][token][unit ^ token]
+    uint4 x[MULTI ? 2 : 1][CH][TB * 16][16];      // [chunk][step][token][unit ^ token]
     floatx4_t sum[4][CT * TB][64];
 };
 
-template <int TB, int CT>
-__device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT> &sh) {
+template <int TB, int CT, int CH, bool MULTI>
+__device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT, CH, MULTI> &sh) {
     const LinArgs &a = f.l;
-    constexpr int U = kMfChunk / 2, DEPTH = TB == 1 ? 2 : 1, XU = kMfChunk * TB * 16 * 16 / (kMfWaves * 64);
+    constexpr int U = CH / 2, XU = CH * TB * 16 * 16 / (kMfWaves * 64);
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, cw = w & 3, kw = w >> 2;
     const int l16 = lane & 15, g = lane >> 4;
     int sc = 0;
@@ -120,23 +119,25 @@ __device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT> &sh) {
             }
         }
     };
-    // DEPTH chunks in flight
-    Chunk ch[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        if (first + d * kMfChunk < last) load(ch[d], first + d * kMfChunk);
-    int buf = 0;
-    for (int s0 = first; s0 < last; s0 += DEPTH * kMfChunk)
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int s = s0 + d * kMfChunk;
-            if (s >= last) break;
-            store_x(ch[d], buf);
-            lds_barrier();
-            compute(ch[d], s, buf);
-            if (s + DEPTH * kMfChunk < last) load(ch[d], s + DEPTH * kMfChunk);
-            buf ^= 1;
+    auto use = [&](const Chunk &c, int s0, int buf) __attribute__((always_inline)) {
+        store_x(c, buf);
+        lds_barrier();
+        compute(c, s0, buf);
+    };
+    // (No chunk ahead of its use: other work-groups of the CU fill the wait, and the
+    // registers of a second chunk would cost them their place.)
+    Chunk ch;
+    if (!MULTI) {
+        if (first < last) {
+            load(ch, first);
+            use(ch, first, 0);
         }
+    } else {
+        for (int s = first, buf = 0; s < last; s += CH, buf ^= 1) {
+            load(ch, s);
+            use(ch, s, buf);
+        }
+    }
     if (kw) {
 #pragma unroll
         for (int i = 0; i < CT; ++i)
@@ -235,13 +236,13 @@ __device__ __forceinline__ void few_ranks(const FewArgs &f, floatx4_t (&s_sum)[k
     *reinterpret_cast<floatx4_t *>(a.part + ((int64_t)blockIdx.y * a.T + t) * a.part_ld + a.cols + s * a.R + j) = r;
 }
 
-template <int TB, int CT>
+template <int TB, int CT, int CH, bool MULTI>
 __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_few(FewArgs f) {
     __shared__ union {
-        FewLds<TB, CT> base;
+        FewLds<TB, CT, CH, MULTI> base;
         floatx4_t ranks[kMfWaves][TB][64];
     } sh;
-    if ((int)blockIdx.x < f.col_tiles) few_base<TB, CT>(f, sh.base);
+    if ((int)blockIdx.x < f.col_tiles) few_base<TB, CT, CH, MULTI>(f, sh.base);
     else few_ranks<TB>(f, sh.ranks);
 }
 
@@ -258,10 +259,11 @@ struct OneArgs {
     int32_t *count;           // [column tiles], zero between calls
 };
 constexpr int kOneCols = 128;
-template <int NRB>
+template <int NRB, int U>
 __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_one(OneArgs f) {
-    constexpr int CT = 2, U = 2;
+    constexpr int CT = 2, XU = 2 * U * 16;            // (U steps a wave and round) 16-byte units of x
     __shared__ float s_y[2][kOneCols], s_p[kMfWaves][16 * NRB], s_u[16 * NRB];
+    __shared__ uint4 s_x[2][XU];
     __shared__ int s_last;
     const LinArgs &a = f.l;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, cw = w & 3, kw = w >> 2;
@@ -284,7 +286,6 @@ __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_one(OneArgs f) {
     for (int i = 0; i < CT; ++i) acc[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NRB; ++i) au[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    const uint4 z = make_uint4(0, 0, 0, 0);
     // (its rank, a load later, only masks sums)
     const int named = a.idx[0], slot = named < a.L ? named : -1;
     const int64_t c = c0 + tid;
@@ -303,29 +304,30 @@ __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_one(OneArgs f) {
         for (int j = 0; j < 2 * NRB; ++j) bv[j] = ldg<uint4>(b + min(j * 8, a.R - 8));
         sc_own = a.scale[slot];
     };
-    for (int s0 = first; s0 < last; s0 += 2 * U) {
-        uint4 code[U][CT], xv[U][4];
+    int buf = 0;
+    for (int s0 = first; s0 < last; s0 += 2 * U, buf ^= 1) {
+        uint4 code[U][CT], xv = make_uint4(0, 0, 0, 0);
         uint32_t scale[U][CT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int st = min(s0 + kw * U + u, steps - 1), b = min(st * 4 + g, blocks - 1);
+            const int st = min(s0 + kw * U + u, last - 1), b = min(st * 4 + g, blocks - 1);
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 code[u][i] = ldg<uint4>(wr[i] + b * 16);
                 scale[u][i] = *reinterpret_cast<const uint32_t *>(sr[i] + st * 4);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) xv[u][k] = ldg<uint4>(a.p + min(b * kMxBlock + k * 8, a.K - 8));
         }
+        // x past the split's or the row's end is zero
+        const int xk = s0 * kMfStep + tid * 8;
+        if (tid < XU && xk < last * kMfStep && xk < a.K) xv = ldg<uint4>(a.p + xk);
         __builtin_amdgcn_sched_barrier(0);
-        // the slot's rows of the same steps: 2 U steps of 128, a wave's 32 at a time
+        // the slot's rows of the same steps: a wave's 32 at a time
         constexpr int AU = 2 * U * kMfStep / (32 * kMfWaves);
-        uint4 av[AU][NRB], ax[AU];
+        uint4 av[AU][NRB];
         if (slot >= 0) {
 #pragma unroll
             for (int v = 0; v < AU; ++v) {
-                const int k = min(s0 * kMfStep + (v * kMfWaves + w) * 32 + g * 8, a.K - 8);
-                ax[v] = ldg<uint4>(a.p + k);
+                const int k = min(s0 * kMfStep + (v * kMfWaves + w) * 32 + g * 8, min(last * kMfStep, a.K) - 8);
 #pragma unroll
                 for (int i = 0; i < NRB; ++i)
                     av[v][i] = ldg<uint4>(a.other[sc] + ((int64_t)slot * a.R + min(i * 16 + l16, a.R - 1)) * a.K + k);
@@ -333,17 +335,19 @@ __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_one(OneArgs f) {
         }
         if (NRB == 1 && s0 == first) load_b();
         __builtin_amdgcn_sched_barrier(0);        // every load of the round in flight
+        if (tid < XU) s_x[buf][tid] = xv;
+        lds_barrier();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // past the end x is zero, and the scale is no NaN
-            const int st = s0 + kw * U + u, b = st * 4 + g;
-            const bool in = st < last && b < blocks;
+            // (past the end the scale is no NaN)
+            const int st = s0 + kw * U + u;
+            const bool in = st < last && st * 4 + g < blocks;
             uint32_t bits[CT];
 #pragma unroll
             for (int i = 0; i < CT; ++i) bits[i] = in ? (scale[u][i] >> (8 * g) & 0xff) << 23 : 0u;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bf16x8_t x = frag(in && b * kMxBlock + k * 8 < a.K ? xv[u][k] : z);
+                const bf16x8_t x = frag(s_x[buf][(kw * U + u) * 16 + g * 4 + k]);
 #pragma unroll
                 for (int i = 0; i < CT; ++i) {
                     const uint32_t c[4] = {code[u][i].x, code[u][i].y, code[u][i].z, code[u][i].w};
@@ -354,12 +358,14 @@ __global__ __launch_bounds__(kMfWaves * 64, 4) void k_mx_one(OneArgs f) {
         if (slot >= 0) {
 #pragma unroll
             for (int v = 0; v < AU; ++v) {
+                // (past the end x is zero, and the row's values there may be anything)
                 const int k = s0 * kMfStep + (v * kMfWaves + w) * 32 + g * 8;
                 const bool in = k < last * kMfStep && k < a.K;
-                const bf16x8_t x = frag(in ? ax[v] : z);
+                const bf16x8_t x = frag(s_x[buf][(v * kMfWaves + w) * 4 + g]);
 #pragma unroll
                 for (int i = 0; i < NRB; ++i)
-                    au[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? av[v][i] : z), x, au[i], 0, 0, 0);
+                    au[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? av[v][i] : make_uint4(0, 0, 0, 0)), x,
+                                                                  au[i], 0, 0, 0);
             }
         }
     }
@@ -443,7 +449,10 @@ hipError_t run(FewArgs f, hipStream_t st) {
     for (int s = a.S; s <= kMaxSlices; ++s) a.tile_start[s] = c;
     f.col_tiles = c;
     const dim3 grid((unsigned)(c + a.S * f.rank_groups * f.slots), (unsigned)a.ksp);
-    hipLaunchKernelGGL((k_mx_few<TB, CT>), grid, dim3(kMfWaves * 64), 0, st, f);
+    const dim3 block(kMfWaves * 64);
+    if (f.per <= 4) hipLaunchKernelGGL((k_mx_few<TB, CT, 4, false>), grid, block, 0, st, f);
+    else if (f.per <= 8 && TB == 1) hipLaunchKernelGGL((k_mx_few<TB, CT, TB == 1 ? 8 : 4, false>), grid, block, 0, st, f);
+    else hipLaunchKernelGGL((k_mx_few<TB, CT, 4, true>), grid, block, 0, st, f);
     return hipGetLastError();
 }
 
@@ -497,8 +506,10 @@ static hipError_t launch_one(LinArgs a, int32_t *count, hipStream_t st) {
     f.per = (steps + a.ksp - 1) / a.ksp;
     f.count = count;
     const dim3 grid((unsigned)c, (unsigned)a.ksp);
-    if (a.R <= 16) hipLaunchKernelGGL(k_mx_one<1>, grid, dim3(kMfWaves * 64), 0, st, f);
-    else hipLaunchKernelGGL(k_mx_one<2>, grid, dim3(kMfWaves * 64), 0, st, f);
+    const dim3 block(kMfWaves * 64);
+    if (a.R > 16) hipLaunchKernelGGL((k_mx_one<2, 2>), grid, block, 0, st, f);
+    else if (f.per <= 4) hipLaunchKernelGGL((k_mx_one<1, 2>), grid, block, 0, st, f);
+    else hipLaunchKernelGGL((k_mx_one<1, 4>), grid, block, 0, st, f);
     return hipGetLastError();
 }
 
