@@ -152,9 +152,15 @@ def _check(code: int, where: str):
 # tensor marshalling helpers
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -584,15 +590,25 @@ def _call(name, dev, stream, *args):
     not), on `stream` or the device's current stream."""
     cuda = _torch().cuda
     if stream is None:
-        stream = cuda.current_stream(dev)
-    if not isinstance(stream, int):
+        stream = _raw_stream(dev)
+    elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    prev = cuda.current_device()
-    if prev == dev:
-        _check(getattr(lib(), name)(*args, stream), name)
-        return
-    with cuda.device(dev):
-        _check(getattr(lib(), name)(*args, stream), name)
+    fn = getattr(lib(), name)
+    if cuda.current_device() == dev:
+        code = fn(*args, stream)
+    else:
+        with cuda.device(dev):
+            code = fn(*args, stream)
+    if code != LORA_OK:
+        raise LoraError(code, name)
+
+
+def _raw_stream(dev):
+    """The device's current stream as an integer (where torch has it, without making a
+    Stream object, whose cost is near that of the rest of a call's checks)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _one_device(tensors):
@@ -608,47 +624,86 @@ def _bad_stack(ts, name, shapes, dtype):
                      f"{[list(s) for s in shapes]}; got {[(list(t.shape), t.dtype) for t in ts]}")
 
 
-def _need_stack(ts, name, shapes, dtype):
+# Each of these checks a tensor, adds its device's index to devs and returns its
+# pointer (and sizes), so that a call looks at a tensor's attributes once.
+
+def _matrix(t, dtype, name, devs):
+    """(pointer, row stride, rows, columns) of a 2-D tensor with unit column stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or stride[1] != 1:
+        _rowmajor(t, name)
+    if t.dtype is not dtype:
+        _need_dtype(t, (dtype,), name)
+    devs.add(t.get_device())
+    return t.data_ptr(), stride[0], shape[0], shape[1]
+
+
+def _stack(ts, name, shapes, dtype, devs):
+    """Pointers of contiguous tensors, as an array whose memory the C call reads."""
     if len(ts) != len(shapes):
         raise ValueError(f"{name} holds {len(ts)} tensors; expected {len(shapes)}")
+    ptrs = []
     for t, shape in zip(ts, shapes):
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             _bad_stack(ts, name, shapes, dtype)
+        devs.add(t.get_device())
+        ptrs.append(t.data_ptr())
+    return array("Q", ptrs)
 
 
-def _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, S_cols):
-    """Checks shared by the layer and its gradient (x None: only there); S_cols:
-    the [T, sum N] tensor (y or dy) and its name.  Returns T, K, L, R and the
-    widths."""
+def _vec(t, n, dtype, name, devs):
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        _need_vec(t, n, dtype, name)
+    devs.add(t.get_device())
+    return t.data_ptr()
+
+
+def _device_of(devs, tensors):
+    """The one GPU among devs, the indexes of the tensors (a list, or lists of them)."""
+    if len(devs) != 1 or -1 in devs:
+        _need_device([t for g in tensors for t in (g if isinstance(g, (list, tuple)) else (g,))])
+    return next(iter(devs))
+
+
+def _layer(t, name, T, K, A, B, idx, slot_rank, scale, buf, ws, devs):
+    """Checks shared by the layer and its gradient; t: the [T, sum N] tensor (y or
+    dy); T, K: x's sizes, or None without it.  Returns T, K, the widths, and the C
+    arguments: t's pointer and row stride; A, B, N, S, L, R (the first three as arrays
+    that have to live as long as the call), idx, slot_rank and scale; buf; ws."""
     torch = _torch()
     bf16 = torch.bfloat16
-    if x is not None:
-        _rowmajor(x, "x")
-        _need_dtype(x, (bf16,), "x")
-    t, name = S_cols
-    _rowmajor(t, name)
-    _need_dtype(t, (bf16,), name)
-    if len(A) < 1 or A[0].dim() != 3 or len(A) != len(B) or any(b.dim() != 3 for b in B):
+    tp, ldt, rows, cols = _matrix(t, bf16, name, devs)
+    S = len(A)
+    if S < 1 or A[0].dim() != 3 or S != len(B) or any(b.dim() != 3 for b in B):
         raise ValueError("A and B must hold one [L, R, K] and one [L, N_s, R] tensor per slice "
-                         f"(got {len(A)} and {len(B)} tensors)")
-    L, R, K = A[0].shape
-    T, K = (t.shape[0], K) if x is None else x.shape
+                         f"(got {S} and {len(B)} tensors)")
+    L, R, Ka = A[0].shape
+    if T is None:
+        T, K = rows, Ka
     N = [b.shape[1] for b in B]
-    _need_stack(A, "A", [(L, R, K)] * len(A), bf16)
-    _need_stack(B, "B", [(L, n, R) for n in N], bf16)
     n = sum(N)
-    if t.shape[0] != T or t.shape[1] < n:
+    Ap = _stack(A, "A", [(L, R, K)] * S, bf16, devs)
+    Bp = _stack(B, "B", [(L, v, R) for v in N], bf16, devs)
+    if rows != T or cols < n:
         raise ValueError(f"{name} has shape {list(t.shape)}; expected [{T}, >= {n}]")
-    if W is not None:
-        _rowmajor(W, "W")
-        _need_dtype(W, (bf16,), "W")
-        _need_shape(W, (n, K), "W")
-    if buf is not None and (buf.dtype is not torch.float32 or buf.shape != (len(A), T, R) or
-                            not buf.is_contiguous()):
-        raise ValueError(f"buf must be a contiguous fp32 [{len(A)}, {T}, {R}] tensor")
-    _check_meta(idx, slot_rank, scale, T, L)
+    bp = None
+    if buf is not None:
+        if buf.dtype is not torch.float32 or buf.shape != (S, T, R) or not buf.is_contiguous():
+            raise ValueError(f"buf must be a contiguous fp32 [{S}, {T}, {R}] tensor")
+        devs.add(buf.get_device())
+        bp = buf.data_ptr()
+    i32, f32 = torch.int32, torch.float32
+    meta = (_vec(idx, T, i32, "idx", devs), None if slot_rank is None else _vec(slot_rank, L, i32, "slot_rank", devs),
+            None if scale is None else _vec(scale, L, f32, "scale", devs))
     _check_ws(ws)
-    return T, K, L, R, N
+    devs.add(ws.get_device())
+    return T, K, N, (tp, ldt), (Ap, Bp, array("q", N), S, L, R), meta, bp, (ws.data_ptr(), ws.nbytes)
+
+
+def _slices(sl):
+    """The slices' C arguments."""
+    Ap, Bp, N, S, L, R = sl
+    return _addr(Ap), _addr(Bp), _addr(N), S, L, R
 
 
 def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bias=None, buf=None,
@@ -658,34 +713,42 @@ def lora_linear(y, x, W, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bi
     None; all bf16.  buf [S, T, R] fp32 (optional) receives x A^T."""
     if x is None or W is None:
         raise ValueError("x and W are needed")
-    T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
-    if bias is not None:
-        _need_vec(bias, sum(N), _torch().bfloat16, "bias")
-    dev = _one_device((y, x, W, *A, *B, idx, slot_rank, scale, buf, bias, ws))
-    S = len(N)
-    _call("lora_linear", dev, stream, _ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
-          W.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B), (_i64 * S)(*N), S, L, R, _ptr(idx),
-          _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
+    bf16, devs = _torch().bfloat16, set()
+    xp, ldx, T, K = _matrix(x, bf16, "x", devs)
+    T, K, N, yp, sl, meta, bp, wsp = _layer(y, "y", T, K, A, B, idx, slot_rank, scale, buf, ws, devs)
+    wp = _frozen(W, sum(N), K, devs)
+    bias_p = None if bias is None else _vec(bias, sum(N), bf16, "bias", devs)
+    dev = _device_of(devs, (y, x, W, A, B, idx, slot_rank, scale, buf, bias, ws))
+    _call("lora_linear", dev, stream, *yp, xp, ldx, T, K, *wp, bias_p, *_slices(sl), *meta, bp, LORA_DT_BF16,
+          flags, *wsp)
 
 
-def _check_backward(dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws, T, K, L, R, N, *more):
-    """Checks of the gradients' outputs; returns the device and the slices."""
+def _frozen(W, n, K, devs):
+    """A bf16 projection's pointer and row stride."""
+    p, ld, rows, cols = _matrix(W, _torch().bfloat16, "W", devs)
+    if rows != n or cols != K:
+        _need_shape(W, (n, K), "W")
+    return p, ld
+
+
+def _outputs(dx, dA, dB, x, buf, T, K, N, sl, devs):
+    """Checks of the gradients' outputs; their C arguments: dx and its row stride, and the
+    arrays of dA and dB (or None)."""
     torch = _torch()
-    S = len(N)
+    S, L, R = sl[3:]
     if x is None and (dA is not None or (dB is not None and buf is None)):
         raise ValueError("x is needed for dA, and for dB without buf")
+    dxp, ld = None, 0
     if dx is not None:
-        _rowmajor(dx, "dx")
-        _need_dtype(dx, (torch.bfloat16,), "dx")
-        _need_shape(dx, (T, K), "dx")
-    if dA is not None:
-        _need_stack(dA, "dA", [(L, R, K)] * S, torch.float32)
-    if dB is not None:
-        _need_stack(dB, "dB", [(L, n, R) for n in N], torch.float32)
-    outs = [t.data_ptr() for t in (dx, *(dA or ()), *(dB or ())) if t is not None and t.numel()]
+        dxp, ld, rows, cols = _matrix(dx, torch.bfloat16, "dx", devs)
+        if rows != T or cols != K:
+            _need_shape(dx, (T, K), "dx")
+    dAp = None if dA is None else _stack(dA, "dA", [(L, R, K)] * S, torch.float32, devs)
+    dBp = None if dB is None else _stack(dB, "dB", [(L, n, R) for n in N], torch.float32, devs)
+    outs = [p for p in (dxp, *(dAp or ()), *(dBp or ())) if p]        # (empty tensors have none)
     if len(set(outs)) != len(outs):
         raise ValueError("dx, dA and dB must be different tensors")
-    return _one_device((dx, *(dA or ()), *(dB or ()), dy, x, W, *A, *B, idx, slot_rank, scale, buf, ws, *more)), S
+    return (dxp, ld), dAp, dBp
 
 
 def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
@@ -695,13 +758,15 @@ def lora_linear_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy,
     [L, R, K] and dB[s] [L, N_s, R] fp32, or None; dy [T, >= sum N].  W None:
     dx += the adapters' part.  buf: x A^T as lora_linear left it, or None.  x
     [T, K] may be None where it is not read: no dA, and no dB or a buf."""
-    T, K, L, R, N = _check_layer(x, W, A, B, idx, slot_rank, scale, buf, ws, (dy, "dy"))
-    dev, S = _check_backward(dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws, T, K, L, R, N)
-    _call("lora_linear_backward", dev, stream, _ptr(dx), 0 if dx is None else dx.stride(0),
-          None if dA is None else _ptr_array(dA), None if dB is None else _ptr_array(dB), _ptr(dy),
-          dy.stride(0), _ptr(x), 0 if x is None else x.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
-          _ptr_array(A), _ptr_array(B), (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank),
-          _ptr(scale), _ptr(buf), LORA_DT_BF16, flags, _ptr(ws), ws.nbytes)
+    devs = set()
+    xp, ldx, T, K = (None, 0, None, None) if x is None else _matrix(x, _torch().bfloat16, "x", devs)
+    T, K, N, dyp, sl, meta, bp, wsp = _layer(dy, "dy", T, K, A, B, idx, slot_rank, scale, buf, ws, devs)
+    wp = (None, 0) if W is None else _frozen(W, sum(N), K, devs)
+    dxp, dAp, dBp = _outputs(dx, dA, dB, x, buf, T, K, N, sl, devs)
+    dev = _device_of(devs, (dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws))
+    _call("lora_linear_backward", dev, stream, *dxp, None if dAp is None else _addr(dAp),
+          None if dBp is None else _addr(dBp), *dyp, xp, ldx, T, K, *wp, *_slices(sl), *meta, bp, LORA_DT_BF16,
+          flags, *wsp)
 
 
 # ---------------------------------------------------------------------------
@@ -716,13 +781,18 @@ def _mx_shapes(M, K, fmt):
     return (M, n * (16 if fmt == LORA_MX_FP4 else 32)), (M, (n + 3) // 4 * 4)
 
 
-def _need_mx(codes, scales, M, K, fmt, name):
+def _mx(codes, scales, M, K, fmt, name, devs):
+    """Pointers and row strides of codes and scales."""
     u8 = _torch().uint8
     cs, ss = _mx_shapes(M, K, fmt)
-    for t, shape, what in ((codes, cs, name), (scales, ss, f"{name}'s scales")):
-        if t.dtype is not u8 or t.shape != shape or t.stride(1) != 1:
-            raise ValueError(f"{what} must be a uint8 {list(shape)} tensor with unit column stride (got {t.dtype} "
-                             f"{list(t.shape)})")
+    c, s = codes.stride(), scales.stride()
+    if (codes.dtype is not u8 or codes.shape != cs or c[1] != 1 or
+            scales.dtype is not u8 or scales.shape != ss or s[1] != 1):
+        raise ValueError(f"{name} and its scales must be uint8 {list(cs)} and {list(ss)} tensors with unit column "
+                         f"stride (got {codes.dtype} {list(codes.shape)} and {scales.dtype} {list(scales.shape)})")
+    devs.add(codes.get_device())
+    devs.add(scales.get_device())
+    return codes.data_ptr(), c[0], scales.data_ptr(), s[0]
 
 
 def alloc_mx(M: int, K: int, fmt: int, device="cuda"):
@@ -734,14 +804,12 @@ def alloc_mx(M: int, K: int, fmt: int, device="cuda"):
 
 
 def _mx_call(name, x, codes, scales, fmt, stream, outs_first):
-    _rowmajor(x, "x")
     _need_dtype(x, _float_types(), "x")
-    M, K = x.shape
-    _need_mx(codes, scales, M, K, fmt, "codes")
-    dev = _one_device((x, codes, scales))
-    mx = (_ptr(codes), codes.stride(0), _ptr(scales), scales.stride(0))
-    xs = (_ptr(x), x.stride(0))
-    _call(name, dev, stream, *(mx + xs if outs_first else xs + mx), M, K, fmt, _dtype_code(x))
+    devs = set()
+    xp, ldx, M, K = _matrix(x, x.dtype, "x", devs)
+    mx = _mx(codes, scales, M, K, fmt, "codes", devs)
+    dev = _device_of(devs, (x, codes, scales))
+    _call(name, dev, stream, *((*mx, xp, ldx) if outs_first else (xp, ldx, *mx)), M, K, fmt, _dtype_code(x))
 
 
 def lora_mx_quantize(codes, scales, x, fmt: int, stream=None):
@@ -772,16 +840,14 @@ def lora_linear_mx(y, x, W, W_scales, A: Sequence, B: Sequence, idx, slot_rank, 
     """lora_linear with W [sum N, K] in 4 bits: LORA_MX_FP4 codes and scales."""
     if x is None or W is None or W_scales is None:
         raise ValueError("x, W and W_scales are needed")
-    T, K, L, R, N = _check_layer(x, None, A, B, idx, slot_rank, scale, buf, ws, (y, "y"))
-    _need_mx(W, W_scales, sum(N), K, LORA_MX_FP4, "W")
-    if bias is not None:
-        _need_vec(bias, sum(N), _torch().bfloat16, "bias")
-    dev = _one_device((y, x, W, W_scales, *A, *B, idx, slot_rank, scale, buf, bias, ws))
-    S = len(N)
-    _call("lora_linear_mx", dev, stream, _ptr(y), y.stride(0), _ptr(x), x.stride(0), T, K, _ptr(W),
-          W.stride(0), _ptr(W_scales), W_scales.stride(0), _ptr(bias), _ptr_array(A), _ptr_array(B),
-          (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags,
-          _ptr(ws), ws.nbytes)
+    bf16, devs = _torch().bfloat16, set()
+    xp, ldx, T, K = _matrix(x, bf16, "x", devs)
+    T, K, N, yp, sl, meta, bp, wsp = _layer(y, "y", T, K, A, B, idx, slot_rank, scale, buf, ws, devs)
+    wp = _mx(W, W_scales, sum(N), K, LORA_MX_FP4, "W", devs)
+    bias_p = None if bias is None else _vec(bias, sum(N), bf16, "bias", devs)
+    dev = _device_of(devs, (y, x, W, W_scales, A, B, idx, slot_rank, scale, buf, bias, ws))
+    _call("lora_linear_mx", dev, stream, *yp, xp, ldx, T, K, *wp, bias_p, *_slices(sl), *meta, bp, LORA_DT_BF16,
+          flags, *wsp)
 
 
 def lora_linear_mx_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], dy, x, W, A: Sequence,
@@ -795,21 +861,24 @@ def lora_linear_mx_backward(dx, dA: Optional[Sequence], dB: Optional[Sequence], 
         raise ValueError("x_scales without x")
     if x_scales is not None and dB is not None and buf is None:
         raise ValueError("dB from an 8-bit x needs buf")
-    T, K, L, R, N = _check_layer(x if x_scales is None else None, W if W_scales is None else None, A, B, idx,
-                                 slot_rank, scale, buf, ws, (dy, "dy"))
-    if W_scales is not None:
-        _need_mx(W, W_scales, sum(N), K, LORA_MX_FP4, "W")
+    devs = set()
+    xp, T, K = (None, 0, None, 0), None, None
+    if x is not None and x_scales is None:
+        xp, ldx, T, K = _matrix(x, _torch().bfloat16, "x", devs)
+        xp = (xp, ldx, None, 0)
+    T, K, N, dyp, sl, meta, bp, wsp = _layer(dy, "dy", T, K, A, B, idx, slot_rank, scale, buf, ws, devs)
     if x_scales is not None:
-        _need_mx(x, x_scales, T, K, LORA_MX_INT8, "x")
-    dev, S = _check_backward(dx, dA, dB, dy, x, W, A, B, idx, slot_rank, scale, buf, ws, T, K, L, R, N,
-                             x_scales, W_scales)
-    _call("lora_linear_mx_backward", dev, stream, _ptr(dx), 0 if dx is None else dx.stride(0),
-          None if dA is None else _ptr_array(dA), None if dB is None else _ptr_array(dB), _ptr(dy),
-          dy.stride(0), _ptr(x), 0 if x is None else x.stride(0), _ptr(x_scales),
-          0 if x_scales is None else x_scales.stride(0), T, K, _ptr(W), 0 if W is None else W.stride(0),
-          _ptr(W_scales), 0 if W_scales is None else W_scales.stride(0), _ptr_array(A), _ptr_array(B),
-          (_i64 * S)(*N), S, L, R, _ptr(idx), _ptr(slot_rank), _ptr(scale), _ptr(buf), LORA_DT_BF16, flags,
-          _ptr(ws), ws.nbytes)
+        xp = _mx(x, x_scales, T, K, LORA_MX_INT8, "x", devs)
+    wp = (None, 0, None, 0)
+    if W_scales is not None:
+        wp = _mx(W, W_scales, sum(N), K, LORA_MX_FP4, "W", devs)
+    elif W is not None:
+        wp = (*_frozen(W, sum(N), K, devs), None, 0)
+    dxp, dAp, dBp = _outputs(dx, dA, dB, x, buf, T, K, N, sl, devs)
+    dev = _device_of(devs, (dx, dA, dB, dy, x, x_scales, W, W_scales, A, B, idx, slot_rank, scale, buf, ws))
+    _call("lora_linear_mx_backward", dev, stream, *dxp, None if dAp is None else _addr(dAp),
+          None if dBp is None else _addr(dBp), *dyp, *xp, T, K, *wp, *_slices(sl), *meta, bp, LORA_DT_BF16, flags,
+          *wsp)
 
 
 # ---------------------------------------------------------------------------
