@@ -504,7 +504,7 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
  * power), at least 2^-127; elements are rounded to nearest, ties to the even code, and
  * those past the largest (6, 127 / 64) become it.  A block that holds an infinity or
  * NaN gets scale 255.  The codes past K of a row's last block and the scales past KB up
- * to whole 4 are written as zeros.  M >= 0, and M * ceil(K / 128) < 2^30.  No output
+ * to whole 4 are written as zeros.  M >= 0, and M * ceil(K / 128) < 2^27.  No output
  * overlaps x or another output.
  */
 lora_status_t lora_mx_quantize(void *codes, int64_t ldc, void *scales, int64_t lds, const void *x,

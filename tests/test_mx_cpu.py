@@ -65,6 +65,8 @@ def store(quantize, **kw):
 STORE_BAD = [
     (dict(M=-1), aa.LORA_E_SHAPE),
     (dict(M=1 << 26), aa.LORA_E_SHAPE),
+    (dict(M=1 << 22), aa.LORA_E_SHAPE),
+    (dict(M=1 << 27, K=8, ldx=8, ldc=16, lds=4), aa.LORA_E_SHAPE),
     (dict(M=1 << 62), aa.LORA_E_SHAPE),
     (dict(K=0), aa.LORA_E_SHAPE),
     (dict(K=4100, ldx=4104, lds=132, ldc=2080), aa.LORA_E_ALIGN),
