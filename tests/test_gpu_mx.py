@@ -186,6 +186,25 @@ SHAPES = [
 ]
 
 
+# The forms of a few tokens: one and several rounds of K steps a split, more than 8
+# splits, one and two blocks of tokens, ranks past one work-group's, rows short of the
+# columns' blocks.
+FEW_SHAPES = [
+    (1, 4104, (8200,), 16, 2, 0),
+    (1, 5000, (68, 36), 24, 3, 4),
+    (1, 136, (16388,), 8, 2, 0),
+    (2, 136, (40,), 80, 4, 0),
+    (7, 4104, (8200,), 16, 3, 4),
+    (3, 4104, (16004,), 8, 3, 0),
+    (9, 5000, (260,), 16, 3, 4),
+    (16, 520, (132, 4), 136, 20, 8),
+    (17, 520, (4100,), 8, 2, 4),
+    (20, 4104, (8200,), 8, 3, 0),
+    (32, 5000, (2000, 132), 16, 3, 4),
+    (32, 1032, (2600,), 8, 9, 4),
+]
+
+
 def layer(shape, seed, **kw):
     T, K, N, R, L, extra = shape
     return MxLayer(T, K, N, R, L, seed=seed, extra=extra, **kw)
@@ -228,7 +247,7 @@ def check_backward(c, buf, dx, dA, dB, with_w=True):
 
 
 @pytest.mark.parametrize("bias", [False, True])
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + FEW_SHAPES, ids=str)
 def test_forward(shape, bias):
     c = layer(shape, shape[0] + shape[1], bias=bias, runs=bias)
     y_ref, y_tol, b_ref, b_tol = c.forward()
@@ -398,6 +417,85 @@ def test_infinite_x_and_dy_stay_in_their_rows():
         assert torch.isfinite(dx[[i for i in range(c.T) if i != 1]].float()).all()
 
 
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] in (1, 5, 33, 256, 777, 2100)], ids=str)
+def test_empty_slots_with_any_scale(shape):
+    """A token of an empty slot (rank 0) gets the projection alone, whatever the
+    slot's scale; and no ranks given: every slot has all of them."""
+    c = layer(shape, 9, ragged=False)
+    c.rank[:] = 0
+    c.scale[:] = float("inf")
+    y_ref, y_tol, _, _ = c.forward()
+    _, y, buf = run_forward(c)
+    within(y, y_ref, y_tol, "y")
+    assert not bool(buf.any())
+    c.rank[:] = c.R
+    c.scale[:] = 0.5
+    y_ref, y_tol, b_ref, b_tol = c.forward()
+    rank, c.rank = c.rank, None
+    _, y, buf = run_forward(c)
+    c.rank = rank
+    within(y, y_ref, y_tol, "y")
+    within(buf, b_ref, b_tol, "buf")
+
+
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] in (1, 5, 16, 100, 1200, 2100)], ids=str)
+def test_values_past_a_slots_rank(shape):
+    """A and B hold other values past each slot's rank (a larger adapter before)."""
+    c = layer(shape, 13, stale=True, x8=True)
+    y_ref, y_tol, b_ref, b_tol = c.forward()
+    _, y, buf = run_forward(c)
+    within(y, y_ref, y_tol, "y")
+    within(buf, b_ref, b_tol, "buf")
+    dx = torch.empty((c.T, c.K), dtype=bf16, device="cuda")
+    dA, dB = gradients(c)
+    call_backward(c, dx, dA, dB, buf=buf)
+    check_backward(c, buf, dx, dA, dB)
+
+
+def test_segments_ready():
+    """The backward call and a second layer reuse the segments in the workspace."""
+    c = layer((1200, 2048, (260,), 16, 3, 4), 17, x8=True)
+    ws = workspace(c)
+    aa.lora_build_segments(c.idx, c.rank, c.L, c.R, ws)
+    y_ref, y_tol, _, _ = c.forward()
+    y = torch.empty((c.T, 260), dtype=bf16, device="cuda")
+    buf = torch.empty((1, c.T, c.R), device="cuda")
+    for _ in range(2):
+        aa.lora_linear_mx(y, c.x, c.Wq, c.Ws, c.A, c.B, c.idx, c.rank, c.scale, ws, buf=buf,
+                          flags=aa.LORA_FLAG_SEGMENTS_READY)
+        within(y, y_ref, y_tol, "y")
+    dx = torch.empty((c.T, c.K), dtype=bf16, device="cuda")
+    dA, dB = gradients(c)
+    call_backward(c, dx, dA, dB, buf=buf, ws=ws, flags=aa.LORA_FLAG_SEGMENTS_READY)
+    check_backward(c, buf, dx, dA, dB)
+
+
+def test_no_tokens():
+    c = layer((3, 72, (36,), 24, 3, 0), 1, x8=True)
+    ws = workspace(c)
+    e = lambda *s, dt=bf16: torch.empty(s, dtype=dt, device="cuda")
+    u8 = torch.uint8
+    aa.lora_linear_mx(e(0, 36), e(0, 72), c.Wq, c.Ws, c.A, c.B, c.idx[:0], c.rank, c.scale, ws)
+    dA, dB = gradients(c)
+    aa.lora_linear_mx_backward(e(0, 72), dA, dB, e(0, 36), e(0, 96, dt=u8), c.Wq, c.A, c.B, c.idx[:0], c.rank, c.scale,
+                               ws, buf=e(1, 0, 24, dt=torch.float32), x_scales=e(0, 4, dt=u8), W_scales=c.Ws)
+    assert not any(bool(t.any()) for t in dA + dB)
+
+
+def test_rows_and_slots_of_one_token_calls():
+    """One token after another on one workspace, each with another slot or none: the
+    counts that a call leaves are the next one's."""
+    c = layer((40, 520, (260, 132), 16, 5, 0), 19)
+    ws = aa.alloc_linear_mx_workspace(1, c.K, c.N, c.R, c.L)
+    y_ref, y_tol, b_ref, b_tol = c.forward()
+    for t in range(c.T):
+        y = torch.full((1, 392), FILL, dtype=bf16, device="cuda")
+        buf = torch.full((2, 1, 16), FILL, device="cuda")
+        aa.lora_linear_mx(y, c.x[t:t + 1], c.Wq, c.Ws, c.A, c.B, c.idx[t:t + 1], c.rank, c.scale, ws, buf=buf)
+        within(y, y_ref[t:t + 1], y_tol[t:t + 1], f"y of token {t}")
+        within(buf, b_ref[:, t:t + 1], b_tol[:, t:t + 1], f"buf of token {t}")
+
+
 def test_workspace_shared_by_layers_and_kinds():
     """Layers of several sizes, bf16 and 4-bit ones, in turn on one workspace as
     large as the largest needs."""
@@ -420,7 +518,8 @@ def test_workspace_shared_by_layers_and_kinds():
             check_backward(c, buf, dx, dA, dB)
 
 
-@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] in (1, 5, 33, 256, 777, 2100)], ids=str)
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] in (1, 5, 33, 256, 777, 2100)] +
+                         FEW_SHAPES[::3], ids=str)
 def test_same_bits_on_another_stream_and_in_graphs(shape):
     """A call on a stream of its own, and two captured calls on one workspace,
     replayed between eager work: the bits of the eager call."""

@@ -203,6 +203,17 @@ def test_workspace_size():
     assert aa.lib().lora_linear_mx_workspace_size(1, 64, i64(64), 1, 8, 1, None) == aa.LORA_E_NULL
 
 
+# T, N, R, L, whether the few-token kernels take it
+@pytest.mark.parametrize("T,N,R,L,few", [
+    (1, (4, ), 8, 1, True), (16, (4096, 1024, 1024), 16, 8, True), (16, (64,), 512, 1024, True),
+    (17, (4096,), 16, 8, True), (32, (4096, 1024, 1024), 16, 8, False), (32, (2600,), 8, 9, True),
+    (33, (65536,), 8, 1, False), (1, (65540,), 8, 1, False), (1, (64,) * 8, 136, 4, False)])
+def test_few_tokens_rule(T, N, R, L, few):
+    f = aa.lib()._ZN2aa6mx_fewEiPKliii
+    f.restype, f.argtypes = C.c_bool, [C.c_int32, C.POINTER(C.c_int64), C.c_int32, C.c_int32, C.c_int32]
+    assert f(T, i64(*N), len(N), R, L) is few
+
+
 # --------------------------------------------------------------------------
 # the binding
 # --------------------------------------------------------------------------
