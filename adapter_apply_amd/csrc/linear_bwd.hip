@@ -314,7 +314,7 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
 // way to LDS.  A thread has its share of a stage in registers (16 codes of a token, of
 // one block, and the rank vectors' units), kWg8Depth stages ahead; all its loads are
 // the compiler's, which then waits for a stage's own only.
-constexpr int kWg8Depth = 2;
+constexpr int kWg8Depth = 3;
 template <int RB>
 __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, WgLds<RB> &sh) {
     constexpr int NP = kLinPartsBwd, TK = kWgStep;
