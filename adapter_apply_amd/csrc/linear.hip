@@ -273,13 +273,16 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     // instructions cover are loaded twice, to the same place.
     constexpr int QC = BN / 32 / NW > 0 ? BN / 32 / NW : 1, SB = BN * 32;      // scales behind the codes
     static_assert(!direct || QC + 1 <= QI, "a base tile issues no more loads than a rank-vector tile");
+    // (a row's two units change places in 8 of 16 rows, so that the 16 rows of a read hit
+    // different banks)
+    auto code_unit = [](int lane) { return (lane & 1) ^ ((lane >> 4) & 1); };
     const uint8_t *cptr[QC], *sptr = nullptr;
     if (direct) {
         auto row = [&](int r) { return a.off[sc] + min(c0 + r, cend - 1); };
 #pragma unroll
         for (int i = 0; i < QC; ++i)
             cptr[i] = reinterpret_cast<const uint8_t *>(a.w) + row((i * NW + w) % (BN / 32) * 32 + lane / 2) * a.ldw +
-                      (lane & 1) * 16;
+                      code_unit(lane) * 16;
         sptr = a.ws + row((w * 64 + lane) % BN) * a.ldws;
     }
     int ktile = 0;                                // direct: the next base tile to load
@@ -412,7 +415,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                 const uint32_t ql0 = stage0 + stage * (PB + QB) + PB;
 #pragma unroll
                 for (int i = 0; i < QC; ++i)
-                    code1(ql0, i, (lane & 1) * 32 < rem ? (const void *)(cptr[i] + ktile * 32) : zero);
+                    code1(ql0, i, code_unit(lane) * 32 < rem ? (const void *)(cptr[i] + ktile * 32) : zero);
                 scales1(ql0);
             }
             if (!codes) {
@@ -474,8 +477,9 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
         const int row = (wm * MB + mb) * 16 + l16;
         return frag(*reinterpret_cast<const uint4 *>(st + row * (BK * 2) + ((unit(kk) ^ pswz(row)) << 4)));
     };
+    const int code_at = (((g >> 1) ^ (l16 >> 3)) << 4) + (g & 1) * 8;     // a row's codes of the lane's 16 steps
     auto qcodes = [&](const char *st, int nb) {
-        return *reinterpret_cast<const uint2 *>(st + PB + ((wn * NB + nb) * 16 + l16) * 32 + g * 8);
+        return *reinterpret_cast<const uint2 *>(st + PB + ((wn * NB + nb) * 16 + l16) * 32 + code_at);
     };
     auto qscale1 = [&](const char *st, int nb, int kt) {
         return (uint32_t)*reinterpret_cast<const uint8_t *>(st + PB + SB + ((wn * NB + nb) * 16 + l16) * 4 + (kt & 1) * 2 +
@@ -604,7 +608,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                 for (int i = 0; i < PI; ++i) pp[i] = pptr[i] + po;
 #pragma unroll
                 for (int i = 0; i < QC; ++i) cp[i] = cptr[i] + ktile * 32;
-                const int c_row = PB + (wn * NB * 16 + l16) * 32 + g * 8, s_row = PB + SB + (wn * NB * 16 + l16) * 4 + (g >> 1);
+                const int c_row = PB + (wn * NB * 16 + l16) * 32 + code_at, s_row = PB + SB + (wn * NB * 16 + l16) * 4 + (g >> 1);
                 const int p_row = (wm * MB * 16 + l16) * (BK * 2);
                 int fast = min(nk - NST - v, (int)(rem / BK));
                 auto read_p = [&](int set, int st, int i) __attribute__((always_inline)) {
