@@ -70,9 +70,10 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // whose scales run along the contraction: a thread loads its share of a tile one tile
 // ahead of the DMA into registers and writes it to the stage as bf16, in the DMA's
 // layout, when the stage is free; everything past the stage is the same.
-template <int BM, int BN, int NST>
+template <int BM, int BN, int NST, bool SCALES>
 struct TileLds {
     __attribute__((aligned(16))) char stage[NST * (BM + BN) * 128];
+    __attribute__((aligned(16))) char scales[2][SCALES ? BN * 4 : 16];     // two pairs of tiles' (forward, codes)
     int tok[BM], slot[BM], list[BM + 1], r8[BM + 1], whole[BM / 16], n, nt, any;
     unsigned bits[32];
 };
@@ -94,8 +95,8 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs &a) {
 // registers do not crowd the other's loop: in one body the 128 x 128 tiles spill).
 enum { kQRows, kQCodes, kQVectors };
 
-template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED, int Q>
-__device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> &sh, int mt, int nt) {
+template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED, int Q, bool SCALES>
+__device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST, SCALES> &sh, int mt, int nt) {
     constexpr int NW = WM * WN, BK = 64, KK = 2;
     constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
     constexpr int PB = BM * BK * 2, QB = BN * BK * 2;
@@ -268,10 +269,11 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     const uint32_t lds0 = lds_addr(s_stage) + w * 1024;
 
     constexpr bool codes = Q == kQCodes, staged = codes && NN, direct = codes && !NN;
-    // direct: QC instructions of codes (32 bytes a row) and one of 4 blocks' scales a
-    // row, of which two tiles in turn take two each.  Fewer rows than a work-group's
-    // instructions cover are loaded twice, to the same place.
-    constexpr int QC = BN / 32 / NW > 0 ? BN / 32 / NW : 1, SB = BN * 32;      // scales behind the codes
+    // direct: QC instructions of codes (32 bytes a row); and one of 4 blocks' scales a
+    // row, a place of their own, before the first of the two tiles that take two each (64
+    // lanes there touch as many lines).  Fewer rows than a work-group's instructions
+    // cover are loaded twice, to the same place.
+    constexpr int QC = BN / 32 / NW > 0 ? BN / 32 / NW : 1;
     static_assert(!direct || QC + 1 <= QI, "a base tile issues no more loads than a rank-vector tile");
     // (a row's two units change places in 8 of 16 rows, so that the 16 rows of a read hit
     // different banks)
@@ -289,10 +291,10 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     auto code1 = [&](uint32_t ql0, int i, const void *from) __attribute__((always_inline)) {
         dma16(ql0 + (i * NW + w) % (BN / 32) * 1024, from);
     };
-    auto scales1 = [&](uint32_t ql0) __attribute__((always_inline)) {
-        dma4(ql0 + SB + (w * 64) % BN * 4, sptr + (ktile >> 1) * 4);
+    const uint32_t stage0 = lds_addr(s_stage), scales0 = lds_addr(sh.scales);
+    auto scales1 = [&]() __attribute__((always_inline)) {
+        dma4(scales0 + (ktile >> 1 & 1) * (BN * 4) + (w * 64) % BN * 4, sptr + (ktile >> 1) * 4);
     };
-    const uint32_t stage0 = lds_addr(s_stage);
 
     // staged: a thread's NQ pieces of a tile, HB code bytes each (a block of 32 or half
     // of one), as rows and blocks such that the 8 lanes of one LDS write hit
@@ -408,6 +410,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                 store_qs(qr, stage);
                 load_qs(qr);
             }
+            if (direct && (v == 0 || !(ktile & 1))) scales1();
 #pragma unroll
             for (int i = 0; i < PI; ++i)
                 dma16(pl + i * NW * 1024, plc * 8 < rem ? (const void *)(pptr[i] + po) : zero);
@@ -416,7 +419,6 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
 #pragma unroll
                 for (int i = 0; i < QC; ++i)
                     code1(ql0, i, code_unit(lane) * 32 < rem ? (const void *)(cptr[i] + ktile * 32) : zero);
-                scales1(ql0);
             }
             if (!codes) {
 #pragma unroll
@@ -481,9 +483,8 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     auto qcodes = [&](const char *st, int nb) {
         return *reinterpret_cast<const uint2 *>(st + PB + ((wn * NB + nb) * 16 + l16) * 32 + code_at);
     };
-    auto qscale1 = [&](const char *st, int nb, int kt) {
-        return (uint32_t)*reinterpret_cast<const uint8_t *>(st + PB + SB + ((wn * NB + nb) * 16 + l16) * 4 + (kt & 1) * 2 +
-                                                            (g >> 1));
+    auto qscale1 = [&](int nb, int kt) {
+        return (uint32_t)(uint8_t)sh.scales[kt >> 1 & 1][((wn * NB + nb) * 16 + l16) * 4 + (kt & 1) * 2 + (g >> 1)];
     };
     auto qfrag = [&](const char *st, int nb, int kk) {
         if (NN) {
@@ -509,7 +510,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
     // all but the NST - 1 youngest tiles' loads; a base tile of codes has fewer
     auto wait_tile = [&](bool more) __attribute__((always_inline)) {
         if (!more) wait_barrier<0>();
-        else if (codes) wait_barrier<(NST - 1) * (PI + (NN ? NL : QC + 1))>();
+        else if (codes) wait_barrier<(NST - 1) * (PI + (NN ? NL : QC))>();       // (scales come first)
         else wait_barrier<(NST - 1) * (PI + QI)>();
     };
     if (staged) {
@@ -608,7 +609,8 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                 for (int i = 0; i < PI; ++i) pp[i] = pptr[i] + po;
 #pragma unroll
                 for (int i = 0; i < QC; ++i) cp[i] = cptr[i] + ktile * 32;
-                const int c_row = PB + (wn * NB * 16 + l16) * 32 + code_at, s_row = PB + SB + (wn * NB * 16 + l16) * 4 + (g >> 1);
+                const int c_row = PB + (wn * NB * 16 + l16) * 32 + code_at;
+                const char *const s_row = sh.scales[0] + (wn * NB * 16 + l16) * 4 + (g >> 1);
                 const int p_row = (wm * MB * 16 + l16) * (BK * 2);
                 int fast = min(nk - NST - v, (int)(rem / BK));
                 auto read_p = [&](int set, int st, int i) __attribute__((always_inline)) {
@@ -618,31 +620,38 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                 // item i of a tile's first reads: codes and scales in turn, P fragments
                 auto read_first = [&](int st, int sst, int i) __attribute__((always_inline)) {
                     if (i >= 2 * NB) read_p(0, st, i - 2 * NB);
-                    else if (i % 2) qs[i / 2] = (uint8_t)*(s_stage + (sst + s_row) + i / 2 * 64);
+                    else if (i % 2) qs[i / 2] = (uint8_t)*(s_row + sst + i / 2 * 64);
                     else qc[i / 2] = *reinterpret_cast<const uint2 *>(s_stage + (st + c_row) + i / 2 * 512);
                 };
                 // item i of the DMA that a free stage takes
-                constexpr int LC = PI + QC + 1;
+                constexpr int LC = 1 + PI + QC;
                 auto dma1 = [&](uint32_t at, int i) __attribute__((always_inline)) {
-                    if (i < PI) dma16(at + w * 1024 + i * NW * 1024, pp[i]);
-                    else if (i < PI + QC) code1(at + PB, i - PI, cp[i - PI]);
-                    else scales1(at + PB);
+                    if (i == 0) {
+                        if (!(ktile & 1)) scales1();
+                    } else if (i <= PI) {
+                        dma16(at + w * 1024 + (i - 1) * NW * 1024, pp[i > 0 && i <= PI ? i - 1 : 0]);
+                    } else {
+                        code1(at + PB, i - 1 - PI, cp[i > PI ? i - 1 - PI : 0]);
+                    }
                 };
                 auto next1 = [&](int i) __attribute__((always_inline)) {
-                    if (i < PI) {
-                        pp[i] += BK;
-                        asm volatile("" : "+v"(pp[i]));
-                    } else if (i < PI + QC) {
-                        cp[i - PI] += 32;
-                        asm volatile("" : "+v"(cp[i - PI]));
+                    if (i > 0 && i <= PI) {
+                        const uint16_t *&p = pp[i > 0 && i <= PI ? i - 1 : 0];
+                        p += BK;
+                        asm volatile("" : "+v"(p));
+                    } else if (i > PI) {
+                        const uint8_t *&c = cp[i > PI ? i - 1 - PI : 0];
+                        c += 32;
+                        asm volatile("" : "+v"(c));
                     }
                 };
                 auto at_of = [&](int v) { return (v % NST) * (PB + QB); };
+                auto scales_of = [&](int v) { return ((k0 + v) >> 1 & 1) * (BN * 4) + ((k0 + v) & 1) * 2; };
                 // Slots between the MFMAs of a half: about three instructions each.
                 constexpr bool WIDE = M >= 64;
                 constexpr int MR = WIDE ? M * 3 / 8 : M / 2, MC = WIDE ? MR : M / 2;
 #pragma unroll
-                for (int i = 0; i < RC; ++i) read_first(at_of(v), at_of(v) + ((k0 + v) & 1) * 2, i);
+                for (int i = 0; i < RC; ++i) read_first(at_of(v), scales_of(v), i);
 #pragma unroll
                 for (int i = 0; i < 5 * NB; ++i) scale1(i);
                 do {
@@ -678,7 +687,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                     wait_tile(true);
                     // second half: the next tile's codes, scales and first P fragments, its
                     // first conversions
-                    const int nx = at_of(v), nxs = nx + ((k0 + v) & 1) * 2;
+                    const int nx = at_of(v), nxs = scales_of(v);
                     each<0, M>([&](auto slot) __attribute__((always_inline)) {
                         constexpr int n = decltype(slot)::value;
                         if constexpr (n < MR)
@@ -792,7 +801,7 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
                 if (direct && base) {
                     // (scales past the row's blocks may be anything)
                     const int kt = k0 + v;
-                    const uint32_t s = kt * BK + (g >> 1) * kMxBlock < a.K ? qscale1(st, i, kt) : 0u;
+                    const uint32_t s = kt * BK + (g >> 1) * kMxBlock < a.K ? qscale1(i, kt) : 0u;
                     const uint2 c = qcodes(st, i);
                     q[kk][i] = frag(mx_fp4_bf16(kk ? c.y : c.x, s << 23));
                 } else {
@@ -978,11 +987,11 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST> 
 
 template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED, bool MX>
 __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
-    __shared__ TileLds<BM, BN, NST> sh;
+    __shared__ TileLds<BM, BN, NST, MX && !NN> sh;
     const TileAt at = tile_at(a);
-    if (!MX) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQRows>(a, sh, at.mt, at.nt);
-    else if (MIXED && at.nt >= a.base_tiles) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQVectors>(a, sh, at.mt, at.nt);
-    else lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQCodes>(a, sh, at.mt, at.nt);
+    if (!MX) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQRows, MX && !NN>(a, sh, at.mt, at.nt);
+    else if (MIXED && at.nt >= a.base_tiles) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQVectors, MX && !NN>(a, sh, at.mt, at.nt);
+    else lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQCodes, MX && !NN>(a, sh, at.mt, at.nt);
 }
 
 // Rank vectors of a small batch: u[t][j] = sum_k x[t][k] A[i][j][k] with no
