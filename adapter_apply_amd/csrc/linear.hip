@@ -331,15 +331,15 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST, 
     }
     auto load_q = [&](Pieces &r, int i) __attribute__((always_inline)) {
         const bool in = qrow_of[i] < q_rem;
-        const void *c = in ? (const void *)(qcode[i] + q_at * a.ldw) : (const void *)g_zero16;
-        const uint8_t *s = in ? qscale[i] + q_at * a.ldws : reinterpret_cast<const uint8_t *>(g_zero16);
+        const uint8_t *c = qcode[i] + q_at * a.ldw;
         if (HB == 16) {
-            r.c[i] = *static_cast<const uint4 *>(c);
+            const u32x4_t v = load_or_zero<u32x4_t>(in, c);
+            r.c[i] = make_uint4(v.x, v.y, v.z, v.w);
         } else {
-            const uint2 h = *static_cast<const uint2 *>(c);
-            r.c[i] = make_uint4(h.x, h.y, 0, 0);
+            const uint64_t v = load_or_zero<uint64_t>(in, c);
+            r.c[i] = make_uint4((uint32_t)v, (uint32_t)(v >> 32), 0, 0);
         }
-        r.s[i] = *s;
+        r.s[i] = load_or_zero<uint8_t>(in, qscale[i] + q_at * a.ldws);
     };
     auto begin_q = [&]() {                        // the next tile's slice
         if (q_rem <= 0 && q_cs + 1 < a.S) q_rem = a.n[++q_cs];

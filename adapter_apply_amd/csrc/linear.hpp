@@ -171,6 +171,15 @@ int64_t grad_items(const int64_t *m, int32_t n, int32_t L);   // partial sums of
 // 16 zero bytes that masked LDS-DMA lanes read instead of their row.
 static __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
+// *p, or zeros from g_zero16: the choice is between addresses, since one between
+// values would wait for the load where it stands, and between global ones (a choice of
+// generic pointers makes a flat load, which the LDS counter waits for too).
+template <typename V>
+__device__ __forceinline__ V load_or_zero(bool in, const void *p) {
+    typedef __attribute__((address_space(1))) const V global_v;
+    return *(in ? (global_v *)p : (global_v *)(const void *)g_zero16);
+}
+
 // 64 lanes x 16 bytes straight from global memory into LDS at `lds` (uniform)
 // + lane * 16.  The load is counted in vmcnt; every reader waits for it with
 // wait_barrier.

@@ -348,7 +348,8 @@ __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, Wg
         for (int j = 0; j < NB; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     struct Stage {
-        uint4 x, q[QL];
+        uint4 x;
+        u32x4_t q[QL];
         uint32_t scale;
     };
     for (int cb = b; cb < e; cb += kWgTokens) {
@@ -368,8 +369,7 @@ __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, Wg
                 const int j = r0 + u % CPQ * 8;
                 const bool in = u < QU && tk < cnt && j < a.R;
                 const uint16_t *q = hl + (int64_t)sh.tok[in ? tk : 0] * hlr + part * a.R + j;
-                // (a choice of values would wait for the load here)
-                t.q[i] = *(in ? reinterpret_cast<const uint4 *>(q) : reinterpret_cast<const uint4 *>(g_zero16));
+                t.q[i] = load_or_zero<u32x4_t>(in, q);
             }
         };
         auto store = [&](const Stage &t, int v) __attribute__((always_inline)) {
@@ -385,8 +385,8 @@ __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, Wg
             for (int i = 0; i < QL; ++i) {
                 const int u = i * 256 + tid, part = u / (QB / 16), row = u % (QB / 16) / CPQ;
                 if (u < QU)
-                    *reinterpret_cast<uint4 *>(st + PB + part * QB + row * (CPQ * 16) +
-                                               ((u % CPQ ^ tr_swz<CPQ>(row)) << 4)) = t.q[i];
+                    *reinterpret_cast<u32x4_t *>(st + PB + part * QB + row * (CPQ * 16) +
+                                                 ((u % CPQ ^ tr_swz<CPQ>(row)) << 4)) = t.q[i];
             }
         };
         Stage ring[kWg8Depth];

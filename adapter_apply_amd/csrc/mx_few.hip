@@ -66,7 +66,8 @@ __device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT, CH, MU
     // A chunk: the wave's U steps of codes (neighbouring ones, whole lines of 128 bytes a
     // row) and a share of all its x, in registers.
     struct Chunk {
-        uint4 code[U][CT], x[XU];
+        uint4 code[U][CT];
+        u32x4_t x[XU];
         uint32_t scale[U][CT];
     };
     auto load = [&](Chunk &c, int s0) __attribute__((always_inline)) {
@@ -84,15 +85,14 @@ __device__ __forceinline__ void few_base(const FewArgs &f, FewLds<TB, CT, CH, MU
             const int q = i * kMfWaves * 64 + tid, row = q >> 4 & (TB * 16 - 1), st = q / (TB * 256);
             const int k = (s0 + st) * kMfStep + (q & 15) * 8;
             const uint16_t *x = a.p + (int64_t)min(row, a.T - 1) * a.ldp + k;
-            // (a choice of values would wait for the load here)
-            c.x[i] = *(k < a.K ? reinterpret_cast<const uint4 *>(x) : reinterpret_cast<const uint4 *>(g_zero16));
+            c.x[i] = load_or_zero<u32x4_t>(k < a.K, x);
         }
     };
     auto store_x = [&](const Chunk &c, int buf) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < XU; ++i) {
             const int q = i * kMfWaves * 64 + tid, row = q >> 4 & (TB * 16 - 1), st = q / (TB * 256);
-            sh.x[buf][st][row][(q ^ row) & 15] = c.x[i];
+            *reinterpret_cast<u32x4_t *>(&sh.x[buf][st][row][(q ^ row) & 15]) = c.x[i];
         }
     };
     auto compute = [&](const Chunk &c, int s0, int buf) __attribute__((always_inline)) {
