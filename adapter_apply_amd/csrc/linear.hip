@@ -69,7 +69,10 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // values an instruction).  Gradient, whose transposed reads take 16-bit values and
 // whose scales run along the contraction: a thread loads its share of a tile one tile
 // ahead of the DMA into registers and writes it to the stage as bf16, in the DMA's
-// layout, when the stage is free; everything past the stage is the same.
+// layout, when the stage is free; everything past the stage is the same.  8192 tokens,
+// 4096 x 28672, rank 64: 1.63 to 1.73 ms, by the matrix rate; 256 tokens of 4096 x 6144
+// 24.6 us, of them 10.7 whatever K is (33 MB of sums) and 1.09 per K tile of a CU's two
+// work-groups; gradient of 96 tokens of 6144 x 4096 25.3 us.
 template <int BM, int BN, int NST, bool SCALES>
 struct TileLds {
     __attribute__((aligned(16))) char stage[NST * (BM + BN) * 128];

@@ -5,8 +5,8 @@
 // whole block, 16 bytes, and x meets it in that order, 4 fragments a block), x through
 // LDS.  A split's codes are in flight together where registers allow, so a call is
 // some round trips to memory and its bytes: one token of 4096 x 6144, rank 16, 9.5 us
-// (14 MB; 5 us and 2.8 TB/s fit one token's sizes); 16 tokens of 14336 x 4096, 16 slots, 15.5
-// us and 4.6 of the join (38 MB).
+// (14 MB; 5 us and 2.8 TB/s fit one token's sizes); 16 tokens of 14336 x 4096, 16 slots, 14.7
+// us and 5.5 of the join (38 MB).
 #include "linear.hpp"
 #include "mx.hpp"
 
@@ -493,8 +493,8 @@ bool mx_few(int32_t T, const int64_t *N, int32_t S, int32_t R, int32_t L) {
 
 // One token of rank at most 32 takes k_mx_one while the slot's lora_a rows, which each
 // of its work-groups reads, are a small part of the work.  Against two launches, us:
-// K x N of 4096 x 4096 8.1 and 10.7, x 6144 10.6 and 12.3, x 8192 11.3 and 14.1, x 14336
-// 16.5 and 16.9, x 28672 27.6 and 25.3; 14336 x 4096 15.2 and 22.7.
+// K x N of 4096 x 4096 8.1 and 10.7, x 6144 9.5 and 12.3, x 8192 10.0 and 14.1, x 14336
+// 14.6 and 16.9, x 28672 26.4 and 25.4; 14336 x 4096 13.5 and 22.7.
 static bool mx_one(const LinArgs &a) { return a.T == 1 && a.R <= 32 && a.cols <= 16384; }
 
 static hipError_t launch_one(LinArgs a, int32_t *count, hipStream_t st) {
