@@ -146,8 +146,9 @@ def moe_algorithmic_bytes(c, reduce_k=False):
 # taken on)
 # ---------------------------------------------------------------------------
 
-# The adapter layer, its gradient and the clip: kernels that no workload here runs.
-LAYER_SOURCES = ("abi_linear.hip", "grad.hip", "linear.hip", "linear.hpp", "linear_bwd.hip")
+# The adapter layer, its gradient, the clip and microscaled storage: kernels that no workload here runs.
+LAYER_SOURCES = ("abi_linear.hip", "grad.hip", "linear.hip", "linear.hpp", "linear_bwd.hip",
+                 "mx.hip", "mx.hpp", "mx_few.hip")
 
 
 def kernel_hash():

@@ -279,3 +279,14 @@ def test_binding_backward():
             aa.lora_linear_mx_backward(a["dx"], a["dA"], a["dB"], a["y"], a["x"], a["W"], a["A"], a["B"],
                                        a["idx"], a["rank"], a["scale"], a["ws"], buf=a["buf"],
                                        x_scales=a["x_scales"], W_scales=a["W_scales"])
+
+
+def test_benchmark_counters_are_those_of_its_kernels():
+    """No workload of the benchmark runs the layer's sources, so its counters outlive them."""
+    import importlib
+    import json
+    import pathlib
+    bench = importlib.import_module("bench")
+    root = pathlib.Path(bench.ROOT)
+    for f in root.glob("profiles/pmc_*.json"):
+        assert json.loads(f.read_text())["kernel_hash"] == bench.kernel_hash(), f.name
