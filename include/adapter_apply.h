@@ -492,6 +492,8 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
  *          ldc % 16 == 0.
  *   scales device bytes [M][lds]: KB bytes of a row rounded up to whole 4 used; 4-byte
  *          aligned, lds % 4 == 0.
+ * What a row's used bytes hold past K (codes) and past KB (scales) is zero: the layer
+ * multiplies it by zeros.
  * bf16 holds every value exactly (fp32 too), overflows to infinity excepted.
  * ------------------------------------------------------------------------ */
 #define LORA_MX_FP4  0
