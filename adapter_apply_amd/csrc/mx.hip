@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_quantize(MxArgs a) {
         top = max4(top);
         const bool finite = top < 0x7f800000u;
         const uint32_t field = top >> 23, byte = !finite ? 255u : FP4 ? (field > 2 ? field - 2 : 0) : field;
-        const bool block = live[u] && col[u] < a.blocks * kMxBlock;
+        const bool block = live[u] && col[u] / kMxBlock < a.blocks;
         if (FP4) {
             const float s = __uint_as_float(byte << 23);
             uint32_t c = 0;
