@@ -464,7 +464,7 @@ static lora_status_t check_mx_call(const void *x, int64_t ldx, const void *codes
     if (dtype != LORA_DT_F32 && dtype != LORA_DT_BF16) return LORA_E_DTYPE;
     if (format != LORA_MX_FP4 && format != LORA_MX_INT8) return LORA_E_DTYPE;
     if (M < 0 || K < 1 || ldx < K) return LORA_E_SHAPE;
-    if (M > 0 && (mx_blocks(K) + 3) / 4 > ((1 << 27) - 1) / M) return LORA_E_SHAPE;   // (a grid of 2^31 threads)
+    if (M > 0 && (mx_blocks(K) + 3) / 4 > kMxItems / M) return LORA_E_SHAPE;
     if (K % 8 || ldx % (dtype == LORA_DT_BF16 ? 8 : 4)) return LORA_E_ALIGN;
     CHECK(check_mx(codes, ldc, scales, lds, K, format));
     if (M == 0) return LORA_OK;

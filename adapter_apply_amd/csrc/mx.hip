@@ -194,10 +194,22 @@ hipError_t run(const MxArgs &a, bool q, hipStream_t st) {
 hipError_t launch_mx(MxArgs a, bool quantize, int32_t format, int32_t dtype, hipStream_t st) {
     a.blocks = (int32_t)mx_blocks(a.K);
     a.groups = (uint32_t)((a.blocks + 3) / 4);
-    a.items = (uint32_t)(a.M * a.groups);
     const bool f32 = dtype == LORA_DT_F32;
-    if (format == LORA_MX_FP4) return f32 ? run<true, true>(a, quantize, st) : run<true, false>(a, quantize, st);
-    return f32 ? run<false, true>(a, quantize, st) : run<false, false>(a, quantize, st);
+    // (rows of one launch: its threads, at most 16 an item, stay under 2^32; only a projection
+    // that is restored has more)
+    const int64_t rows = a.M, most = kMxItems / a.groups;
+    for (int64_t r = 0; r < rows; r += most) {
+        a.M = rows - r < most ? rows - r : most;
+        a.items = (uint32_t)(a.M * a.groups);
+        hipError_t e;
+        if (format == LORA_MX_FP4) e = f32 ? run<true, true>(a, quantize, st) : run<true, false>(a, quantize, st);
+        else e = f32 ? run<false, true>(a, quantize, st) : run<false, false>(a, quantize, st);
+        if (e != hipSuccess) return e;
+        a.x = static_cast<const char *>(a.x) + a.M * a.ldx * (f32 ? 4 : 2);
+        a.codes += a.M * a.ldc;
+        a.scales += a.M * a.lds;
+    }
+    return hipSuccess;
 }
 
 }  // namespace aa

@@ -10,6 +10,7 @@
 namespace aa {
 
 constexpr int kMxBlock = 32;
+constexpr int64_t kMxItems = (1 << 27) - 1;   // most groups of 4 blocks in a launch
 inline int64_t mx_blocks(int64_t K) { return (K + kMxBlock - 1) / kMxBlock; }
 
 struct MxArgs {

@@ -1,4 +1,4 @@
-"""Microscaled storage at the ends of what it takes."""
+"""Microscaled storage and the layer on it at the ends of what they take."""
 import pytest
 import torch
 
@@ -34,3 +34,35 @@ def test_store_of_the_longest_row(fmt):
     end = parts[1][0]
     assert not bool(codes[:, 8 * per:end // 32 * per].any()) and not bool(scales[:, 8:end // 32].any())
     assert not bool(x[:, 256:end].any())
+
+
+def test_gradient_through_a_projection_of_2_36_values():
+    """One that is restored (128 GB of bf16): the tokens' dx are the sums of the rows that
+    are not zero."""
+    T, K, n, R = 8, 1 << 16, 1 << 20, 8
+    if torch.cuda.mem_get_info()[1] < 200 << 30:                    # (the whole card's)
+        pytest.skip("needs 180 GB")
+    torch.cuda.empty_cache()
+    g = torch.Generator().manual_seed(4)
+    rows = torch.tensor([0, 1, 63, 64, 1 << 17, (1 << 18) - 1, 1 << 18, (1 << 19) + 5, n - 65, n - 1])
+    code, scale = mx_util.quantize(torch.randn((len(rows), K), generator=g), aa.LORA_MX_FP4)
+    w = mx_util.restore(code, scale, K, aa.LORA_MX_FP4)
+    W = torch.zeros((n, K // 2), dtype=torch.uint8, device="cuda")
+    Ws = torch.full((n, K // 32), 127, dtype=torch.uint8, device="cuda")
+    W[rows.cuda()], Ws[rows.cuda()] = code.cuda(), scale.cuda()
+    dy = torch.randn((T, n), generator=g).to(bf16)
+    A, B = torch.zeros((1, R, K), dtype=bf16, device="cuda"), torch.zeros((1, n, R), dtype=bf16, device="cuda")
+    x = torch.zeros((T, K), dtype=bf16, device="cuda")
+    dA, dB = torch.full((1, R, K), FILL, device="cuda"), torch.full((1, n, R), FILL, device="cuda")
+    dx = torch.full((T, K), FILL, dtype=bf16, device="cuda")
+    ws = aa.alloc_linear_mx_workspace(T, K, [n], R, 1)
+    aa.lora_linear_mx_backward(dx, [dA], [dB], dy.cuda(), x, W, [A], [B],
+                               torch.full((T,), -1, dtype=torch.int32, device="cuda"), None,
+                               torch.ones(1, device="cuda"), ws, W_scales=Ws)
+    d = dy[:, rows].double()
+    # 10 products (the others are zeros), each sum within 2^-23; one bf16 rounding
+    tol = (d @ w).abs() * 2.0 ** -8 + 1.01 * 10 * 2.0 ** -23 * (d.abs() @ w.abs())
+    assert bool(((dx.cpu().double() - d @ w).abs() <= tol).all())
+    assert not bool(dA.any()) and not bool(dB.any())
+    del ws, W
+    torch.cuda.empty_cache()
