@@ -166,10 +166,9 @@ lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t 
                       int32_t L, int32_t R, const int32_t *idx, const int32_t *slot_rank, const float *scale,
                       float *buf, int32_t dtype, uint32_t flags, void *ws, size_t ws_bytes, void *stream) {
     CHECK(check_layer(T, K, ldx, N, S, L, R, ldy, dtype));
-    if (mx && !W.scales) return LORA_E_NULL;
-    CHECK(check_mat(W, K, LORA_MX_FP4));
+    CHECK(mx ? check_mx(W.p, W.ld, W.scales, W.lds, K, LORA_MX_FP4) : check_k(K, W.ld));
     if (T == 0) return LORA_OK;
-    if (!y || !x || !W.p || !idx || !scale) return LORA_E_NULL;
+    if (!y || !x || !W.p || (mx && !W.scales) || !idx || !scale) return LORA_E_NULL;
     CHECK(check_ptrs(A, S));
     CHECK(check_ptrs(B, S));
     if (!al(y, 16) || !al(x, 16) || !al(W.p, 16) || !al(buf, 16) || !al(bias, 2)) return LORA_E_ALIGN;
