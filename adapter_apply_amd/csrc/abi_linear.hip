@@ -244,7 +244,8 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
     if (X.p && X.scales) CHECK(check_mat(X, K, LORA_MX_INT8));
     if (dx) CHECK(check_k(K, lddx));
     if (dx && Wm.p) CHECK(check_mat(Wm, K, LORA_MX_FP4));
-    if (!dx && !dA && !dB) return LORA_E_NULL;
+    // (of no tokens, dx is an empty matrix, whose address may be null)
+    if (T > 0 && !dx && !dA && !dB) return LORA_E_NULL;
     for (int s = 0; s < S; ++s) {
         if ((dA && !dA[s]) || (dB && !dB[s])) return LORA_E_NULL;
         if ((dA && !al(dA[s], 16)) || (dB && !al(dB[s], 16))) return LORA_E_ALIGN;

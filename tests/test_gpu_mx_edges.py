@@ -4,7 +4,7 @@ import torch
 
 import adapter_apply_amd as aa
 from tests import mx_util
-from tests.test_gpu_mx import FILL, FMTS, bf16
+from tests.test_gpu_mx import FILL, FMTS, bf16, layer, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,12 @@ def test_gradient_through_a_projection_of_2_36_values():
     assert not bool(dA.any()) and not bool(dB.any())
     del ws, W
     torch.cuda.empty_cache()
+
+
+def test_dx_alone_of_no_tokens():
+    """With a bf16 and with a 4-bit projection."""
+    c = layer((3, 72, (36,), 24, 3, 0), 1)
+    e = lambda *s: torch.empty(s, dtype=bf16, device="cuda")
+    args = (e(0, 72), None, None, e(0, 36), None)
+    aa.lora_linear_backward(*args, c.W, c.A, c.B, c.idx[:0], c.rank, c.scale, workspace(c))
+    aa.lora_linear_mx_backward(*args, c.Wq, c.A, c.B, c.idx[:0], c.rank, c.scale, workspace(c), W_scales=c.Ws)
