@@ -37,12 +37,6 @@ struct LinWs {
 
 constexpr size_t kMxCountBytes = 4096;
 
-// Whether a gradient through a 4-bit projection that is not wide takes the 256 x 256
-// tiles, which read it restored.
-bool lin_restores(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
-    return T > 0 && lin_tile_plan(T, K, N, S, R, L, true, false, false, true).tile == 256;
-}
-
 LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool mx = false) {
     LinWs w{};
     w.seg = seg_layout(T, L);
@@ -96,7 +90,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         w.pad_cols += round8(N[s]);
     }
     if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
-    if (mx && lin_restores(T, K, N, S, R, L)) {
+    if (mx && (lin_restores(T, K, N, S, R, L, true) || lin_restores(T, K, N, S, R, L, false))) {
         size_t n = 0;
         for (int s = 0; s < S; ++s) n += (size_t)N[s];
         w.w16 = o; o = align256(o + sizeof(uint16_t) * n * K);
@@ -290,12 +284,7 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
     float *part = reinterpret_cast<float *>(wp + wl.part);
     int32_t *order = reinterpret_cast<int32_t *>(wp + wl.order);
     const bool wide = dx && W && lin_wide_gradient(T, K, N, S, R, L, dA || dB);
-    // The largest gradient tiles read a restored projection: their transposed reads of
-    // codes cost more than restoring them once (us for dx: 2048 tokens, 4096 x 14336 256
-    // and 283, 4096 tokens, 6144 x 4096 216 and 246, 8192 tokens, 28672 x 4096 1700 and
-    // 2013; with 128 x 128 tiles the other way: 512 tokens, 6144 x 4096 70 and 58, 1024
-    // tokens, 28672 x 4096 351 and 301).
-    if (W && Wm.scales && !wide && lin_restores(T, K, N, S, R, L)) {
+    if (W && Wm.scales && lin_restores(T, K, N, S, R, L, dA || dB)) {
         CHECK(launched(restore(Wm, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
         W = Wm.p;
         ldw = Wm.ld;

@@ -309,15 +309,13 @@ __device__ __forceinline__ void lin_tile(const LinArgs &a, TileLds<BM, BN, NST, 
     int q_cs = sc;
     int64_t q_rem = 0, q_at = 0;                  // rows left in the slice, first row
     static_assert(!staged || NL <= QI, "a base tile issues no more loads than a rank-vector tile");
+    static_assert(!staged || BN <= 128, "the places of the pieces in a tile");
     if (staged) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             const int b = i * NT + tid;
             int row, blk, half = 0;
-            if (BN == 256) {
-                blk = (b & 3) | ((b >> 3) & 1) << 2;
-                row = ((b >> 2) & 1) | b >> 4 << 1;
-            } else if (HB == 16) {
+            if (HB == 16) {
                 blk = b % (BN / 32);
                 row = b / (BN / 32);
             } else {
@@ -992,9 +990,12 @@ template <int BM, int BN, int WM, int WN, int NST, bool NN, bool MIXED, bool MX>
 __global__ __launch_bounds__(WM * WN * 64, BM < 256 ? 2 : 1) void k_lin_tile(LinArgs a) {
     __shared__ TileLds<BM, BN, NST, MX && !NN> sh;
     const TileAt at = tile_at(a);
-    if (!MX) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQRows, MX && !NN>(a, sh, at.mt, at.nt);
-    else if (MIXED && at.nt >= a.base_tiles) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQVectors, MX && !NN>(a, sh, at.mt, at.nt);
-    else lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQCodes, MX && !NN>(a, sh, at.mt, at.nt);
+    if constexpr (!MX) {
+        lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQRows, false>(a, sh, at.mt, at.nt);
+    } else {
+        if (MIXED && at.nt >= a.base_tiles) lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQVectors, !NN>(a, sh, at.mt, at.nt);
+        else lin_tile<BM, BN, WM, WN, NST, NN, MIXED, kQCodes, !NN>(a, sh, at.mt, at.nt);
+    }
 }
 
 // Rank vectors of a small batch: u[t][j] = sum_k x[t][k] A[i][j][k] with no
@@ -1898,7 +1899,8 @@ hipError_t launch_lin_gemm(LinArgs a, bool gradient, hipStream_t st) {
         return run_few<4, 2, 2>(a, st);
     }
     const LinTilePlan p = lin_tile_plan(a.T, a.K, a.n, a.S, a.R, a.L, gradient, a.join_delta, a.wide, a.w != nullptr);
-    // (a gradient's 4-bit projection is restored for these)
+    // (a gradient's 4-bit projection is restored for these: its codes are no bf16 rows)
+    if (p.tile == 256 && gradient && a.ws) return hipErrorInvalidValue;
     if (p.tile == 256) return gradient ? run_tile_of<256, 256, 2, 2, 2, false, false>(a, true, 1, st)
                                        : run_tile<256, 256, 2, 2, 2, false>(a, false, 1, st);
     if (p.tile == 128) return run_tile<128, 128, 2, 2, 2, true>(a, gradient, p.splits, st);
@@ -1996,6 +1998,17 @@ bool lin_wide_gradient(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_
     if (T > (weights ? 512 : kLinDirectTokens) || wide_cols(K, S, R, L) == 0) return false;
     if (weights && columns(N, S) > 4 * (int64_t)K) return false;
     return (int64_t)T * K * (2 * S * R + 16) <= (weights ? kLinWideBytesB : kLinWideBytesA);
+}
+
+// The largest gradient tiles (of a call that is not wide: their plan is the one that
+// launch_lin_gemm makes) read a restored projection: their transposed reads of codes
+// cost more than restoring it once (us for dx: 2048 tokens, 4096 x 14336 256 and 283,
+// 4096 tokens, 6144 x 4096 216 and 246, 8192 tokens, 28672 x 4096 1700 and 2013; with
+// 128 x 128 tiles the other way: 512 tokens, 6144 x 4096 70 and 58, 1024 tokens, 28672
+// x 4096 351 and 301).
+bool lin_restores(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights) {
+    return T > 0 && !lin_wide_gradient(T, K, N, S, R, L, weights) &&
+           lin_tile_plan(T, K, N, S, R, L, true, false, false, true).tile == 256;
 }
 
 // Direct batches whose rank vectors the slot-grouped kernels find (whole

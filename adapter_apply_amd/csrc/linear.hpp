@@ -71,6 +71,8 @@ struct LinTilePlan {
 };
 LinTilePlan lin_tile_plan(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool gradient,
                           bool join, bool wide, bool base);
+// Whether a gradient's dx through a 4-bit projection reads it restored to bf16.
+bool lin_restores(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights);
 // bf16 parts of a rank vector: two where the product is rounded to bf16 (y,
 // dx), three where it is an fp32 gradient (split_bf16).
 constexpr int kLinPartsFwd = 2;

@@ -13,8 +13,6 @@ namespace aa {
 
 namespace {
 
-typedef float floatx4_t __attribute__((ext_vector_type(4)));
-
 // 16 lanes take 4 blocks (one word of scales), a lane 8 values: 16-byte loads of
 // bf16, whole lines of codes per wave.  Each thread has U such items' loads in
 // flight.  Bound by bytes: bf16 28672 x 4096 to 4 bits 52 us (5.7 TB/s), back 43.5 (6.8
