@@ -103,6 +103,7 @@ SIGNATURES = {
     "lora_mx_quantize": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
     "lora_mx_dequantize": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
     "lora_linear_mx_workspace_size": (_i32, [_i32, _i32, _vp, _i32, _i32, _i32, C.POINTER(_sz)]),
+    "lora_linear_mx_forward_workspace_size": (_i32, [_i32, _i32, _vp, _i32, _i32, _i32, C.POINTER(_sz)]),
     "lora_linear_mx": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                               _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _u32, _vp, _sz, _vp]),
     "lora_linear_mx_backward": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
@@ -823,16 +824,26 @@ def lora_mx_dequantize(x, codes, scales, fmt: int, stream=None):
     _mx_call("lora_mx_dequantize", x, codes, scales, fmt, stream, False)
 
 
-def lora_linear_mx_workspace_size(T: int, K: int, N: Sequence[int], R: int, L: int) -> int:
+def _mx_workspace_size(name, T, K, N, R, L):
     n = _sz(0)
-    _check(lib().lora_linear_mx_workspace_size(T, K, (_i64 * len(N))(*N), len(N), R, L, C.byref(n)),
-           "lora_linear_mx_workspace_size")
+    _check(getattr(lib(), name)(T, K, (_i64 * len(N))(*N), len(N), R, L, C.byref(n)), name)
     return int(n.value)
 
 
-def alloc_linear_mx_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, device="cuda"):
-    """alloc_linear_workspace for lora_linear_mx and lora_linear_mx_backward."""
-    return _aligned_ws(lora_linear_mx_workspace_size(T, K, N, R, L), device)
+def lora_linear_mx_workspace_size(T: int, K: int, N: Sequence[int], R: int, L: int) -> int:
+    return _mx_workspace_size("lora_linear_mx_workspace_size", T, K, N, R, L)
+
+
+def lora_linear_mx_forward_workspace_size(T: int, K: int, N: Sequence[int], R: int, L: int) -> int:
+    return _mx_workspace_size("lora_linear_mx_forward_workspace_size", T, K, N, R, L)
+
+
+def alloc_linear_mx_workspace(T: int, K: int, N: Sequence[int], R: int, L: int, device="cuda",
+                              forward_only: bool = False):
+    """alloc_linear_workspace for lora_linear_mx and lora_linear_mx_backward.  forward_only:
+    without room for a bf16 copy of W, which only long batches' dx through 4 bits takes."""
+    size = lora_linear_mx_forward_workspace_size if forward_only else lora_linear_mx_workspace_size
+    return _aligned_ws(size(T, K, N, R, L), device)
 
 
 def lora_linear_mx(y, x, W, W_scales, A: Sequence, B: Sequence, idx, slot_rank, scale, ws, bias=None,

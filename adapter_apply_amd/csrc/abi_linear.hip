@@ -28,7 +28,8 @@ struct LinWs {
     size_t v;           // fp32 [S][T][R]: v by token (wide gradients)
     size_t part;        // fp32 partial sums
     size_t pad;         // bf16 [T][pad_cols]: dy with slices of whole 8-element units
-    size_t w16;         // bf16 [sum N][K]: the projection restored from 4 bits
+    size_t w16;         // bf16 [sum N][K]: the projection restored from 4 bits (last, so that
+                        // a call without it lays out the rest alike)
     size_t data;        // end of the call's own regions
     size_t end;
     bool padded;        // some N_s % 8: dy goes through pad
@@ -37,7 +38,9 @@ struct LinWs {
 
 constexpr size_t kMxCountBytes = 4096;
 
-LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool mx = false) {
+// mx: of a call on a 4-bit projection; restored: that reads it restored to bf16.
+LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool mx = false,
+             bool restored = false) {
     LinWs w{};
     w.seg = seg_layout(T, L);
     size_t o = w.seg.end;
@@ -90,7 +93,7 @@ LinWs lin_ws(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
         w.pad_cols += round8(N[s]);
     }
     if (w.padded) o = align256(o + sizeof(uint16_t) * (size_t)T * w.pad_cols);
-    if (mx && (lin_restores(T, K, N, S, R, L, true) || lin_restores(T, K, N, S, R, L, false))) {
+    if (restored) {
         size_t n = 0;
         for (int s = 0; s < S; ++s) n += (size_t)N[s];
         w.w16 = o; o = align256(o + sizeof(uint16_t) * n * K);
@@ -244,7 +247,9 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
         if ((dA && !dA[s]) || (dB && !dB[s])) return LORA_E_NULL;
         if ((dA && !al(dA[s], 16)) || (dB && !al(dB[s], 16))) return LORA_E_ALIGN;
     }
-    const LinWs wl = lin_ws(T, K, N, S, R, L, mx);
+    const bool wide = dx && Wm.p && lin_wide_gradient(T, K, N, S, R, L, dA || dB);
+    const bool restored = dx && Wm.p && Wm.scales && lin_restores(T, K, N, S, R, L, dA || dB);
+    const LinWs wl = lin_ws(T, K, N, S, R, L, mx, restored);
     if (!wl.padded && lddy % 8) return LORA_E_ALIGN;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (T == 0) {
@@ -283,8 +288,7 @@ lora_status_t backward(void *dx, int64_t lddx, float *const *dA, float *const *d
     uint16_t *hl_v = reinterpret_cast<uint16_t *>(wp + wl.hl_v);
     float *part = reinterpret_cast<float *>(wp + wl.part);
     int32_t *order = reinterpret_cast<int32_t *>(wp + wl.order);
-    const bool wide = dx && W && lin_wide_gradient(T, K, N, S, R, L, dA || dB);
-    if (W && Wm.scales && lin_restores(T, K, N, S, R, L, dA || dB)) {
+    if (restored) {
         CHECK(launched(restore(Wm, sl.off[S], K, LORA_MX_FP4, wp + wl.w16, st)));
         W = Wm.p;
         ldw = Wm.ld;
@@ -419,6 +423,15 @@ lora_status_t lora_linear_backward(void *dx, int64_t lddx, float *const *dA, flo
 
 lora_status_t lora_linear_mx_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
                                             int32_t L, size_t *bytes) {
+    CHECK(lora_linear_workspace_size(T, K, N, S, R, L, bytes));
+    // (whether a gradient with or without weights restores the projection)
+    const bool restored = lin_restores(T, K, N, S, R, L, true) || lin_restores(T, K, N, S, R, L, false);
+    *bytes = lin_ws(T, K, N, S, R, L, true, restored).end;
+    return LORA_OK;
+}
+
+lora_status_t lora_linear_mx_forward_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
+                                                    int32_t L, size_t *bytes) {
     CHECK(lora_linear_workspace_size(T, K, N, S, R, L, bytes));
     *bytes = lin_ws(T, K, N, S, R, L, true).end;
     return LORA_OK;

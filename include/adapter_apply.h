@@ -519,9 +519,15 @@ lora_status_t lora_mx_dequantize(void *x, int64_t ldx, const void *codes, int64_
                                  int32_t format, int32_t dtype, void *stream);
 
 /* Workspace bytes of lora_linear_mx and lora_linear_mx_backward for these sizes; rules
- * of `ws` as for lora_linear, whose calls may share it. */
+ * of `ws` as for lora_linear, whose calls may share it.  Long batches' dx through a 4-bit
+ * W restores it to bf16 there, 2 bytes for each of its sum N * K values. */
 lora_status_t lora_linear_mx_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R,
                                             int32_t L, size_t *bytes);
+
+/* The same without the restored projection: for lora_linear_mx, and for
+ * lora_linear_mx_backward without dx, or without W_scales. */
+lora_status_t lora_linear_mx_forward_workspace_size(int32_t T, int32_t K, const int64_t *N, int32_t S,
+                                                    int32_t R, int32_t L, size_t *bytes);
 
 /*
  * lora_linear with the projection in 4 bits: W are LORA_MX_FP4 codes [sum N][ldw

@@ -4,7 +4,9 @@ import torch
 
 import adapter_apply_amd as aa
 from tests import mx_util
-from tests.test_gpu_mx import FILL, FMTS, bf16, layer, workspace
+from tests.layer_util import within
+from tests.test_gpu_mx import (FILL, FMTS, bf16, call_backward, check_backward, gradients, layer, run_forward,
+                               workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +77,29 @@ def test_dx_alone_of_no_tokens():
     args = (e(0, 72), None, None, e(0, 36), None)
     aa.lora_linear_backward(*args, c.W, c.A, c.B, c.idx[:0], c.rank, c.scale, workspace(c))
     aa.lora_linear_mx_backward(*args, c.Wq, c.A, c.B, c.idx[:0], c.rank, c.scale, workspace(c), W_scales=c.Ws)
+
+
+@pytest.mark.parametrize("shape", [(2100, 5640, (100, 36), 72, 12, 4), (1, 4104, (8200,), 16, 2, 0),
+                                   (20, 4104, (8200,), 8, 3, 0), (777, 1352, (1100, 36, 516), 24, 5, 0),
+                                   (2100, 1032, (5000, 260), 16, 4, 0)], ids=str)
+def test_workspaces_of_exactly_the_size(shape):
+    """Calls on a workspace of the size that they need, the bytes around it left alone:
+    forward and the weights' gradients without room for a bf16 projection, then all."""
+    c = layer(shape, 47, x8=True)
+    y_ref, y_tol, b_ref, b_tol = c.forward()
+    args = (c.T, c.K, c.N, c.R, c.L)
+    for size, with_dx in ((aa.lora_linear_mx_forward_workspace_size(*args), False),
+                          (aa.lora_linear_mx_workspace_size(*args), True)):
+        around = torch.full((size + 8192 + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        at = 4096 + (-around.data_ptr()) % 256
+        ws = around[at:at + size]
+        aa.lora_workspace_init(ws)
+        for _ in range(2):
+            _, y, buf = run_forward(c, ws=ws)
+            within(y, y_ref, y_tol, "y")
+            within(buf, b_ref, b_tol, "buf")
+            dx = torch.empty((c.T, c.K), dtype=bf16, device="cuda") if with_dx else None
+            dA, dB = gradients(c)
+            call_backward(c, dx, dA, dB, buf=buf, W=with_dx, ws=ws)
+            check_backward(c, buf, dx, dA, dB)
+        assert bool((around[:at] == 0xA5).all()) and bool((around[at + size:] == 0xA5).all())
