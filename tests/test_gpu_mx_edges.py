@@ -103,3 +103,75 @@ def test_workspaces_of_exactly_the_size(shape):
             call_backward(c, dx, dA, dB, buf=buf, W=with_dx, ws=ws)
             check_backward(c, buf, dx, dA, dB)
         assert bool((around[:at] == 0xA5).all()) and bool((around[at + size:] == 0xA5).all())
+
+
+# The forms of a few tokens and one, the tiles with and without a join, restored projections.
+EDGE_SHAPES = [
+    (1, 4104, (8200,), 16, 2, 0), (1, 72, (36, 20), 32, 3, 4), (1, 136, (16388,), 8, 2, 0),
+    (7, 4104, (8200,), 16, 3, 4), (16, 1416, (260,), 16, 16, 0), (20, 4104, (8200,), 8, 3, 0),
+    (32, 1032, (2600,), 8, 9, 4), (33, 8256, (1100, 36), 48, 5, 0), (256, 520, (260, 132), 16, 4, 4),
+    (777, 1352, (1100, 36, 516), 24, 5, 0), (1200, 2048, (260,), 16, 3, 4), (2100, 1032, (5000, 260), 16, 4, 0),
+    (2100, 5640, (100, 36), 72, 12, 4),
+]
+
+
+@pytest.mark.parametrize("shape", EDGE_SHAPES, ids=str)
+def test_scale_255_stays_in_its_block(shape):
+    """NaN blocks in the middle of a row and at the end of the last one, of W and of x:
+    only their own outputs are NaN."""
+    c = layer(shape, 41, x8=True, ragged=False)
+    T, K, n, last = c.T, c.K, sum(c.N), mx_util.blocks(c.K) - 1
+    c.idx[0] = c.idx[T // 2] = 0
+    c.rank[:] = c.R
+    buf = c.forward()[2].float()
+    w_bad = [(n // 2, last // 2), (n - 1, last)]
+    x_bad = [(0, last // 3), (T // 2, last)]
+    for i, b in w_bad:
+        c.Ws[i, b] = 255
+    for t, b in x_bad:
+        c.xs[t, b] = 255
+    _, y, _ = run_forward(c, want_buf=False)
+    want = torch.zeros((T, n), dtype=torch.bool, device="cuda")
+    want[:, [i for i, _ in w_bad]] = True
+    assert torch.equal(y.isnan(), want) and bool(torch.isfinite(y[~want]).all())
+    dx = torch.full((T, K), FILL, dtype=bf16, device="cuda")
+    dA, dB = gradients(c)
+    call_backward(c, dx, dA, dB, buf=buf)
+    want = torch.zeros((T, K), dtype=torch.bool, device="cuda")
+    for _, b in w_bad:
+        want[:, 32 * b:32 * b + 32] = True
+    assert torch.equal(dx.isnan(), want) and bool(torch.isfinite(dx[~want]).all())
+    want = torch.zeros((c.L, c.R, K), dtype=torch.bool, device="cuda")
+    for _, b in x_bad:
+        want[0, :, 32 * b:32 * b + 32] = True
+    for t in dA:
+        assert torch.equal(t.isnan(), want) and bool(torch.isfinite(t[~want]).all())
+    assert all(bool(torch.isfinite(t).all()) for t in dB)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("shape", EDGE_SHAPES, ids=str)
+def test_bad_adapter_stays_with_its_tokens(shape, bad):
+    """A slot of infinities or NaN: tokens and gradients of all others keep their bits."""
+    c = layer(shape, 43, x8=True, ragged=False)
+    c.rank[:] = c.R
+    c.idx[c.T // 2:] = torch.arange(c.T - c.T // 2, dtype=torch.int32, device="cuda") % (c.L + 1) - 1
+    c.idx[0] = 0 if c.T > 1 else 1
+    buf = c.forward()[2].float()
+    ws = workspace(c)
+
+    def step():
+        _, y, u = run_forward(c, ws=ws)
+        dx = torch.full((c.T, c.K), FILL, dtype=bf16, device="cuda")
+        dA, dB = gradients(c)
+        call_backward(c, dx, dA, dB, buf=buf, ws=ws)
+        return y, u, dx, dA, dB
+
+    y0, u0, dx0, dA0, dB0 = step()
+    for t in (*c.A, *c.B):
+        t[0] = bad
+    y, u, dx, dA, dB = step()
+    mine = c.idx != 0
+    assert torch.equal(y[mine], y0[mine]) and torch.equal(u[:, mine], u0[:, mine]) and torch.equal(dx[mine], dx0[mine])
+    for got, want in zip(dA + dB, dA0 + dB0):
+        assert torch.equal(got[1:], want[1:])
