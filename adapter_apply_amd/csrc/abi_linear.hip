@@ -177,7 +177,8 @@ lora_status_t forward(void *y, int64_t ldy, const void *x, int64_t ldx, int32_t 
     const Slices sl = make_slices(A, B, N, S, 0);
     uint16_t *hl = reinterpret_cast<uint16_t *>(wp + wl.hl_u);
     int32_t *order = nullptr;
-    // (a few tokens on 4 bits take their own kernels or the wide tiles, never lin_few)
+    // (a few tokens on 4 bits take their own kernels or the tiles, with wide columns or the
+    // rank vectors found first, never lin_few)
     const bool few = mx && mx_few(T, N, S, R, L);
     const bool direct = few || lin_direct(T, K, N, S, R, L);
     const bool join = direct || lin_join_delta(T, K, N, S, R, L);

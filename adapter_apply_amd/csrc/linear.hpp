@@ -55,6 +55,8 @@ hipError_t launch_lin_join_rows(const LinArgs &a, hipStream_t st);
 constexpr int64_t kMxFewCols = 65536;   // most columns of a token
 constexpr int kMxFewTokens = 32;        // most tokens
 bool mx_few(int32_t T, const int64_t *N, int32_t S, int32_t R, int32_t L);
+bool mx_one(int32_t T, const int64_t *N, int32_t S, int32_t R);     // of those, in one launch
+int32_t mx_few_splits(int32_t K, const int64_t *N, int32_t S);
 constexpr int kMxFewSplits = 16;        // most K splits
 constexpr int kMxCounts = kMxFewCols / 128 + kMaxSlices;   // counts, zero between calls
 hipError_t launch_mx_few(LinArgs a, int32_t *count, hipStream_t st);

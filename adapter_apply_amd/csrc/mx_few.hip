@@ -463,9 +463,9 @@ hipError_t run(FewArgs f, hipStream_t st) {
 
 }  // namespace
 
-// K splits of a few tokens: about 512 work-groups of four K steps or more
-// (a round of a work-group's loads).
-static int32_t mx_few_splits(int32_t K, const int64_t *N, int32_t S) {
+// K splits of a few tokens: about 512 work-groups of about four K steps or more (a round
+// of a work-group's loads; three of five steps in two).
+int32_t mx_few_splits(int32_t K, const int64_t *N, int32_t S) {
     int64_t c = 0;
     for (int s = 0; s < S; ++s) c += (N[s] + 127) / 128;
     const int64_t steps = (K + kMfStep - 1) / kMfStep;
@@ -495,7 +495,11 @@ bool mx_few(int32_t T, const int64_t *N, int32_t S, int32_t R, int32_t L) {
 // of its work-groups reads, are a small part of the work.  Against two launches, us:
 // K x N of 4096 x 4096 8.1 and 10.7, x 6144 9.5 and 12.3, x 8192 10.0 and 14.1, x 14336
 // 14.6 and 16.9, x 28672 26.4 and 25.4; 14336 x 4096 13.5 and 22.7.
-static bool mx_one(const LinArgs &a) { return a.T == 1 && a.R <= 32 && a.cols <= 16384; }
+bool mx_one(int32_t T, const int64_t *N, int32_t S, int32_t R) {
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) n += N[s];
+    return T == 1 && R <= 32 && n <= 16384;
+}
 
 static hipError_t launch_one(LinArgs a, int32_t *count, hipStream_t st) {
     OneArgs f{};
@@ -522,7 +526,7 @@ hipError_t launch_mx_few(LinArgs a, int32_t *count, hipStream_t st) {
     a.cols = 0;
     for (int s = 0; s < a.S; ++s) a.cols += a.n[s];
     a.part_ld = a.cols + (int64_t)a.S * a.R;
-    if (mx_one(a)) return launch_one(a, count, st);
+    if (mx_one(a.T, a.n, a.S, a.R)) return launch_one(a, count, st);
     FewArgs f{};
     a.ksp = mx_few_splits(a.K, a.n, a.S);
     a.wide = 1;
