@@ -70,9 +70,11 @@ __device__ __forceinline__ bf16x8_t frag(const uint4 &u) { return __builtin_bit_
 // whose scales run along the contraction: a thread loads its share of a tile one tile
 // ahead of the DMA into registers and writes it to the stage as bf16, in the DMA's
 // layout, when the stage is free; everything past the stage is the same.  8192 tokens,
-// 4096 x 28672, rank 64: 1.63 to 1.73 ms, by the matrix rate; 256 tokens of 4096 x 6144
-// 24.6 us, of them 10.7 whatever K is (33 MB of sums) and 1.09 per K tile of a CU's two
-// work-groups; gradient of 96 tokens of 6144 x 4096 25.3 us.
+// 4096 x 28672, rank 64: 1.63 to 1.75 ms, by the matrix rate (bf16 rows the same); 256
+// tokens of 4096 x 6144 25.0 us, of them 10.7 whatever K is (33 MB of sums) and 1.09 per K
+// tile of a CU's two work-groups (bf16 rows 23.3); gradient of 96 tokens of 6144 x 4096
+// 25.4 us (bf16 rows 18.4: what the codes save in bytes is less than the conversions and
+// the loads one tile ahead cost, so what 4 bits give there is memory).
 template <int BM, int BN, int NST, bool SCALES>
 struct TileLds {
     __attribute__((aligned(16))) char stage[NST * (BM + BN) * 128];
@@ -1975,8 +1977,9 @@ bool lin_few(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32
 }
 
 // Direct batches whose rank vectors come out of the tiles as further columns: a
-// launch less (256 tokens, rank 16, 4096 x 6144, us: 8 slots 38.5 against 46.7
-// of the slot-grouped kernels, 128 slots 54.0 against 66.6).
+// launch less (256 tokens, rank 16, 4096 x 6144, us, on bf16 and on codes: 8 slots
+// 37.2 and 37.1 against 46.4 and 46.2 of the slot-grouped kernels, 64 slots 41.0 and
+// 41.2 against 45.7 and 46.3, 128 slots 47.4 and 48.6 against 52.4 and 52.7).
 bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     return !lin_few(T, K, N, S, R, L) && wide_cols(columns(N, S), S, R, L) > 0;
 }
@@ -1993,19 +1996,26 @@ bool lin_wide(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int3
 // them, and past 256 MB what is lost grows larger than what is won.  With weights 96
 // tokens 45.4 and 55.3, 256 55.9 and 62.0; rank 64, 96 tokens (150 MB) 67.7 and 72.5,
 // 256 (400 MB) 81.8 and 78.0.  A contraction many times K keeps the further columns'
-// few tiles long: 28672 x 4096, 96 tokens, with weights 119 and 108.
+// few tiles long: 28672 x 4096, 96 tokens, with weights 119 and 108.  Through 4 bits: dx
+// alone, 6144 x 4096, 512 tokens 57.1 and 67.2, 640 74.2 and 73.2, 896 85.1 and 103.9, 1024
+// 107 and 104; 4096 x 4096, 768 tokens 54.8 and 69.4, 1024 73.4 and 69.6; with weights 96
+// tokens of rank 16, 4 slots 47.9 and 49.8, 256 of 8 slots 56.9 and 59.1; rank 64, 96
+// tokens 60.5 and 58.8, 256 78.1 and 66.3.
 bool lin_wide_gradient(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights) {
     if (T > (weights ? 512 : kLinDirectTokens) || wide_cols(K, S, R, L) == 0) return false;
     if (weights && columns(N, S) > 4 * (int64_t)K) return false;
     return (int64_t)T * K * (2 * S * R + 16) <= (weights ? kLinWideBytesB : kLinWideBytesA);
 }
 
-// The largest gradient tiles (of a call that is not wide: their plan is the one that
-// launch_lin_gemm makes) read a restored projection: their transposed reads of codes
-// cost more than restoring it once (us for dx: 2048 tokens, 4096 x 14336 256 and 283,
-// 4096 tokens, 6144 x 4096 216 and 246, 8192 tokens, 28672 x 4096 1700 and 2013; with
-// 128 x 128 tiles the other way: 512 tokens, 6144 x 4096 70 and 58, 1024 tokens, 28672
-// x 4096 351 and 301).
+// The 256 x 256 gradient tiles (of a call that is not wide: their plan is the one that
+// launch_lin_gemm makes) read a restored projection; they have no form on codes.  Against
+// 128 x 128 tiles on codes, us for dx (N x K; number of 256 x 256 tiles): 769 and 1024
+// tokens, 4096 x 14336 (224) 146 and 158, 141 and 160; 1536 and 1792 tokens, 8192 x 8192
+// (192, 224) 220 and 241, 226 and 288; 3200 and 4096 tokens, 6144 x 4096 (208, 256) 207
+// and 249, 212 and 261, 28672 x 4096 765 and 941, 807 and 994; 8192 tokens of those 1642
+// and 2069.  Just past 256 tiles, where some CUs take two of them, it is the other way:
+// 1280 tokens, 4096 x 14336 (280) 234 and 203, 2560 tokens, 8192 x 8192 (320) 397 and
+// 362, 5120 tokens, 6144 x 4096 (320) 364 and 330.
 bool lin_restores(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L, bool weights) {
     return T > 0 && !lin_wide_gradient(T, K, N, S, R, L, weights) &&
            lin_tile_plan(T, K, N, S, R, L, true, false, false, true).tile == 256;
@@ -2022,15 +2032,20 @@ bool lin_grouped(int32_t T, int32_t K, int32_t R, int32_t L) {
 // build, and the delta in k_lin_few or k_lin_join_rows.  k_lin_join_rows reads
 // lora_b rows once per token, and k_lin_shrink lora_a rows once per block of 16
 // tokens, so their bytes bound it, with some 16 of sums per output.  Wide against
-// sorted (us; MB of lora_b and sums), K 4096, 6144 columns: 512 tokens of rank 16
-// (151 MB) 54.9 and 63.5, 777 tokens (229 MB) 82.1 and 81.6; 128 tokens of rank
-// 64 (113 MB) 45.8 and 47.9, 256 tokens (226 MB) 76.3 and 58.7; 28672 columns, 128
-// tokens of rank 16 (176 MB) 78.9 and 97.2, 256 of rank 8 (235 MB) 117 and 90;
-// 14336 x 4096, 777 tokens of rank 16 (153 MB) 121 and 155.
-// With the slot-grouped kernels, 4096 x 6144: 192 tokens of rank 32, 16 slots (94
-// MB) 53.2 and 55.5, 256 tokens (126 MB) 58.1 and 56.7.  With k_lin_shrink, rank
-// 24 (MB of lora_a): 128 tokens of 8 slots (100 MB) 47.6 and 48.4, 192 of 8 (151
-// MB) 57.8 and 56.3, 256 of 8 (201 MB) 64.8 and 57.4.
+// sorted (us; MB of lora_b and sums; 8 slots), bf16 and in brackets 4-bit projections,
+// K 4096, 6144 columns: 512 tokens of rank 16 (151 MB) 54.5 and 60.1 (55.7 and 64.2),
+// 777 tokens (229 MB) 82.5 and 82.3 (82.6 and 82.5), 1024 (302 MB) 92.1 and 84.5 (93.1
+// and 85.2); rank 64, 128 tokens (113 MB) 37.4 and 43.9 (41.1 and 47.6), 192 (170 MB)
+// 54.6 and 55.0 (53.5 and 56.0), 256 (226 MB) 62.9 and 56.6 (61.4 and 57.5); 28672
+// columns, 128 tokens of rank 16 (176 MB) 72.8 and 64.5, the only one the other way
+// (59.1 and 64.7), 256 of rank 8 (235 MB) 113 and 83 (95 and 82); 14336 x 4096, 777 tokens
+// of rank 16 (153 MB) 122 and 150 (123 and 150).
+// With the slot-grouped kernels, 4096 x 6144, rank 48, 64 slots: 96 tokens (66 MB) 42.0
+// and 45.0 (46.1 and 48.7), 128 (88 MB) 45.5 and 43.9 (50.2 and 48.3), 160 (110 MB) 55.9
+// and 51.7 (54.9 and 52.1), 256 (176 MB) 65.8 and 54.7 (65.3 and 54.9): the bound is
+// some 5 % late for them.  With k_lin_shrink, rank 40, 64 slots (MB of lora_a): 32 tokens
+// (75 MB) 34.5 and 41.9 (34.4 and 41.8), 48 (113 MB) 30.7 and 42.5 (30.6 and 42.9), 96
+// (226 MB) 43.8 and 45.1 (47.6 and 49.3).
 bool lin_direct(int32_t T, int32_t K, const int64_t *N, int32_t S, int32_t R, int32_t L) {
     if (lin_few(T, K, N, S, R, L)) return true;
     const bool wide = lin_wide(T, K, N, S, R, L);

@@ -314,9 +314,9 @@ __device__ __forceinline__ void wg_tile(const LinWgArgs &a, int nrb, int bx, WgL
 // way to LDS.  A thread has its share of a stage in registers (16 codes of a token, of
 // one block, and the rank vectors' units), kWg8Depth stages ahead; all its loads are
 // the compiler's, which then waits for a stage's own only.  With dB beside it: 4096
-// tokens, 14336 -> 4096, rank 32 43 us (from bf16 36, whose bytes the DMA moves without
-// an instruction a value); 8192 tokens, 4096 -> 28672, rank 64 188 us (170).  So what 8
-// bits give is memory; the conversions take the time.
+// tokens, 14336 -> 4096, rank 32 42.5 us (from bf16 39.8, whose bytes the DMA moves without
+// an instruction a value); 1501 ragged tokens 21.1 (20.9); 8192 tokens, 4096 -> 28672, rank
+// 64 189 us (188).  So what 8 bits give is memory; the conversions take the time.
 constexpr int kWg8Depth = 3;
 template <int RB>
 __device__ __forceinline__ void wg_tile8(const LinWgArgs &a, int nrb, int bx, WgLds<RB> &sh) {

@@ -5,8 +5,10 @@
 // whole block, 16 bytes, and x meets it in that order, 4 fragments a block), x through
 // LDS.  A split's codes are in flight together where registers allow, so a call is
 // some round trips to memory and its bytes: one token of 4096 x 6144, rank 16, 9.5 us
-// (14 MB; 5 us and 2.8 TB/s fit one token's sizes); 16 tokens of 14336 x 4096, 16 slots, 14.7
-// us and 5.5 of the join (38 MB).
+// (14 MB; 5 us and 2.8 TB/s fit one token's sizes); 16 tokens of 14336 x 4096, 16 slots, 14.8
+// us (38 MB, 31 of them codes and scales, those at 2.1 TB/s: the CUs hold 512 work-groups
+// at once, the columns' alone, and the 256 of the rank vectors take their places as they
+// end) and 5.4 of the join.
 #include "linear.hpp"
 #include "mx.hpp"
 
