@@ -175,3 +175,52 @@ def test_bad_adapter_stays_with_its_tokens(shape, bad):
     assert torch.equal(y[mine], y0[mine]) and torch.equal(u[:, mine], u0[:, mine]) and torch.equal(dx[mine], dx0[mine])
     for got, want in zip(dA + dB, dA0 + dB0):
         assert torch.equal(got[1:], want[1:])
+
+
+@pytest.mark.parametrize("T,K,n", [(1, 1 << 21, 4200), (5, 1 << 21, 4200), (40, 1 << 21, 4200), (100, 40960, 212000)])
+def test_codes_past_4_gb(T, K, n):
+    """Rows and blocks at both ends of a projection of more bytes than 32 bits count, the
+    rest of it zeros: y of one, a few and more tokens; dx of many rows alone, and with dA
+    and dB."""
+    R, g = 8, torch.Generator(device="cuda").manual_seed(6)
+    rows = torch.tensor([0, 1, n // 2, n - 1], device="cuda")
+    cols = torch.cat([torch.arange(32) + 32 * b for b in (0, K // 64, K // 32 - 1)]).cuda()
+    randn = lambda *s: torch.randn(s, generator=g, device="cuda").to(bf16)
+    full = torch.zeros((len(rows), K), device="cuda")
+    full[:, cols] = torch.randn((len(rows), len(cols)), generator=g, device="cuda")
+    part = [aa.alloc_mx(len(rows), K, aa.LORA_MX_FP4), torch.empty_like(full)]
+    aa.lora_mx_quantize(*part[0], full, aa.LORA_MX_FP4)
+    aa.lora_mx_dequantize(part[1], *part[0], aa.LORA_MX_FP4)
+    w = part[1][:, cols].double()
+    W = torch.zeros((n, K // 2), dtype=torch.uint8, device="cuda")
+    Ws = torch.full((n, K // 32), 127, dtype=torch.uint8, device="cuda")
+    W[rows], Ws[rows] = part[0]
+    x, dy = randn(T, K), randn(T, n)
+    A, B = torch.zeros((1, R, K), dtype=bf16, device="cuda"), torch.zeros((1, n, R), dtype=bf16, device="cuda")
+    A[:, :, cols], B[:, rows] = randn(1, R, len(cols)), randn(1, len(rows), R)
+    a, b = A[0][:, cols].double(), B[0][rows].double()
+    idx = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    idx[0] = 0
+    one, ws = torch.ones(1, device="cuda"), aa.alloc_linear_mx_workspace(T, K, [n], R, 1)
+    mine = (idx == 0).double()[:, None]
+
+    def check(got, at, base, mags, u, v, other):
+        # sums of the values that are not zero, at most 104 each and 16 splits of them; the
+        # rank vector as two bf16 parts; one rounding of the result
+        ref = base + mine * (u @ other)
+        tol = ref.abs() * 2.0 ** -8 + 256 * 2.0 ** -23 * (mags + mine * (v @ other.abs())) + 2.0 ** -16 * mine * (v @ other.abs())
+        assert bool(((got[:, at].double() - ref).abs() <= 1.01 * tol).all())
+        assert int((got != 0).sum()) <= T * len(at)          # (every other one is a sum of zeros)
+
+    xs, ds = x[:, cols].double(), dy[:, rows].double()
+    y = torch.full((T, n), FILL, dtype=bf16, device="cuda")
+    aa.lora_linear_mx(y, x, W, Ws, [A], [B], idx, None, one, ws)
+    check(y, rows, xs @ w.T, xs.abs() @ w.abs().T, xs @ a.T, xs.abs() @ a.abs().T, b.T)
+    if n < K:
+        return
+    for weights in (False, True):
+        dx = torch.full((T, K), FILL, dtype=bf16, device="cuda")
+        dA, dB = [torch.empty((1, R, K), device="cuda")], [torch.empty((1, n, R), device="cuda")]
+        aa.lora_linear_mx_backward(dx, dA if weights else None, dB if weights else None, dy, x, W, [A], [B], idx, None,
+                                   one, ws, W_scales=Ws)
+        check(dx, cols, ds @ w, ds.abs() @ w.abs(), ds @ b, ds.abs() @ b.abs(), a)
