@@ -42,9 +42,9 @@ def test_gradient_through_a_projection_of_2_36_values():
     """One that is restored (128 GB of bf16): the tokens' dx are the sums of the rows that
     are not zero."""
     T, K, n, R = 8, 1 << 16, 1 << 20, 8
-    if torch.cuda.mem_get_info()[1] < 200 << 30:                    # (the whole card's)
-        pytest.skip("needs 180 GB")
     torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 180 << 30:
+        pytest.skip("needs 175 GB")
     g = torch.Generator().manual_seed(4)
     rows = torch.tensor([0, 1, 63, 64, 1 << 17, (1 << 18) - 1, 1 << 18, (1 << 19) + 5, n - 65, n - 1])
     code, scale = mx_util.quantize(torch.randn((len(rows), K), generator=g), aa.LORA_MX_FP4)
